@@ -15,6 +15,13 @@
  * gptq_output_error), and the propagation of a quantized layer's output to
  * the next layer of a chain (gptq_propagate).
  *
+ * Beside the few-bit path stand operators on 8-bit floating-point operands,
+ * for the layers that stay in 8 bits: weights and activations stored as e4m3
+ * values with a scale per block of 128 (gptq_fp8_weight,
+ * gptq_fp8_activations, gptq_fp8_rms_norm), the product of two such operands
+ * (gptq_fp8_matmul) and the gated feed-forward projections
+ * (gptq_fp8_gated).
+ *
  * Conventions shared by every entry point
  *   - Tensor arguments are DEVICE pointers allocated and owned by the caller;
  *     the library never allocates, frees or keeps caller memory.  Scratch
@@ -53,7 +60,8 @@ typedef enum {
 
 typedef enum {
     GPTQ_F16 = 0, /* IEEE binary16 */
-    GPTQ_F32 = 1  /* IEEE binary32 */
+    GPTQ_F32 = 1, /* IEEE binary32 */
+    GPTQ_BF16 = 2 /* bfloat16; taken by the gptq_fp8_* calls only */
 } gptq_dtype;
 
 /*
@@ -401,6 +409,121 @@ size_t gptq_obq_workspace(int64_t d_in);
 int gptq_obq_quantize(const void* W, int w_dtype, int64_t d_out, int64_t d_in, const float* U, const uint8_t* dead,
                       int bits, uint8_t* codes, float* scales, int32_t* zeros, int32_t* order, double* loss,
                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * 8-bit operands.  A matrix of `rows` rows and d columns is held as
+ *   values  [rows, ldq] e4m3 (1 sign, 4 exponent, 3 fraction bits, bias 7, no
+ *           infinity, largest value 448), one byte each, row stride ldq
+ *           bytes, 16-byte aligned, ldq a multiple of 16 and at least d
+ *           rounded up to a multiple of 128; the bytes from d up to that
+ *           multiple are zero;
+ *   scales  float32.  Activations (a row per token): [ceil(d/128), lds], one
+ *           scale per 128 channels and token, tokens along the row
+ *           (lds >= rows).  Weights (a row per output channel):
+ *           [ceil(rows/128), lds], one scale per 128 x 128 block
+ *           (lds >= ceil(d/128)).
+ * A value stands for e4m3 * scale of its block.  The three calls that write
+ * the format use, for every block,
+ *     s = max(largest |x|, 2^-96) / 448,   value = e4m3(fl32(x * fl32(1/s)))
+ * to nearest even, with x in float32, and zero the bytes behind d.  A block
+ * that holds an infinity or a NaN gets an infinite or NaN scale and codes of
+ * which every one stands for NaN after the multiplication.  Bytes of a row
+ * behind the multiple of 128, and rows behind the last, are left as they
+ * were.  Outputs must not overlap inputs unless a call says so.  Sizes of 0
+ * are empty problems.  Sums are float32 throughout.
+ */
+
+/*
+ * Weights to 8 bits, one scale per 128 x 128 block.
+ *   W       [d_out, d_in] of w_dtype (GPTQ_F16, GPTQ_F32 or GPTQ_BF16), row
+ *           stride ldw elements.
+ *   q, scales  the outputs: values [d_out, ldq], scales
+ *           [ceil(d_out/128), lds].
+ * Errors: GPTQ_EINVAL (negative size, ldw < d_in, ldq or lds too small,
+ * unknown dtype, null pointer), GPTQ_EUNSUPPORTED (q or ldq not 16-byte
+ * aligned, d_out or d_in above 2^24, 2^31 blocks or more).
+ */
+int gptq_fp8_weight(const void* W, int w_dtype, int64_t d_out, int64_t d_in, int64_t ldw, uint8_t* q,
+                    int64_t ldq, float* scales, int64_t lds, void* stream);
+
+/*
+ * Activations to 8 bits, one scale per token and 128 channels.
+ *   X       channel_major 0: [n_tokens, d], 1: [d, n_tokens] (the layout of
+ *           the calibration inputs), of x_dtype, row stride ldx elements.
+ *   q, scales  the outputs: values [n_tokens, ldq], scales [ceil(d/128), lds].
+ * Errors: as gptq_fp8_weight, and GPTQ_EINVAL for channel_major not 0 or 1;
+ * the limits are n_tokens below 2^31, d at most 2^24 and fewer than 2^31
+ * (token, block) pairs.
+ */
+int gptq_fp8_activations(const void* X, int x_dtype, int64_t n_tokens, int64_t d, int64_t ldx, int channel_major,
+                         uint8_t* q, int64_t ldq, float* scales, int64_t lds, void* stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, written in 8 bits:
+ *     h = x + residual,   y = h / sqrt(mean(h^2) + eps) * gain
+ * per token, in float32; y goes to (q, scales) as activations, h rounded to
+ * the input type goes to sum_out (y is formed from the unrounded h).
+ *   x         [n_tokens, d] of dtype (GPTQ_F16, GPTQ_F32 or GPTQ_BF16), row
+ *             stride ldx.
+ *   residual  the same type and shape, row stride ldr, or NULL (h = x).
+ *   sum_out   the same type and shape, row stride ldo, or NULL; it may be x
+ *             or residual itself (same pointer and stride).  Not without
+ *             residual.
+ *   gain      [d] of dtype.
+ *   eps       in [1e-20, 1e20].
+ * A row whose sum of squares leaves float32 is summed again scaled by 2^-80,
+ * so that every finite row has a finite norm.
+ * Errors: GPTQ_EINVAL (negative size, a row stride below d, ldq or lds too
+ * small, unknown dtype, eps outside its range or NaN, sum_out without
+ * residual, null pointer), GPTQ_EUNSUPPORTED (q or ldq not 16-byte aligned,
+ * d above 2^24, n_tokens above 2^31 - 1).
+ */
+int gptq_fp8_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* sum_out, int64_t ldo,
+                      const void* gain, int dtype, int64_t n_tokens, int64_t d, double eps, uint8_t* q,
+                      int64_t ldq, float* scales, int64_t lds, void* stream);
+
+/*
+ * Product of 8-bit operands, Y = act(X W^T):
+ *     y[t, o] = sum_b xs[b, t] ws[o/128, b] sum_{k in block b} xq[t, k] wq[o, k]
+ * The products of a block are summed in float32 by one MFMA, scaled by
+ * fl32(xs * ws) and added in float32; y is rounded once to y_dtype.
+ *   wq, ws    weights [d_out, ldwq], scales [ceil(d_out/128), ldws].
+ *   xq, xs    activations [n_tokens, ldxq], scales [ceil(d_in/128), ldxs].
+ *   Y         channel_major 0: [n_tokens, d_out]; 1: [d_out, n_tokens] (the
+ *             layout gptq_hessian_* and gptq_propagate read); of y_dtype
+ *             (GPTQ_F16, GPTQ_F32 or GPTQ_BF16), row stride ldy elements.
+ *   activation 0: none; 1: max(0, .), a NaN kept.
+ * d_in = 0 gives zeros.  fl32(xs * ws) has to be finite for finite results
+ * (it is for every scale of float16 data).
+ * Errors: GPTQ_EINVAL (negative size, a stride too small, unknown dtype,
+ * activation or channel_major, null pointer), GPTQ_EUNSUPPORTED (xq, wq or
+ * their strides not 16-byte aligned, a value stride above 2^22 (so d_in too),
+ * d_out or n_tokens above 2^24).
+ */
+int gptq_fp8_matmul(const uint8_t* wq, int64_t ldwq, const float* ws, int64_t ldws, int64_t d_out, int64_t d_in,
+                    const uint8_t* xq, int64_t ldxq, const float* xs, int64_t ldxs, int64_t n_tokens, void* Y,
+                    int y_dtype, int64_t ldy, int channel_major, int activation, void* stream);
+
+/*
+ * Gated feed-forward projections on 8-bit operands, written in 8 bits:
+ *     h = silu(X G^T) * (X U^T),   silu(g) = g / (1 + exp(-g))
+ * with both projections as gptq_fp8_matmul in float32 (neither is rounded or
+ * stored) and h written as activations of d_ff channels: the input of the
+ * down projection.
+ *   gq, gs, uq, us  the gate and up weights [d_ff, ldwq], scales
+ *             [ceil(d_ff/128), ldws] (one shape and strides for both).
+ *   xq, xs    activations [n_tokens, ldxq], scales [ceil(d_in/128), ldxs].
+ *   q, scales the output: values [n_tokens, ldq], scales [ceil(d_ff/128), lds].
+ *   workspace device memory of at least gptq_fp8_gated_workspace(n_tokens,
+ *             d_ff) bytes (0 for many tokens: then it may be NULL), 256-byte
+ *             aligned; clobbered.
+ * Errors: as gptq_fp8_matmul, and GPTQ_EWORKSPACE.
+ */
+size_t gptq_fp8_gated_workspace(int64_t n_tokens, int64_t d_ff);
+int gptq_fp8_gated(const uint8_t* gq, const float* gs, const uint8_t* uq, const float* us, int64_t ldwq,
+                   int64_t ldws, int64_t d_ff, int64_t d_in, const uint8_t* xq, int64_t ldxq, const float* xs,
+                   int64_t ldxs, int64_t n_tokens, uint8_t* q, int64_t ldq, float* scales, int64_t lds,
+                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a gptq_status value (static string). */
 const char* gptq_status_string(int status);

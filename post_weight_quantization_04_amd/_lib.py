@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libgptq_mi355x.so")
 
 GPTQ_OK, GPTQ_EINVAL, GPTQ_EUNSUPPORTED, GPTQ_EHIP, GPTQ_EWORKSPACE, GPTQ_ESCRATCH = 0, 1, 2, 3, 4, 5
-GPTQ_F16, GPTQ_F32 = 0, 1
+GPTQ_F16, GPTQ_F32, GPTQ_BF16 = 0, 1, 2
 
 EXPORTS = (
     "gptq_hessian_accumulate",
@@ -39,6 +39,12 @@ EXPORTS = (
     "gptq_propagate",
     "gptq_obq_workspace",
     "gptq_obq_quantize",
+    "gptq_fp8_weight",
+    "gptq_fp8_activations",
+    "gptq_fp8_rms_norm",
+    "gptq_fp8_matmul",
+    "gptq_fp8_gated_workspace",
+    "gptq_fp8_gated",
     "gptq_kernel_count",
     "gptq_kernel_name",
     "gptq_timing_enable",
@@ -96,6 +102,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "gptq_obq_workspace": (_sz, [_i64]),
         "gptq_obq_quantize": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
                                      _sz, _vp]),
+        "gptq_fp8_weight": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]),
+        "gptq_fp8_activations": (_i32, [_vp, _i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp]),
+        "gptq_fp8_rms_norm": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i32, _i64, _i64, ctypes.c_double, _vp,
+                                     _i64, _vp, _i64, _vp]),
+        "gptq_fp8_matmul": (_i32, [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i32, _i64,
+                                   _i32, _i32, _vp]),
+        "gptq_fp8_gated_workspace": (_sz, [_i64, _i64]),
+        "gptq_fp8_gated": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64,
+                                  _vp, _i64, _vp, _sz, _vp]),
         "gptq_kernel_count": (_i32, []),
         "gptq_kernel_name": (ctypes.c_char_p, [_i32]),
         "gptq_timing_enable": (_i32, [_i32]),
@@ -300,6 +315,157 @@ def obq_quantize(W, U, dead, bits: int, codes, scales, zeros, order=None, loss=N
                                   workspace.numel() * workspace.element_size() if workspace is not None else 0,
                                   _stream(stream))
     _check("gptq_obq_quantize", rc)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit operands: e4m3 values [rows, ld] (ld a multiple of 16, zeros behind
+# the columns up to a multiple of 128) and float32 scales, as include/gptq.h
+# lays them out.  `values` may be float8_e4m3fn or uint8.
+# ---------------------------------------------------------------------------
+def _fp8_dtype_code(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return GPTQ_BF16
+    return _dtype_code(t)
+
+
+def _fp8_where(device, stream):
+    """The stream to enqueue on: the given one, or the current one of
+    ``device`` (which the library's launches need to be the current device)."""
+    import torch
+    if torch.cuda.current_device() != device.index:
+        raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    if stream.device != device:
+        raise ValueError(f"tensors on {device}, stream on {stream.device}")
+    return stream.cuda_stream
+
+
+def _fp8_matrix(t, device, what: str):
+    """(pointer, row stride) of a 2-D device view with unit column stride."""
+    if t.dim() != 2 or t.device != device or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be a 2-D view on {device} with unit column stride")
+    return t.data_ptr(), _row_stride(t)
+
+
+def _row_stride(t) -> int:
+    # the stride of a single row is never used, and torch leaves it arbitrary
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _fp8_operand(values, scales, cols: int, lead: int, along: int, device, what: str):
+    """(values pointer, ld, scales pointer, lds), with the layout checked."""
+    import torch
+    if values.dtype != torch.float8_e4m3fn and values.dtype != torch.uint8:
+        raise ValueError(f"{what}: values must be float8_e4m3fn")
+    if scales.dtype != torch.float32:
+        raise ValueError(f"{what}: scales must be float32")
+    vp, ld = _fp8_matrix(values, device, what)
+    sp, lds = _fp8_matrix(scales, device, what)
+    if values.shape[1] < (cols + 127) // 128 * 128:
+        raise ValueError(f"{what}: {values.shape[1]} stored columns hold fewer than {cols} rounded up to 128")
+    if scales.shape[0] < lead or scales.shape[1] < along:
+        raise ValueError(f"{what}: scales {tuple(scales.shape)}, expected [{lead}, {along}]")
+    return vp, ld, sp, lds
+
+
+def _blocks(d: int) -> int:
+    return (d + 127) // 128
+
+
+def _device_of(t):
+    if not t.is_cuda:
+        raise ValueError("device tensor expected")
+    return t.device
+
+
+def fp8_weight(W, values, scales, stream=None) -> None:
+    """``W [d_out, d_in]`` to 8 bits, a scale per 128 x 128 block."""
+    dev = _device_of(W)
+    wp, ldw = _fp8_matrix(W, dev, "W")
+    d_out, d_in = W.shape
+    if values.shape[0] != d_out:
+        raise ValueError("rows of the output")
+    vp, ld, sp, lds = _fp8_operand(values, scales, d_in, _blocks(d_out), _blocks(d_in), dev, "out")
+    _check("gptq_fp8_weight", load().gptq_fp8_weight(wp, _fp8_dtype_code(W), d_out, d_in, ldw, vp, ld, sp, lds,
+                                                     _fp8_where(dev, stream)))
+
+
+def fp8_activations(X, values, scales, channel_major: bool = False, stream=None) -> None:
+    """``X [n, d]`` (or ``[d, n]`` with ``channel_major``) to 8 bits, a scale
+    per token and 128 channels."""
+    dev = _device_of(X)
+    xp, ldx = _fp8_matrix(X, dev, "X")
+    n, d = (X.shape[1], X.shape[0]) if channel_major else X.shape
+    if values.shape[0] != n:
+        raise ValueError("rows of the output")
+    vp, ld, sp, lds = _fp8_operand(values, scales, d, _blocks(d), n, dev, "out")
+    _check("gptq_fp8_activations",
+           load().gptq_fp8_activations(xp, _fp8_dtype_code(X), n, d, ldx, int(bool(channel_major)), vp, ld, sp, lds,
+                                       _fp8_where(dev, stream)))
+
+
+def fp8_rms_norm(x, gain, eps: float, values, scales, residual=None, sum_out=None, stream=None) -> None:
+    """``h = x + residual``; ``h / sqrt(mean(h^2) + eps) * gain`` to 8 bits;
+    ``sum_out = h``."""
+    dev = _device_of(x)
+    xp, ldx = _fp8_matrix(x, dev, "x")
+    n, d = x.shape
+    rp, ldr, op, ldo = None, 0, None, 0
+    if residual is not None:
+        rp, ldr = _fp8_matrix(residual, dev, "residual")
+        if residual.shape != x.shape or residual.dtype != x.dtype:
+            raise ValueError("residual must have the shape and type of x")
+    if sum_out is not None:
+        op, ldo = _fp8_matrix(sum_out, dev, "sum_out")
+        if sum_out.shape != x.shape or sum_out.dtype != x.dtype:
+            raise ValueError("sum_out must have the shape and type of x")
+    if gain.shape != (d,) or gain.dtype != x.dtype or gain.device != dev or not gain.is_contiguous():
+        raise ValueError("gain must be a contiguous vector of x's type, one value per channel")
+    if values.shape[0] != n:
+        raise ValueError("rows of the output")
+    vp, ld, sp, lds = _fp8_operand(values, scales, d, _blocks(d), n, dev, "out")
+    _check("gptq_fp8_rms_norm",
+           load().gptq_fp8_rms_norm(xp, ldx, rp, ldr, op, ldo, gain.data_ptr(), _fp8_dtype_code(x), n, d, float(eps),
+                                    vp, ld, sp, lds, _fp8_where(dev, stream)))
+
+
+def fp8_matmul(wq, ws, xq, xs, d_in: int, Y, channel_major: bool = False, activation: int = 0, stream=None) -> None:
+    """``Y = act(X W^T)`` of 8-bit operands; ``Y [n, d_out]``, or ``[d_out,
+    n]`` with ``channel_major``; activation 0 none, 1 ReLU."""
+    dev = _device_of(Y)
+    yp, ldy = _fp8_matrix(Y, dev, "Y")
+    d_out, n = wq.shape[0], xq.shape[0]
+    wp, ldw, wsp, ldws = _fp8_operand(wq, ws, d_in, _blocks(d_out), _blocks(d_in), dev, "weights")
+    xp, ldx, xsp, ldxs = _fp8_operand(xq, xs, d_in, _blocks(d_in), n, dev, "activations")
+    if Y.shape != ((d_out, n) if channel_major else (n, d_out)):
+        raise ValueError("shape of Y")
+    _check("gptq_fp8_matmul",
+           load().gptq_fp8_matmul(wp, ldw, wsp, ldws, d_out, d_in, xp, ldx, xsp, ldxs, n, yp, _fp8_dtype_code(Y), ldy,
+                                  int(bool(channel_major)), int(activation), _fp8_where(dev, stream)))
+
+
+def fp8_gated_workspace(n: int, d_ff: int) -> int:
+    return int(load().gptq_fp8_gated_workspace(n, d_ff))
+
+
+def fp8_gated(gq, gs, uq, us, xq, xs, d_in: int, values, scales, workspace=None, stream=None) -> None:
+    """``silu(X G^T) * (X U^T)`` of 8-bit operands, written in 8 bits."""
+    dev = _device_of(values)
+    d_ff, n = gq.shape[0], xq.shape[0]
+    gp, ldw, gsp, ldws = _fp8_operand(gq, gs, d_in, _blocks(d_ff), _blocks(d_in), dev, "gate")
+    up, ldu, usp, ldus = _fp8_operand(uq, us, d_in, _blocks(d_ff), _blocks(d_in), dev, "up")
+    if uq.shape[0] != d_ff or (d_ff > 1 and ldu != ldw) or (ldus != ldws and d_ff > 128):
+        raise ValueError("gate and up must have one shape and strides")
+    xp, ldx, xsp, ldxs = _fp8_operand(xq, xs, d_in, _blocks(d_in), n, dev, "activations")
+    if values.shape[0] != n:
+        raise ValueError("rows of the output")
+    vp, ld, sp, lds = _fp8_operand(values, scales, d_ff, _blocks(d_ff), n, dev, "out")
+    _check("gptq_fp8_gated",
+           load().gptq_fp8_gated(gp, gsp, up, usp, ldw, ldws, d_ff, d_in, xp, ldx, xsp, ldxs, n, vp, ld, sp, lds,
+                                 _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None
+                                 else 0, _fp8_where(dev, stream)))
 
 
 # ---------------------------------------------------------------------------

@@ -22,6 +22,7 @@ const char* const kNames[K_COUNT] = {
     "q_grid_convert",         "q_group_grid",       "q_step",    "q_trail",
     "pack_codes",  "dequantize",  "output_error", "obq_hinv", "obq_rows", "propagate",
     "hinv32_load_reversed", "chol32_step", "hinv32_store_u",
+    "fp8_weight", "fp8_rows", "fp8_columns", "fp8_rms_norm", "fp8_matmul", "fp8_gated",
 };
 // The timing state is process-wide; the mutex makes concurrent entry-point
 // calls from several host threads safe, though the events then interleave.
@@ -349,6 +350,97 @@ int gptq_propagate(const void* W_hat, int w_dtype, int64_t d_out, int64_t d_in, 
     if (d_out > ((int64_t)1 << 24) || d_in > ((int64_t)1 << 22) || ldx > ((int64_t)1 << 23)) return GPTQ_EUNSUPPORTED;
     if (((d_out + 127) / 128) * ((n_tokens + 127) / 128) > (int64_t)INT32_MAX) return GPTQ_EUNSUPPORTED;
     return hip_status(launch_propagate(W_hat, d_out, d_in, X, n_tokens, ldx, Y, ldy, activation, as_stream(stream)));
+}
+
+namespace {
+constexpr int64_t kF8Cols = 128;
+inline int64_t f8_blocks(int64_t d) { return (d + kF8Cols - 1) / kF8Cols; }
+inline bool f8_dtype(int t) { return t == GPTQ_F16 || t == GPTQ_F32 || t == GPTQ_BF16; }
+inline bool f8_aligned(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0; }
+// strides of an 8-bit operand of `along` scales a row: too small for its sizes?
+inline bool f8_short(int64_t ldq, int64_t d, int64_t lds, int64_t along) {
+    return ldq < f8_blocks(d) * kF8Cols || lds < along;
+}
+constexpr int64_t kF8MaxLd = (int64_t)1 << 22;  // 256 rows of a tile stay within 2^30 bytes
+constexpr int64_t kF8MaxRows = (int64_t)1 << 24;
+}  // namespace
+
+int gptq_fp8_weight(const void* W, int w_dtype, int64_t d_out, int64_t d_in, int64_t ldw, uint8_t* q, int64_t ldq,
+                    float* scales, int64_t lds, void* stream) {
+    if (d_out < 0 || d_in < 0 || ldw < d_in || !f8_dtype(w_dtype)) return GPTQ_EINVAL;
+    if (f8_short(ldq, d_in, lds, f8_blocks(d_in))) return GPTQ_EINVAL;
+    if (d_out == 0 || d_in == 0) return GPTQ_OK;
+    if (!W || !q || !scales) return GPTQ_EINVAL;
+    if (!f8_aligned(q, ldq) || d_out > kF8MaxRows || d_in > ((int64_t)1 << 24)) return GPTQ_EUNSUPPORTED;
+    if (f8_blocks(d_out) * f8_blocks(d_in) > (int64_t)INT32_MAX) return GPTQ_EUNSUPPORTED;
+    return hip_status(launch_f8_weight(W, w_dtype, d_out, d_in, ldw, q, ldq, scales, lds, as_stream(stream)));
+}
+
+int gptq_fp8_activations(const void* X, int x_dtype, int64_t n, int64_t d, int64_t ldx, int channel_major, uint8_t* q,
+                         int64_t ldq, float* scales, int64_t lds, void* stream) {
+    if (n < 0 || d < 0 || !f8_dtype(x_dtype) || (channel_major != 0 && channel_major != 1)) return GPTQ_EINVAL;
+    if (ldx < (channel_major ? n : d) || f8_short(ldq, d, lds, n)) return GPTQ_EINVAL;
+    if (n == 0 || d == 0) return GPTQ_OK;
+    if (!X || !q || !scales) return GPTQ_EINVAL;
+    if (!f8_aligned(q, ldq) || n > (int64_t)INT32_MAX || d > ((int64_t)1 << 24)) return GPTQ_EUNSUPPORTED;
+    if (n * f8_blocks(d) > (int64_t)INT32_MAX) return GPTQ_EUNSUPPORTED;
+    return hip_status(
+        launch_f8_activations(X, x_dtype, n, d, ldx, channel_major, q, ldq, scales, lds, as_stream(stream)));
+}
+
+int gptq_fp8_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* sum_out, int64_t ldo,
+                      const void* gain, int dtype, int64_t n, int64_t d, double eps, uint8_t* q, int64_t ldq,
+                      float* scales, int64_t lds, void* stream) {
+    if (n < 0 || d < 0 || !f8_dtype(dtype) || ldx < d) return GPTQ_EINVAL;
+    if ((residual && ldr < d) || (sum_out && (!residual || ldo < d))) return GPTQ_EINVAL;
+    if (!(eps >= 1e-20 && eps <= 1e20) || f8_short(ldq, d, lds, n)) return GPTQ_EINVAL;
+    if (n == 0 || d == 0) return GPTQ_OK;
+    if (!x || !gain || !q || !scales) return GPTQ_EINVAL;
+    if (!f8_aligned(q, ldq) || n > (int64_t)INT32_MAX || d > ((int64_t)1 << 24)) return GPTQ_EUNSUPPORTED;
+    const RmsNormCall c = {x, residual, gain, sum_out, q, scales, ldx, ldr, ldo, ldq, lds, n, d, eps};
+    return hip_status(launch_f8_rms_norm(c, dtype, as_stream(stream)));
+}
+
+int gptq_fp8_matmul(const uint8_t* wq, int64_t ldwq, const float* ws, int64_t ldws, int64_t d_out, int64_t d_in,
+                    const uint8_t* xq, int64_t ldxq, const float* xs, int64_t ldxs, int64_t n, void* Y, int y_dtype,
+                    int64_t ldy, int channel_major, int activation, void* stream) {
+    if (d_out < 0 || d_in < 0 || n < 0 || !f8_dtype(y_dtype)) return GPTQ_EINVAL;
+    if ((channel_major != 0 && channel_major != 1) || (activation != 0 && activation != 1)) return GPTQ_EINVAL;
+    if (f8_short(ldwq, d_in, ldws, f8_blocks(d_in)) || f8_short(ldxq, d_in, ldxs, n)) return GPTQ_EINVAL;
+    if (ldy < (channel_major ? n : d_out)) return GPTQ_EINVAL;
+    if (d_out == 0 || n == 0) return GPTQ_OK;
+    if (!Y || (d_in > 0 && (!wq || !ws || !xq || !xs))) return GPTQ_EINVAL;
+    if (d_in > 0 && (!f8_aligned(wq, ldwq) || !f8_aligned(xq, ldxq))) return GPTQ_EUNSUPPORTED;
+    if (ldwq > kF8MaxLd || ldxq > kF8MaxLd) return GPTQ_EUNSUPPORTED;
+    if (d_out > kF8MaxRows || n > kF8MaxRows) return GPTQ_EUNSUPPORTED;
+    const F8Product c = {{wq, nullptr}, {ws, nullptr}, xq, xs, Y, ldwq, ldws, ldxq, ldxs, ldy, d_out, d_in, n,
+                         channel_major, activation};
+    return hip_status(launch_f8_matmul(c, y_dtype, as_stream(stream)));
+}
+
+size_t gptq_fp8_gated_workspace(int64_t n, int64_t d_ff) {
+    if (n <= 0 || d_ff <= 0 || n > kF8MaxRows || d_ff > kF8MaxRows) return 0;
+    return f8_gated_workspace_bytes(n, d_ff);
+}
+
+int gptq_fp8_gated(const uint8_t* gq, const float* gs, const uint8_t* uq, const float* us, int64_t ldwq, int64_t ldws,
+                   int64_t d_ff, int64_t d_in, const uint8_t* xq, int64_t ldxq, const float* xs, int64_t ldxs,
+                   int64_t n, uint8_t* q, int64_t ldq, float* scales, int64_t lds, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+    if (d_ff < 0 || d_in < 0 || n < 0) return GPTQ_EINVAL;
+    if (f8_short(ldwq, d_in, ldws, f8_blocks(d_in)) || f8_short(ldxq, d_in, ldxs, n) || f8_short(ldq, d_ff, lds, n))
+        return GPTQ_EINVAL;
+    if (d_ff == 0 || n == 0) return GPTQ_OK;
+    if (!q || !scales || (d_in > 0 && (!gq || !gs || !uq || !us || !xq || !xs))) return GPTQ_EINVAL;
+    if (d_in > 0 && (!f8_aligned(gq, ldwq) || !f8_aligned(uq, ldwq) || !f8_aligned(xq, ldxq))) return GPTQ_EUNSUPPORTED;
+    if (!f8_aligned(q, ldq)) return GPTQ_EUNSUPPORTED;
+    if (ldwq > kF8MaxLd || ldxq > kF8MaxLd || d_ff > kF8MaxRows || n > kF8MaxRows) return GPTQ_EUNSUPPORTED;
+    if (n * f8_blocks(d_ff) > (int64_t)INT32_MAX) return GPTQ_EUNSUPPORTED;
+    const size_t need = f8_gated_workspace_bytes(n, d_ff);
+    if (need > 0 && (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256 != 0))
+        return GPTQ_EWORKSPACE;
+    const F8Product c = {{gq, uq}, {gs, us}, xq, xs, nullptr, ldwq, ldws, ldxq, ldxs, 0, d_ff, d_in, n, 0, 0};
+    return hip_status(launch_f8_gated(c, q, ldq, scales, lds, workspace, as_stream(stream)));
 }
 
 }  // extern "C"

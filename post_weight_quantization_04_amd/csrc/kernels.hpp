@@ -28,6 +28,12 @@ enum KernelId {
     K_HINV32_LOAD,
     K_CHOL32_STEP,
     K_HINV32_STORE,
+    K_F8_WEIGHT,
+    K_F8_ROWS,
+    K_F8_COLUMNS,
+    K_F8_NORM,
+    K_F8_MATMUL,
+    K_F8_GATED,
     K_COUNT
 };
 
@@ -110,5 +116,35 @@ hipError_t launch_obq(const void* W, int w_is_f16, int64_t d_out, int64_t d_in, 
 // ---- propagation to the next layer ------------------------------------------
 hipError_t launch_propagate(const void* W, int64_t d_out, int64_t d_in, const void* X, int64_t ntok, int64_t ldx,
                             void* Y, int64_t ldy, int relu, hipStream_t s);
+
+// ---- 8-bit operands (e4m3, a scale per block of 128) -------------------------
+// dtype codes as gptq_dtype: 0 f16, 1 f32, 2 bf16
+hipError_t launch_f8_weight(const void* W, int dtype, int64_t d_out, int64_t d_in, int64_t ldw, uint8_t* q,
+                            int64_t ldq, float* scales, int64_t lds, hipStream_t s);
+hipError_t launch_f8_activations(const void* X, int dtype, int64_t n, int64_t d, int64_t ldx, int channel_major,
+                                 uint8_t* q, int64_t ldq, float* scales, int64_t lds, hipStream_t s);
+struct RmsNormCall {
+    const void *x, *residual, *gain;  // residual, sum_out: or null
+    void* sum_out;
+    uint8_t* q;
+    float* scales;
+    int64_t ldx, ldr, ldo, ldq, lds, n, d;
+    double eps;
+};
+hipError_t launch_f8_rms_norm(const RmsNormCall& c, int dtype, hipStream_t s);
+// X [n, K] against one (product) or two (gate, up) weights [M, K]
+struct F8Product {
+    const uint8_t* wq[2];
+    const float* ws[2];
+    const uint8_t* xq;
+    const float* xs;
+    void* y;
+    int64_t ldw, ldws, ldx, ldxs, ldy, M, K, n;
+    int channel_major, relu;
+};
+hipError_t launch_f8_matmul(const F8Product& c, int y_dtype, hipStream_t s);
+size_t f8_gated_workspace_bytes(int64_t n, int64_t d_ff);
+hipError_t launch_f8_gated(const F8Product& c, uint8_t* q, int64_t ldq, float* scales, int64_t lds, void* ws,
+                           hipStream_t s);
 
 }  // namespace gptq

@@ -174,3 +174,123 @@ def quantize_greedy(W, factor: Factor, bits: int, ws: Optional[Workspace] = None
     _lib.obq_quantize(W, factor.U, factor.dead if use_dead else None, bits, out.codes, out.scales, out.zeros,
                       out.order, out.loss, buf, stream=stream)
     return out
+
+
+# ---------------------------------------------------------------------------
+# 8-bit operands (e4m3 values, a float32 scale per block of 128)
+# ---------------------------------------------------------------------------
+@dataclasses.dataclass
+class Fp8:
+    """An 8-bit matrix of ``cols`` columns.  Activations hold a row per token
+    and ``scales [ceil(cols/128), rows]``; weights a row per output channel
+    and ``scales [ceil(rows/128), ceil(cols/128)]``."""
+    data: "torch.Tensor"     # [rows, ld] float8_e4m3fn, ld >= cols rounded up to 128, zeros behind cols
+    scales: "torch.Tensor"   # float32
+    cols: int
+
+    @property
+    def values(self):
+        """``[rows, cols]`` view of the e4m3 values (without their scales)."""
+        return self.data[:, :self.cols]
+
+
+def _fp8_out(rows: int, cols: int, scales, device, stream) -> Fp8:
+    import torch
+    with _on(stream):
+        return Fp8(torch.empty((rows, (cols + 127) // 128 * 128), dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty(scales, dtype=torch.float32, device=device), cols)
+
+
+def _on(stream):
+    """Memory made inside belongs to the stream that the call runs on."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _fp8_cols(out: Fp8, cols: int) -> Fp8:
+    if out.cols != cols:
+        raise ValueError(f"out holds {out.cols} columns, the result has {cols}")
+    return out
+
+
+def fp8_weight(W, out: Optional[Fp8] = None, stream=None) -> Fp8:
+    """``W [d_out, d_in]`` (float16, bfloat16 or float32) in 8 bits, one scale
+    per 128 x 128 block (``gptq_fp8_weight``)."""
+    d_out, d_in = W.shape
+    out = (_fp8_cols(out, d_in) if out is not None else
+           _fp8_out(d_out, d_in, ((d_out + 127) // 128, (d_in + 127) // 128), W.device, stream))
+    _lib.fp8_weight(W, out.data, out.scales, stream=stream)
+    return out
+
+
+def fp8_activations(X, channel_major: bool = False, out: Optional[Fp8] = None, stream=None) -> Fp8:
+    """Activations ``X [n, d]``, or ``[d, n]`` with ``channel_major`` (the
+    layout of the calibration inputs), in 8 bits, one scale per token and 128
+    channels (``gptq_fp8_activations``)."""
+    n, d = (X.shape[1], X.shape[0]) if channel_major else X.shape
+    out = (_fp8_cols(out, d) if out is not None else _fp8_out(n, d, ((d + 127) // 128, n), X.device, stream))
+    _lib.fp8_activations(X, out.data, out.scales, channel_major=channel_major, stream=stream)
+    return out
+
+
+def fp8_rms_norm(x, gain, eps: float = 1e-6, residual=None, out: Optional[Fp8] = None, sum_out=None, stream=None):
+    """``h = x + residual`` and ``h / sqrt(mean(h^2) + eps) * gain`` in 8 bits
+    (``gptq_fp8_rms_norm``): returns the 8-bit activations and ``h`` in x's
+    type (None without a residual).  ``sum_out`` may be ``x`` or ``residual``."""
+    import torch
+    n, d = x.shape
+    out = (_fp8_cols(out, d) if out is not None else _fp8_out(n, d, ((d + 127) // 128, n), x.device, stream))
+    if residual is not None and sum_out is None:
+        with _on(stream):
+            sum_out = torch.empty((n, d), dtype=x.dtype, device=x.device)
+    _lib.fp8_rms_norm(x, gain, eps, out.data, out.scales, residual=residual, sum_out=sum_out, stream=stream)
+    return out, sum_out
+
+
+def fp8_matmul(w: Fp8, x: Fp8, dtype=None, relu: bool = False, channel_major: bool = False, out=None, stream=None):
+    """``act(X W^T)`` of an 8-bit weight and 8-bit activations
+    (``gptq_fp8_matmul``): ``[n, d_out]``, or ``[d_out, n]`` with
+    ``channel_major``, as ``dtype`` (float16 by default)."""
+    import torch
+    if w.cols != x.cols:
+        raise ValueError(f"weights of {w.cols} columns, activations of {x.cols}")
+    if out is None:
+        shape = (w.data.shape[0], x.data.shape[0])
+        with _on(stream):
+            out = torch.empty(shape if channel_major else shape[::-1], dtype=dtype or torch.float16,
+                              device=x.data.device)
+    elif dtype is not None and dtype != out.dtype:
+        raise ValueError(f"out is {out.dtype}, not {dtype}")
+    _lib.fp8_matmul(w.data, w.scales, x.data, x.scales, w.cols, out, channel_major=channel_major,
+                    activation=1 if relu else 0, stream=stream)
+    return out
+
+
+def fp8_gated(gate: Fp8, up: Fp8, x: Fp8, ws: Optional[Workspace] = None, out: Optional[Fp8] = None, stream=None) -> Fp8:
+    """``silu(X G^T) * (X U^T)`` in 8 bits (``gptq_fp8_gated``): the input of
+    the down projection.  Few tokens need scratch memory: that of ``ws``, or
+    memory of the call's own."""
+    import torch
+    if gate.cols != x.cols or up.cols != x.cols:
+        raise ValueError(f"weights of {gate.cols} and {up.cols} columns, activations of {x.cols}")
+    n, d_ff = x.data.shape[0], gate.data.shape[0]
+    out = (_fp8_cols(out, d_ff) if out is not None else
+           _fp8_out(n, d_ff, ((d_ff + 127) // 128, n), x.data.device, stream))
+    need = _lib.fp8_gated_workspace(n, d_ff)
+    buf = None
+    if need:
+        with _on(stream):
+            buf = ws.get(need) if ws is not None else torch.empty(need, dtype=torch.uint8, device=x.data.device)
+    _lib.fp8_gated(gate.data, gate.scales, up.data, up.scales, x.data, x.scales, gate.cols, out.data, out.scales, buf,
+                   stream=stream)
+    return out
+
+
+def propagate_fp8(w: Fp8, X, relu: bool = False, out=None, stream=None):
+    """``propagate`` through a layer kept in 8 bits: the activations ``X [d_in,
+    n]`` go to 8 bits, and ``act(W X)`` comes back as ``[d_out, n]`` in X's
+    type, the next layer's input."""
+    x = fp8_activations(X, channel_major=True, stream=stream)
+    return fp8_matmul(w, x, dtype=X.dtype if out is None else None, relu=relu, channel_major=True, out=out,
+                      stream=stream)

@@ -1,0 +1,122 @@
+"""Plain definitions of the 8-bit operators in numpy: the e4m3 format by its
+bits, block scales in the stated float32 steps, and products, norm and gated
+block in 64 bits with bounds on what the float32 sums may lose."""
+import numpy as np
+
+BLOCK = 128
+U = 2.0 ** -24          # float32: half a step, relative
+HALF = {"float16": 2.0 ** -11, "bfloat16": 2.0 ** -8, "float32": 2.0 ** -24}
+TINY = {"float16": 2.0 ** -25, "bfloat16": 2.0 ** -134, "float32": 2.0 ** -150}  # half the smallest step
+
+
+def _decode(c):
+    sign, e, f = -1.0 if c & 0x80 else 1.0, (c >> 3) & 15, c & 7
+    if e == 15 and f == 7:
+        return np.nan
+    return sign * (f * 2.0 ** -9 if e == 0 else (1 + f / 8) * 2.0 ** (e - 7))
+
+
+TABLE = np.array([_decode(c) for c in range(256)])
+_POS = TABLE[:127]                      # 0 .. 448 in order
+
+
+def decode(codes):
+    return TABLE[np.asarray(codes, dtype=np.uint8)]
+
+
+def encode(v):
+    """Codes nearest to v (|v| < 464), halves to the even code; NaN to 0x7F."""
+    v = np.asarray(v, dtype=np.float64)
+    a = np.abs(np.where(np.isnan(v), 0.0, v))
+    hi = np.searchsorted(_POS, a, side="left").clip(0, 126)
+    lo = (hi - 1).clip(0)
+    dh, dl = _POS[hi] - a, a - _POS[lo]
+    c = np.where((dl < dh) | ((dl == dh) & (lo % 2 == 0)), lo, hi)
+    c = np.where(a >= 448.0, 126, c)
+    c = c | np.where(np.signbit(v), 0x80, 0)
+    return np.where(np.isnan(v), 0x7F, c).astype(np.uint8)
+
+
+def blocks(d):
+    return (d + BLOCK - 1) // BLOCK
+
+
+def _scale(peak):
+    return np.maximum(peak, np.float32(2.0 ** -96)) / np.float32(448.0)  # maximum keeps NaN
+
+
+def quantize_rows(x):
+    """x [n, d] float32 -> codes [n, 128 nb], scales [nb, n], in float32 steps."""
+    n, d = x.shape
+    nb = blocks(d)
+    h = np.zeros((n, nb * BLOCK), np.float32)
+    h[:, :d] = x
+    h = h.reshape(n, nb, BLOCK)
+    with np.errstate(all="ignore"):
+        s = _scale(np.abs(h).max(axis=2))
+        inv = np.float32(1.0) / s
+        codes = encode(h * inv[:, :, None])
+    return codes.reshape(n, nb * BLOCK), np.ascontiguousarray(s.T)
+
+
+def quantize_tiles(w):
+    m, d = w.shape
+    mb, nb = blocks(m), blocks(d)
+    h = np.zeros((mb * BLOCK, nb * BLOCK), np.float32)
+    h[:m, :d] = w
+    h = h.reshape(mb, BLOCK, nb, BLOCK)
+    with np.errstate(all="ignore"):
+        s = _scale(np.abs(h).max(axis=(1, 3)))
+        inv = np.float32(1.0) / s
+        codes = encode(h * inv[:, None, :, None])
+    return codes.reshape(mb * BLOCK, nb * BLOCK)[:m], s
+
+
+def rows_values(codes, scales, d):
+    return (decode(codes) * np.repeat(scales.astype(np.float64).T, BLOCK, axis=1))[:, :d]
+
+
+def tiles_values(codes, scales, d):
+    s = np.repeat(np.repeat(scales.astype(np.float64), BLOCK, axis=0)[:codes.shape[0]], BLOCK, axis=1)
+    return (decode(codes) * s)[:, :d]
+
+
+def product(x, w):
+    """X W^T in 64 bits and a bound on the error of the float32 sums: the 128
+    products of a block (exact) are added with at most one step of error each
+    (the adder may cut instead of rounding), two roundings scale the block,
+    and the blocks are added one by one, twice where waves share them."""
+    y = x @ w.T
+    size = np.abs(x) @ np.abs(w).T
+    return y, (BLOCK + 2 * blocks(x.shape[1]) + 4) * 2 * U * size
+
+
+def silu_gate(g, u, dg, du):
+    """silu(g) u in 64 bits and its bound from those of g and u (|silu'| is
+    below 1.1; exp, quotient and products add a few roundings)."""
+    with np.errstate(over="ignore"):
+        sg = g / (1.0 + np.exp(-g))
+    # exp(-g) is formed from fl32(g log2 e): relative error up to |g| 2^-23
+    return sg * u, 1.1 * dg * (np.abs(u) + du) + np.abs(sg) * du + (8 + 2 * np.abs(g)) * 2 * U * np.abs(sg * u) + 2.0 ** -140
+
+
+def check_quantized(codes, scales, h, dh):
+    """The codes and scales of h [n, d], known to dh: every scale within what
+    dh allows, every value within half a step of e4m3 of its own."""
+    n, d = h.shape
+    nb = blocks(d)
+    hp = np.zeros((n, nb * BLOCK))
+    ep = np.zeros((n, nb * BLOCK))
+    hp[:, :d], ep[:, :d] = h, dh
+    peak = np.abs(hp).reshape(n, nb, BLOCK).max(axis=2)
+    slack = ep.reshape(n, nb, BLOCK).max(axis=2)
+    s = scales.astype(np.float64).T
+    want = np.maximum(peak, 2.0 ** -96) / 448.0
+    assert np.all(np.abs(s - want) <= slack / 448.0 + 2 * U * want), np.max(np.abs(s - want) / want)
+    sv = np.repeat(s, BLOCK, axis=1)
+    off = np.abs(decode(codes) * sv - hp)
+    # half a step: 2^-4 of the value, 2^-10 scales below the normal range; the
+    # reciprocal and its product move the value by 2 more float32 roundings
+    most = ep + 2.0 ** -4 * (np.abs(hp) + ep) * (1 + 2.0 ** -20) + 2.0 ** -10 * sv + 4 * U * np.abs(hp)
+    assert np.all(off <= most), float(np.max(off / most))
+    assert not codes[:, d:].any(), "columns behind the last are zero"
