@@ -413,6 +413,7 @@ int gptq_fp8_matmul(const uint8_t* wq, int64_t ldwq, const float* ws, int64_t ld
     if (d_in > 0 && (!f8_aligned(wq, ldwq) || !f8_aligned(xq, ldxq))) return GPTQ_EUNSUPPORTED;
     if (ldwq > kF8MaxLd || ldxq > kF8MaxLd) return GPTQ_EUNSUPPORTED;
     if (d_out > kF8MaxRows || n > kF8MaxRows) return GPTQ_EUNSUPPORTED;
+    if (((d_out + 63) / 64) * ((n + 63) / 64) > (int64_t)INT32_MAX) return GPTQ_EUNSUPPORTED;
     const F8Product c = {{wq, nullptr}, {ws, nullptr}, xq, xs, Y, ldwq, ldws, ldxq, ldxs, ldy, d_out, d_in, n,
                          channel_major, activation};
     return hip_status(launch_f8_matmul(c, y_dtype, as_stream(stream)));

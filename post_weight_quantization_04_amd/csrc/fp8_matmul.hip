@@ -8,11 +8,16 @@
 // The inner sum over a block of 128 runs on MFMA from zero; its result times
 // the product of the two scales is added to the float32 accumulators.
 //
-// The MFMA is the float16 one (four 16x16x32, the values converted in
-// registers, every product exact, within 1e-7 of the sum).  The e4m3 one adds
-// each lane's eight neighbouring k with 14 bits below the largest of the eight
+// Two kinds of MFMA form the inner sum.  The e4m3 one (16x16x128) adds each
+// lane's eight neighbouring k with 14 bits below the largest of the eight
 // products and cuts the rest (measured: beside a product of 2^16, one of 2^3
-// stays and one of 2^2 is lost), which leaves results 2e-5 of their norm off.
+// stays and one of 2^2 is lost), which leaves results about 2e-5 of their norm
+// from exact.  The float16 one (four 16x16x32, the values converted in
+// registers, every product exact) stays within 1e-7 at half the rate.  float16
+// and bfloat16 outputs, whose last bit is 5e-4 and 4e-3, come from the e4m3
+// MFMA in the tile kernel; float32 outputs and the gated block, whose scales
+// are float32, from the float16 one, and so does everything the few-token
+// kernel computes, which HBM bounds either way.
 #include "fp8_common.hpp"
 #include "kernels.hpp"
 
@@ -58,26 +63,58 @@ __device__ __forceinline__ float4v block_product(const Halves& a, const Halves& 
     return c;
 }
 
-__device__ __forceinline__ int8v f8_load32(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    union {
-        uint4v h[2];
-        int8v v;
-    } u;
-    u.h[0] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-    u.h[1] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(r, off + 16, 0, 0));
-    return u.v;
+// D = A B + C over 128 e4m3 values of k.  Lane l holds 32 consecutive k of row
+// (A) or column (B) l % 16, the k group l / 16; result lane l holds
+// C[4 (l / 16) + v][l % 16].  Both operands are loaded by the same map, so the
+// sum does not depend on the order of k inside a group.
+__device__ __forceinline__ float4v block_product(int8v a, int8v b) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, (float4v){}, 0, 0, 0, 0, 0, 0);
 }
+
+template <bool kHalf>
+struct Operand {
+    typedef int8v type;
+    static __device__ __forceinline__ type of(int8v v) { return v; }
+};
+template <>
+struct Operand<true> {
+    typedef Halves type;
+    static __device__ __forceinline__ type of(int8v v) { return to_halves(v); }
+};
 
 __device__ __forceinline__ float relu_if(float y, int relu) { return relu && y < 0.0f ? 0.0f : y; }  // keeps NaN
 
 // silu(g) u; exp overflows to infinity for g below -88, where the result is -0
 __device__ __forceinline__ float gated(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
 
-// ---------------------------------------------------------------------------
-// Few tokens: sixteen weight rows and 16 kTn tokens a workgroup.  The weights
-// are read once, straight into registers; the waves share the blocks of k and
-// their sums meet in LDS, added in wave order.
-// ---------------------------------------------------------------------------
+// Where chunk c of row r goes in the row's 128 bytes of LDS: c ^ f8_swizzle(r).
+// A fragment read takes 16 bytes a lane, row l % 16, and LDS serves it sixteen
+// lanes at a time: eight rows of one k group (0-3, 12-15) with the other eight
+// (4-11) of the next, then the reverse (measured).  The next group's chunk is
+// the same one with bit 1 flipped, so rows 4-11 repeat the others' values and
+// the sixteen lanes take sixteen different chunks of two rows' 256 bytes.
+__host__ __device__ constexpr int f8_swizzle(int r) { return (r / 2 % 2) | (r / 8 % 2) * 6; }
+
+typedef __attribute__((address_space(3))) void lds_void;
+__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off, uint32_t base) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, base, 0, 0);
+}
+__device__ __forceinline__ void copy4(__amdgpu_buffer_rsrc_t r, float* lds, uint32_t off, uint32_t base) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 4, off, base, 0, 0);
+}
+
+// The fragment of sixteen rows at p that lane (l16, kg) holds: chunks 2 kg and
+// 2 kg + 1 of row l16 (swz0, swz1: where they lie in a row).
+__device__ __forceinline__ int8v f8_fragment(const uint8_t* p, int l16, int swz0, int swz1) {
+    union {
+        uint4v h[2];
+        int8v v;
+    } u;
+    u.h[0] = *reinterpret_cast<const uint4v*>(p + l16 * kF8Block + swz0);
+    u.h[1] = *reinterpret_cast<const uint4v*>(p + l16 * kF8Block + swz1);
+    return u.v;
+}
+
 struct MmArgs {
     const uint8_t* wq[2];
     const float* ws[2];
@@ -88,70 +125,153 @@ struct MmArgs {
     int nb, channel_major, relu;
 };
 
-template <typename T, int kWaves, int kTn, int kMats>
+// ---------------------------------------------------------------------------
+// Few tokens: 16 kTm weight rows and 16 kTn tokens a workgroup.  The waves
+// share the blocks of k and work on their own, without barriers: a wave copies
+// its next kStages - 1 blocks to its own part of LDS (eight rows of 128 bytes
+// an instruction; loads into registers would ask for 64 separate pieces of 16
+// bytes, since neighbouring lanes of a fragment hold different rows, and the
+// address unit bounds them: 16 us at 24 tokens of 11008 x 4096).  The waves'
+// sums meet in LDS, added in wave order.  kOctets: rows of tokens that are
+// copied, in eights (the others' columns are computed from whatever lies there
+// and never stored).
+// ---------------------------------------------------------------------------
+template <typename T, int kWaves, int kTm, int kOctets, int kMats, int kStages>
 __global__ __launch_bounds__(kWaves* kWave) void f8_few_kernel(MmArgs a) {
-    __shared__ float part[kWaves][kMats * kTn][4][kWave];
+    constexpr int kTn = (kOctets + 1) / 2;
+    constexpr int kA = kTm * kMats;  // fragments of weights: row tiles of the first matrix, then of the second
+    constexpr int kLoads = 2 * kA + kOctets + kTn + kMats;  // vector memory instructions a block
+    constexpr int kPart = (16 * kA + 16 * kTn) * kF8Block;  // a wave's part of a stage
+    static_assert(kStages >= 2 && kStages <= 4 && (kStages - 1) * kLoads < 64, "stages; the wait counts to 63");
+    static_assert(kA * kTn * 1024 <= kPart, "the sums meet in the first stage");
+    __shared__ __align__(16) uint8_t stage0[kWaves * kPart];
+    __shared__ __align__(16) uint8_t stage1[kWaves * kPart];
+    __shared__ __align__(16) uint8_t stage2[kStages > 2 ? kWaves * kPart : 16];
+    __shared__ __align__(16) uint8_t stage3[kStages > 3 ? kWaves * kPart : 16];
     const int tid = threadIdx.x, lane = tid % kWave, w = wave_id();
-    const int64_t r0 = (int64_t)blockIdx.x * 16, t0 = (int64_t)blockIdx.y * (16 * kTn);
-    const int rows = (int)min(a.M - r0, (int64_t)16), toks = (int)min(a.n - t0, (int64_t)(16 * kTn));
-    __amdgpu_buffer_rsrc_t rw[kMats];
-#pragma unroll
-    for (int m = 0; m < kMats; ++m) rw[m] = f8_rsrc(a.wq[m] + r0 * a.ldw, (uint32_t)((rows - 1) * a.ldw + a.nb * kF8Block));
-    const __amdgpu_buffer_rsrc_t rx = f8_rsrc(a.xq + t0 * a.ldx, (uint32_t)((toks - 1) * a.ldx + a.nb * kF8Block));
-    const int l16 = lane % 16, kg = lane / 16;
+    const int64_t r0 = (int64_t)blockIdx.x * (16 * kTm), t0 = (int64_t)blockIdx.y * (16 * kTn);
+    const int rows = (int)min(a.M - r0, (int64_t)(16 * kTm)), toks = (int)min(a.n - t0, (int64_t)(16 * kTn));
+    const int nb = a.nb, l16 = lane % 16, kg = lane / 16;
+    const uint32_t wbytes = (uint32_t)((rows - 1) * a.ldw + nb * kF8Block);
+    const __amdgpu_buffer_rsrc_t rw = f8_rsrc(a.wq[0] + r0 * a.ldw, wbytes);
+    const __amdgpu_buffer_rsrc_t ru = kMats == 2 ? f8_rsrc(a.wq[1] + r0 * a.ldw, wbytes) : rw;
+    const __amdgpu_buffer_rsrc_t rx = f8_rsrc(a.xq + t0 * a.ldx, (uint32_t)((toks - 1) * a.ldx + nb * kF8Block));
+    const __amdgpu_buffer_rsrc_t rws = f8_rsrc(a.ws[0] + (r0 / kF8Block) * a.ldws, (uint32_t)(4 * nb));
+    const __amdgpu_buffer_rsrc_t rus =
+        kMats == 2 ? f8_rsrc(a.ws[1] + (r0 / kF8Block) * a.ldws, (uint32_t)(4 * nb)) : rws;
 
-    float4v acc[kMats][kTn];
+    uint32_t ao[2 * kTm], bo[kOctets], so[kTn];
 #pragma unroll
-    for (int m = 0; m < kMats; ++m)
+    for (int i = 0; i < 2 * kTm; ++i) {
+        const int r = 8 * i + lane / 8;
+        ao[i] = r < rows ? (uint32_t)(r * a.ldw + 16 * ((lane % 8) ^ f8_swizzle(r))) : kF8Out;
+    }
+#pragma unroll
+    for (int i = 0; i < kOctets; ++i) {
+        const int r = 8 * i + lane / 8;
+        bo[i] = r < toks ? (uint32_t)(r * a.ldx + 16 * ((lane % 8) ^ f8_swizzle(r))) : kF8Out;
+    }
+#pragma unroll
+    for (int j = 0; j < kTn; ++j) so[j] = 16 * j + l16 < toks ? (uint32_t)(4 * (16 * j + l16)) : kF8Out;
+    const int swz0 = 16 * ((2 * kg) ^ f8_swizzle(l16)), swz1 = 16 * ((2 * kg + 1) ^ f8_swizzle(l16));
+
+    float4v acc[kA][kTn];
+#pragma unroll
+    for (int m = 0; m < kA; ++m)
 #pragma unroll
         for (int j = 0; j < kTn; ++j) acc[m][j] = (float4v){};
-    const float* wsr[kMats];
-#pragma unroll
-    for (int m = 0; m < kMats; ++m) wsr[m] = a.ws[m] + (r0 / kF8Block) * a.ldws;
 
-    for (int b = w; b < a.nb; b += kWaves) {
-        const uint32_t ko = (uint32_t)(b * kF8Block + 32 * kg);
-        int8v av[kMats], bv[kTn];
-        float xsv[kTn];
+    // the wave's i-th block; workgroups start at different ones, so that they
+    // do not all ask for the same lines of X at once
+    const int shift = nb > 0 ? (int)(blockIdx.x * 5u % (unsigned)nb) : 0;
+    const int mine = w < nb ? (nb - w + kWaves - 1) / kWaves : 0;
+    float xs[kStages][kTn], ws[kStages][kMats];
+    auto copy = [&](uint8_t* stage, float (&x)[kTn], float (&s)[kMats], int i) {
+        int b = w + min(i, mine - 1) * kWaves + shift;  // past the wave's last block, that one again, never used
+        b = b >= nb ? b - nb : b;
+        const uint32_t ko = (uint32_t)(b * kF8Block);
+        uint8_t* p = stage + w * kPart;
 #pragma unroll
-        for (int m = 0; m < kMats; ++m) av[m] = f8_load32(rw[m], l16 < rows ? (uint32_t)(l16 * a.ldw) + ko : kF8Out);
+        for (int m = 0; m < kMats; ++m)
 #pragma unroll
-        for (int j = 0; j < kTn; ++j) {
-            const int t = 16 * j + l16;
-            bv[j] = f8_load32(rx, t < toks ? (uint32_t)(t * a.ldx) + ko : kF8Out);
-            xsv[j] = t < toks ? a.xs[b * a.ldxs + t0 + t] : 0.0f;
-        }
+            for (int c = 0; c < 2 * kTm; ++c) copy16(m ? ru : rw, p + 1024 * (2 * kTm * m + c), ao[c], ko);
 #pragma unroll
-        for (int m = 0; m < kMats; ++m) {
-            const float sw = wsr[m][b];
+        for (int c = 0; c < kOctets; ++c) copy16(rx, p + 2048 * kA + 1024 * c, bo[c], ko);
+        const __amdgpu_buffer_rsrc_t rs = f8_rsrc(a.xs + b * a.ldxs + t0, (uint32_t)(4 * toks));
+#pragma unroll
+        for (int j = 0; j < kTn; ++j) x[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, so[j], 0, 0));
+        s[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rws, 4 * b, 0, 0));
+        if (kMats == 2) s[kMats - 1] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rus, 4 * b, 0, 0));
+    };
+    auto step = [&](uint8_t* stage, float (&x)[kTn], float (&s)[kMats], int i) {
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStages - 1) * kLoads) : "memory");
+        const uint8_t* p = stage + w * kPart;
+        int8v av[kA], bv[kTn];
+#pragma unroll
+        for (int m = 0; m < kA; ++m) av[m] = f8_fragment(p + 2048 * m, l16, swz0, swz1);
+#pragma unroll
+        for (int j = 0; j < kTn; ++j) bv[j] = f8_fragment(p + 2048 * (kA + j), l16, swz0, swz1);
+        float sc[kMats][kTn];
+#pragma unroll
+        for (int m = 0; m < kMats; ++m)
+#pragma unroll
+            for (int j = 0; j < kTn; ++j) sc[m][j] = x[j] * s[m];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read, before it is copied over
+        copy(stage, x, s, i + kStages);
+        Halves bh[kTn];
+#pragma unroll
+        for (int j = 0; j < kTn; ++j) bh[j] = to_halves(bv[j]);
+#pragma unroll
+        for (int m = 0; m < kA; ++m) {
             const Halves ah = to_halves(av[m]);
 #pragma unroll
             for (int j = 0; j < kTn; ++j) {
-                const float4v p = block_product(ah, to_halves(bv[j]));
-                const float s = xsv[j] * sw;
+                const float4v q = block_product(ah, bh[j]);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) acc[m][j][v] = fmaf(p[v], s, acc[m][j][v]);
+                for (int v = 0; v < 4; ++v) acc[m][j][v] = fmaf(q[v], sc[m / kTm][j], acc[m][j][v]);
             }
         }
+    };
+    if (mine > 0) {
+        copy(stage0, xs[0], ws[0], 0);
+        copy(stage1, xs[1], ws[1], 1);
+        if (kStages > 2) copy(stage2, xs[kStages > 2 ? 2 : 0], ws[kStages > 2 ? 2 : 0], 2);
+        if (kStages > 3) copy(stage3, xs[kStages > 3 ? 3 : 0], ws[kStages > 3 ? 3 : 0], 3);
+        int i = 0;
+        for (; i + kStages <= mine; i += kStages) {
+            step(stage0, xs[0], ws[0], i);
+            step(stage1, xs[1], ws[1], i + 1);
+            if (kStages > 2) step(stage2, xs[kStages > 2 ? 2 : 0], ws[kStages > 2 ? 2 : 0], i + 2);
+            if (kStages > 3) step(stage3, xs[kStages > 3 ? 3 : 0], ws[kStages > 3 ? 3 : 0], i + 3);
+        }
+        if (i < mine) step(stage0, xs[0], ws[0], i);
+        if (i + 1 < mine) step(stage1, xs[1], ws[1], i + 1);
+        if (kStages > 3 && i + 2 < mine) step(stage2, xs[kStages > 2 ? 2 : 0], ws[kStages > 2 ? 2 : 0], i + 2);
     }
+    // every copy has landed before the memory is used for the sums
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __syncthreads();
+    float* part = reinterpret_cast<float*>(stage0);  // [kWaves][kA kTn][4][kWave]
 #pragma unroll
-    for (int m = 0; m < kMats; ++m)
+    for (int m = 0; m < kA; ++m)
 #pragma unroll
         for (int j = 0; j < kTn; ++j)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) part[w][m * kTn + j][v][lane] = acc[m][j][v];
+            for (int v = 0; v < 4; ++v) part[((w * kA * kTn + m * kTn + j) * 4 + v) * kWave + lane] = acc[m][j][v];
     __syncthreads();
-    // value i of the 256 kTn: token subtile i / 256, register (i / 64) % 4, lane i % 64
-    for (int i = tid; i < 256 * kTn; i += kWaves * kWave) {
-        const int j = i / 256, v = (i / kWave) % 4, l = i % kWave;
+    // value i of the 256 kTm kTn: row tile, token tile, register, lane
+#pragma unroll
+    for (int i = tid; i < 256 * kTm * kTn; i += kWaves * kWave) {
+        const int mj = i / 256, v = (i / kWave) % 4, l = i % kWave;
         float sum[kMats];
 #pragma unroll
         for (int m = 0; m < kMats; ++m) {
             sum[m] = 0.0f;
 #pragma unroll
-            for (int ww = 0; ww < kWaves; ++ww) sum[m] += part[ww][m * kTn + j][v][l];
+            for (int ww = 0; ww < kWaves; ++ww)
+                sum[m] += part[((ww * kA * kTn + m * kTm * kTn + mj) * 4 + v) * kWave + l];
         }
-        const int t = 16 * j + l % 16, r = 4 * (l / 16) + v;
+        const int t = 16 * (mj % kTn) + l % 16, r = 16 * (mj / kTn) + 4 * (l / 16) + v;
         if (t < toks && r < rows) {
             const float y = kMats == 2 ? gated(sum[0], sum[kMats - 1]) : relu_if(sum[0], a.relu);
             T* o = static_cast<T*>(a.y);
@@ -161,32 +281,481 @@ __global__ __launch_bounds__(kWaves* kWave) void f8_few_kernel(MmArgs a) {
     }
 }
 
-template <typename T, int kMats>
-hipError_t few_launch(const MmArgs& a, TimedLaunch t, hipStream_t s) {
-    const unsigned gx = (unsigned)((a.M + 15) / 16);
-    if (a.n <= 16) GPTQ_LAUNCH(t, (f8_few_kernel<T, 8, 1, kMats>), dim3(gx, 1), dim3(512), 0, s, a);
-    else GPTQ_LAUNCH(t, (f8_few_kernel<T, 8, 2, kMats>), dim3(gx, (unsigned)((a.n + 31) / 32)), dim3(512), 0, s, a);
+template <typename T, int kWaves, int kTm, int kOctets, int kMats, int kStages>
+hipError_t few_go(const MmArgs& a, TimedLaunch t, hipStream_t s) {
+    constexpr int kTn = (kOctets + 1) / 2;
+    const dim3 grid((unsigned)((a.M + 16 * kTm - 1) / (16 * kTm)), (unsigned)((a.n + 16 * kTn - 1) / (16 * kTn)));
+    GPTQ_LAUNCH(t, (f8_few_kernel<T, kWaves, kTm, kOctets, kMats, kStages>), grid, dim3(kWaves * kWave), 0, s, a);
     return hipGetLastError();
 }
 
+// Eight waves share k where a workgroup has a CU to itself and blocks enough
+// for them, four otherwise (two workgroups a CU then hide each other's ends):
+// 11008 x 4096 weights, 24 tokens, 10.9 against 12.3 us; 4096 x 11008, one
+// token, 9.7 against 9.5 us, 24 tokens 14.3 against 11.8 us.
+template <typename T, int kOctets, int kMats>
+hipError_t few_waves(const MmArgs& a, TimedLaunch t, hipStream_t s) {
+    if constexpr (kMats == 1 && kOctets <= 4)
+        if ((a.M + 15) / 16 <= device_cu_count() && a.nb >= 16) return few_go<T, 8, 1, kOctets, kMats, 2>(a, t, s);
+    return few_go<T, 4, 1, kOctets, kMats, 2>(a, t, s);
+}
+
+template <typename T, int kMats>
+hipError_t few_launch(const MmArgs& a, TimedLaunch t, hipStream_t s) {
+    if (a.n <= 8) return few_waves<T, 1, kMats>(a, t, s);
+    if (a.n <= 16) return few_waves<T, 2, kMats>(a, t, s);
+    if (a.n <= 24) return few_waves<T, 3, kMats>(a, t, s);
+    if (a.n <= 32) return few_waves<T, 4, kMats>(a, t, s);
+    if constexpr (kMats == 1) return few_waves<T, 8, kMats>(a, t, s);
+    return hipErrorInvalidValue;  // not reached: the gated block comes here with at most 32 tokens
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens: a workgroup computes kTM weight rows by kTN tokens, its waves
+// (kWM x kWN) a rectangle each.  One block of k (128 bytes a row) of both
+// operands is a stage; stages are copied from memory to LDS without passing
+// registers, kStages - 1 ahead of the one in use, one barrier a stage.
+//
+// A copy instruction of a wave places 64 x 16 bytes one after the other: eight
+// rows of 128 bytes.  The chunk c of row r is put at c ^ (r / 2 % 8) (each lane
+// chooses its source accordingly), so that the sixteen rows a fragment read
+// touches spread over all 64 banks.
+//
+// The gated form stages 128 gate rows and the same 128 up rows; every wave
+// holds both projections of its channels, and the workgroup holds whole blocks
+// of 128 of the result, which it writes in 8 bits.
+// ---------------------------------------------------------------------------
+struct TileArgs {
+    MmArgs m;
+    uint8_t* q;  // gated: the 8-bit result
+    float* qs;
+    int64_t ldq, ldqs;
+    unsigned mt, nt;  // tiles along the weight rows and the tokens
+    int wide;         // Y's lines may be stored 16 bytes at a time
+};
+
+constexpr int kXcd = 8;
+constexpr unsigned kBand = 8;  // tiles of weight rows that share their tokens before the next tokens
+
+// Workgroup id -> tile.  Workgroups go to the eight XCDs in turn; each XCD gets
+// a run of tiles, in bands of kBand tile rows, tokens outermost in a band, so
+// that the tiles it works on at a time share rows in its own L2.
+__device__ __forceinline__ void f8_tile_of(unsigned id, unsigned mt, unsigned nt, unsigned& mi, unsigned& ni) {
+    const unsigned tiles = mt * nt, per = tiles / kXcd, rest = tiles % kXcd;
+    const unsigned x = id % kXcd, i = id / kXcd;
+    const unsigned t = x * per + min(x, rest) + i;
+    const unsigned band = t / (kBand * nt), in = t % (kBand * nt);
+    const unsigned rows = min(kBand, mt - band * kBand);
+    mi = band * kBand + in % rows;
+    ni = in / rows;
+}
+
+template <typename T, int kTM, int kTN, int kWM, int kWN, int kStages, bool kGated, bool kHalf, bool kChannels>
+__global__ __launch_bounds__(kWM* kWN* kWave) void f8_tile_kernel(TileArgs a) {
+    constexpr int kWaves = kWM * kWN, kThreads = kWaves * kWave;
+    constexpr int kMt = kTM / kWM / 16, kNt = kTN / kWN / 16;
+    constexpr int kAi = kTM / 8 / kWaves, kBi = kTN / 8 / kWaves;  // copy instructions of a wave and stage
+    constexpr int kLoads = kAi + kBi + 1;                          // and one for the token scales
+    static_assert(kTM % (8 * kWaves) == 0 && kTN % (8 * kWaves) == 0 && kTN % 64 == 0, "whole copies");
+    static_assert(kTN / 64 <= kWaves && kWaves % (kTN / 64) == 0, "every wave copies one run of scales");
+    static_assert(!kGated || kTM == 256, "a gated tile holds one block of channels of both matrices");
+    static_assert(kStages >= 2 && kStages <= 4 && kMt >= 2 && kNt >= 2, "stages, tiles of a wave");
+    constexpr int kABytes = kTM * kF8Block, kBBytes = kTN * kF8Block, kBytes = kABytes + kBBytes + 4 * kTN;
+    // separate arrays: the compiler then knows that a read of one does not wait for copies into another
+    __shared__ __align__(16) uint8_t stage0[kBytes];
+    __shared__ __align__(16) uint8_t stage1[kBytes];
+    __shared__ __align__(16) uint8_t stage2[kStages > 2 ? kBytes : 16];
+    __shared__ __align__(16) uint8_t stage3[kStages > 3 ? kBytes : 16];
+
+    const MmArgs& m = a.m;
+    const int tid = threadIdx.x, lane = tid % kWave, w = wave_id();
+    const int wm = w / kWN, wn = w % kWN, l16 = lane % 16, kg = lane / 16;
+    unsigned mi, ni;
+    f8_tile_of(blockIdx.x, a.mt, a.nt, mi, ni);
+    constexpr int kRows = kGated ? kTM / 2 : kTM;  // rows of one matrix
+    const int64_t m0 = (int64_t)mi * kRows, t0 = (int64_t)ni * kTN;
+    const int rows = (int)min(m.M - m0, (int64_t)kRows), toks = (int)min(m.n - t0, (int64_t)kTN);
+    const int nb = m.nb;
+
+    const __amdgpu_buffer_rsrc_t rw = f8_rsrc(m.wq[0] + m0 * m.ldw, (uint32_t)((rows - 1) * m.ldw + nb * kF8Block));
+    const __amdgpu_buffer_rsrc_t ru =
+        kGated ? f8_rsrc(m.wq[1] + m0 * m.ldw, (uint32_t)((rows - 1) * m.ldw + nb * kF8Block)) : rw;
+    const __amdgpu_buffer_rsrc_t rx = f8_rsrc(m.xq + t0 * m.ldx, (uint32_t)((toks - 1) * m.ldx + nb * kF8Block));
+
+    // sources of this lane's copies: wave w copies rows 8 kAi w .. of A and 8 kBi w .. of B
+    uint32_t ao[kAi], bo[kBi];
+#pragma unroll
+    for (int i = 0; i < kAi; ++i) {
+        const int r = 8 * (kAi * w + i) + lane / 8, rr = kGated ? r % kRows : r;
+        ao[i] = rr < rows ? (uint32_t)(rr * m.ldw + 16 * ((lane % 8) ^ f8_swizzle(r))) : kF8Out;
+    }
+#pragma unroll
+    for (int i = 0; i < kBi; ++i) {
+        const int r = 8 * (kBi * w + i) + lane / 8;
+        bo[i] = r < toks ? (uint32_t)(r * m.ldx + 16 * ((lane % 8) ^ f8_swizzle(r))) : kF8Out;
+    }
+    const int sr = 64 * (w % (kTN / 64));  // this wave's run of token scales
+    const uint32_t so = sr + lane < toks ? (uint32_t)(4 * (sr + lane)) : kF8Out;
+    const bool up = kGated && w >= kWaves / 2;  // rows of the up matrix (whole waves)
+
+    // copy c of the wave's kLoads into stage st: block b of k (past the last block, that one again, never used)
+    auto copy = [&](uint8_t* st, int b, int c) {
+        b = min(b, nb - 1);
+        const uint32_t ko = (uint32_t)(b * kF8Block);
+        if (c < kAi) copy16(up ? ru : rw, st + 1024 * (kAi * w + c), ao[c < kAi ? c : 0], ko);
+        else if (c < kAi + kBi) copy16(rx, st + kABytes + 1024 * (kBi * w + c - kAi), bo[c < kAi + kBi ? c - kAi : 0], ko);
+        else {
+            const __amdgpu_buffer_rsrc_t rs = f8_rsrc(m.xs + b * m.ldxs + t0, (uint32_t)(4 * toks));
+            copy4(rs, reinterpret_cast<float*>(st + kABytes + kBBytes) + sr, so, 0);
+        }
+    };
+
+    float4v acc[kMt][kNt];
+#pragma unroll
+    for (int i = 0; i < kMt; ++i)
+#pragma unroll
+        for (int j = 0; j < kNt; ++j) acc[i][j] = (float4v){};
+
+    constexpr int kWaveRows = kTM / kWM;
+    // weight scales: a wave's rows lie in one block of 128 of each matrix
+    const int64_t ob = kGated ? mi : (m0 + wm * kWaveRows) / kF8Block;
+    const bool live = kGated || m0 + wm * kWaveRows < m.M;
+    const float* wsr = m.ws[0] + (live ? ob : 0) * m.ldws;
+    const float* usr = kGated ? m.ws[1] + ob * m.ldws : nullptr;
+
+    auto row_of = [&](int i) {  // first row of the wave's m-tile i in the stage
+        if (!kGated) return wm * kWaveRows + 16 * i;
+        return i < kMt / 2 ? wm * (kRows / kWM) + 16 * i : kRows + wm * (kRows / kWM) + 16 * (i - kMt / 2);
+    };
+    const int swz0 = 16 * ((2 * kg) ^ f8_swizzle(l16)), swz1 = 16 * ((2 * kg + 1) ^ f8_swizzle(l16));
+    auto fragment = [&](const uint8_t* p, int row) { return f8_fragment(p + row * kF8Block, l16, swz0, swz1); };
+
+    // What a step starts with, read from its stage while the step before ends:
+    // the token fragments, the first weight fragment and the token scales.
+    constexpr int kMats = kGated ? 2 : 1, kPer = kChannels ? 4 : 1;  // a lane holds one token, or four of a channel
+    typedef typename Operand<kHalf>::type op_t;
+    op_t bf[kNt];
+    int8v raw;
+    float sx[kNt][kPer];
+    auto read_scales = [&](const uint8_t* st) {
+        const float* S = reinterpret_cast<const float*>(st + kABytes + kBBytes);
+#pragma unroll
+        for (int j = 0; j < kNt; ++j)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) sx[j][e] = S[(wn * kNt + j) * 16 + (kChannels ? 4 * kg + e : l16)];
+    };
+    // products that are still to be scaled and added: two MFMAs old when that
+    // happens, the last two of a step in the next one
+    float4v late[2];
+    float late_s[2][kPer];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        late[e] = (float4v){};
+#pragma unroll
+        for (int v = 0; v < kPer; ++v) late_s[e][v] = 0.0f;
+    }
+    auto add = [&](float4v& to, const float4v& p, const float (&s)[kPer]) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) to[v] = fmaf(p[v], s[kChannels ? v : 0], to[v]);
+    };
+
+    constexpr int kPerTile = 2;  // copies issued with the barrier and with each m-tile after it, all before the last
+    constexpr int kPre = kPerTile;
+    constexpr int kAhead = kStages - 1;
+
+    // One block of k, from stage st.  Copies go to the block kAhead later, whose
+    // stage `to` was free at the last barrier.  Before the last m-tile, with
+    // every fragment of st in registers, the waves meet: the next stage `nx`
+    // has landed for all of them, and st may be copied over.
+    auto step = [&](uint8_t* st, uint8_t* nx, uint8_t* to, int b, float sw, float su) {
+        float sc[kMats][kNt][kPer];
+        if (kChannels) read_scales(st);
+#pragma unroll
+        for (int j = 0; j < kNt; ++j)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                sc[0][j][e] = sx[j][e] * sw;
+                if (kGated) sc[kMats - 1][j][e] = sx[j][e] * su;
+            }
+        int8v nraw[kNt];
+#pragma unroll
+        for (int i = 0; i < kMt; ++i) {
+            const op_t af = Operand<kHalf>::of(raw);
+            if (i + 1 < kMt) {
+                raw = fragment(st, row_of(i + 1));
+                constexpr int kLast = kMt - 2;
+#pragma unroll
+                for (int c = 0; c < kLoads; ++c)
+                    if (c >= kPre && (i == kLast ? c >= kPre + i * kPerTile
+                                                 : c >= kPre + i * kPerTile && c < kPre + (i + 1) * kPerTile))
+                        copy(to, b + kAhead, c);
+            } else {
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kAhead - 1) * kLoads) : "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+#pragma unroll
+                for (int j = 0; j < kNt; ++j) nraw[j] = fragment(nx + kABytes, (wn * kNt + j) * 16);
+                raw = fragment(nx, row_of(0));
+                if (!kChannels) read_scales(nx);  // four times as many: too many registers to hold ahead
+#pragma unroll
+                for (int c = 0; c < kPre; ++c) copy(st, b + 1 + kAhead, c);
+            }
+#pragma unroll
+            for (int j = 0; j < kNt; ++j) {
+                const float4v p = kChannels ? block_product(bf[j], af) : block_product(af, bf[j]);
+                const int g = kGated && i >= kMt / 2 ? kMats - 1 : 0;
+                const int q = i * kNt + j;
+                // the one two back: of this step or, for its first two, of the step before
+                add(q >= 2 ? acc[(q - 2) / kNt][(q - 2) % kNt] : acc[kMt - 1][kNt - 2 + q], late[q % 2], late_s[q % 2]);
+                late[q % 2] = p;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) late_s[q % 2][e] = sc[g][j][e];
+                if (i == kMt - 1) bf[j] = Operand<kHalf>::of(nraw[j]);
+            }
+            __builtin_amdgcn_sched_barrier(0);  // left alone, the scheduler reads every fragment first and spills
+        }
+    };
+    if (nb > 0) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d)
+#pragma unroll
+            for (int c = 0; c < kLoads; ++c) copy(d == 0 ? stage0 : d == 1 ? stage1 : stage2, d, c);
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kAhead - 1) * kLoads) : "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        uint8_t* const last = kStages == 2 ? stage1 : kStages == 3 ? stage2 : stage3;
+#pragma unroll
+        for (int j = 0; j < kNt; ++j) bf[j] = Operand<kHalf>::of(fragment(stage0 + kABytes, (wn * kNt + j) * 16));
+        raw = fragment(stage0, row_of(0));
+        read_scales(stage0);
+#pragma unroll
+        for (int c = 0; c < kPre; ++c) copy(last, kAhead, c);
+
+        // the weight scales of kRun blocks at a time, one a lane
+        constexpr int kMany = 64 / kStages * kStages;
+        for (int b0 = 0; b0 < nb; b0 += kMany) {
+            const int run = min(kMany, nb - b0);
+            const int at = b0 + min(lane, run - 1);
+            const int wl = __builtin_bit_cast(int, wsr[at]);
+            const int ul = kGated ? __builtin_bit_cast(int, usr[at]) : 0;
+            auto go = [&](uint8_t* st, uint8_t* nx, uint8_t* to, int b) {
+                step(st, nx, to, b0 + b, __builtin_bit_cast(float, __builtin_amdgcn_readlane(wl, b)),
+                     kGated ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(ul, b)) : 0.0f);
+            };
+            uint8_t* const after0 = stage1;
+            uint8_t* const after1 = kStages > 2 ? stage2 : stage0;
+            uint8_t* const after2 = kStages > 3 ? stage3 : stage0;
+            // no branch between the steps of the loop: the compiler would move
+            // the scaling of products past it and keep them all in registers
+            int b = 0;
+            for (; b + kStages <= run; b += kStages) {
+                go(stage0, after0, last, b);
+                go(stage1, after1, stage0, b + 1);
+                if (kStages > 2) go(stage2, after2, stage1, b + 2);
+                if (kStages > 3) go(stage3, stage0, stage2, b + 3);
+            }
+            if (b < run) go(stage0, after0, last, b);
+            if (kStages > 2 && b + 1 < run) go(stage1, after1, stage0, b + 1);
+            if (kStages > 3 && b + 2 < run) go(stage2, after2, stage1, b + 2);
+        }
+        add(acc[kMt - 1][kNt - 2], late[0], late_s[0]);
+        add(acc[kMt - 1][kNt - 1], late[1], late_s[1]);
+    }
+    // copies still in flight would land in memory that the epilogue (or the
+    // next workgroup) uses
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+
+    if (kGated) {
+        uint32_t* peaks = reinterpret_cast<uint32_t*>(stage1);  // [kWM][kTN]
+        uint32_t* codes = reinterpret_cast<uint32_t*>(stage0);  // [kTN][kCodePitch]
+        constexpr int kCodePitch = kF8Block / 4 + 1;
+        static_assert(4 * kTN * kCodePitch <= kABytes + kBBytes && 4 * kWM * kTN <= kABytes, "epilogue's LDS");
+        uint32_t pk[kNt];
+#pragma unroll
+        for (int j = 0; j < kNt; ++j) {
+            pk[j] = 0;
+#pragma unroll
+            for (int i = 0; i < kMt / 2; ++i)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    acc[i][j][v] = gated(acc[i][j][v], acc[i + kMt / 2][j][v]);
+                    pk[j] = max(pk[j], abs_bits(acc[i][j][v]));
+                }
+            pk[j] = max(pk[j], (uint32_t)__shfl_xor((int)pk[j], 16, kWave));
+            pk[j] = max(pk[j], (uint32_t)__shfl_xor((int)pk[j], 32, kWave));
+            if (kg == 0) peaks[wm * kTN + (wn * kNt + j) * 16 + l16] = pk[j];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kNt; ++j) {
+            const int t = (wn * kNt + j) * 16 + l16;
+            uint32_t p = 0;
+#pragma unroll
+            for (int g = 0; g < kWM; ++g) p = max(p, peaks[g * kTN + t]);
+            const float s = f8_scale(p), inv = 1.0f / s;
+            if (wm == 0 && kg == 0 && t < toks) a.qs[(int64_t)mi * a.ldqs + t0 + t] = s;
+#pragma unroll
+            for (int i = 0; i < kMt / 2; ++i)
+                codes[t * kCodePitch + (wm * (kRows / kWM) + 16 * i) / 4 + kg] =
+                    f8_pack4(acc[i][j][0] * inv, acc[i][j][1] * inv, acc[i][j][2] * inv, acc[i][j][3] * inv);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kTN * 8 / kThreads; ++i) {
+            const int t = (i * kThreads + tid) / 8, c = 4 * (tid % 8);
+            const uint32_t* r = codes + t * kCodePitch + c;
+            if (t < toks)
+                *reinterpret_cast<uint4v*>(a.q + (t0 + t) * a.ldq + m0 + 4 * c) = (uint4v){r[0], r[1], r[2], r[3]};
+        }
+        return;
+    }
+    // A lane holds four neighbours of sixteen lines of Y (a line: one token's
+    // rows, or one channel's tokens).  A wave turns sixteen lines at a time in
+    // LDS of its own and stores whole runs of them.
+    constexpr int kRun = kChannels ? 16 * kNt : 16 * kMt, kOuter = kChannels ? kMt : kNt, kInner = kChannels ? kNt : kMt;
+    constexpr int kPitch = kRun * (int)sizeof(T) + 16, kVec = 16 / (int)sizeof(T);
+    static_assert(kGated || kWaves * 16 * kPitch <= kBytes, "the lines of every wave in the first stage");
+    uint8_t* lines = stage0 + w * 16 * kPitch;
+    T* y = static_cast<T*>(m.y);
+    const int first = kChannels ? wn * kRun : wm * kRun;           // of the run, within the tile
+    const int left = (kChannels ? toks : rows) - first;            // of the run, within Y
+    const int64_t at0 = (kChannels ? t0 : m0) + first;
+#pragma unroll
+    for (int o = 0; o < kOuter; ++o) {
+#pragma unroll
+        for (int k = 0; k < kInner; ++k) {
+            const float4v& v = acc[kChannels ? o : k][kChannels ? k : o];
+            struct alignas(4 * sizeof(T)) { T e[4]; } out;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out.e[e] = (T)relu_if(v[e], m.relu);
+            *reinterpret_cast<decltype(out)*>(lines + l16 * kPitch + (16 * k + 4 * kg) * sizeof(T)) = out;
+        }
+        __builtin_amdgcn_wave_barrier();
+        const int line0 = kChannels ? wm * kWaveRows + 16 * o : (wn * kNt + o) * 16;
+        const int count = (kChannels ? rows : toks) - line0;       // lines within Y
+        T* base = y + ((kChannels ? m0 : t0) + line0) * m.ldy + at0;
+        if (a.wide) {
+            constexpr int kPer = kRun / kVec;
+#pragma unroll
+            for (int q = 0; q < 16 * kPer / kWave; ++q) {
+                const int line = (q * kWave + lane) / kPer, at = (q * kWave + lane) % kPer * kVec;
+                const uint4v v = *reinterpret_cast<const uint4v*>(lines + line * kPitch + at * sizeof(T));
+                if (line >= count) continue;
+                if (at + kVec <= left) *reinterpret_cast<uint4v*>(base + line * m.ldy + at) = v;
+                else {
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e)
+                        if (at + e < left) base[line * m.ldy + at + e] = reinterpret_cast<const T*>(&v)[e];
+                }
+            }
+        } else {
+            for (int q = 0; q < 16 * kRun / kWave; ++q) {
+                const int line = (q * kWave + lane) / kRun, at = (q * kWave + lane) % kRun;
+                if (line < count && at < left)
+                    base[line * m.ldy + at] = *reinterpret_cast<const T*>(lines + line * kPitch + at * sizeof(T));
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+template <typename T, int kTM, int kTN, int kWM, int kWN, int kStages, bool kGated, bool kHalf>
+hipError_t tile_launch(TileArgs a, TimedLaunch t, hipStream_t s) {
+    constexpr int kRows = kGated ? kTM / 2 : kTM;
+    a.mt = (unsigned)((a.m.M + kRows - 1) / kRows);
+    a.nt = (unsigned)((a.m.n + kTN - 1) / kTN);
+    a.wide = a.m.ldy * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(a.m.y) % 16 == 0;
+    const dim3 grid(a.mt * a.nt), block(kWM * kWN * kWave);
+    if (!kGated && a.m.channel_major)
+        GPTQ_LAUNCH(t, (f8_tile_kernel<T, kTM, kTN, kWM, kWN, kStages, kGated, kHalf, !kGated>), grid, block, 0, s, a);
+    else
+        GPTQ_LAUNCH(t, (f8_tile_kernel<T, kTM, kTN, kWM, kWN, kStages, kGated, kHalf, false>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+constexpr int64_t kFewTokens = 32;      // the few-token kernel up to here,
+constexpr int64_t kSomeTokens = 64;     // and up to here for weights of few rows
+
+// Few tokens or many?  The tile kernel at its smallest tile against the
+// few-token one, us on 4096 x 4096, 11008 (k) x 4096 and 4096 x 11008 weights:
+// 32 tokens 12.0, 30 and 12.5 against 6.8, 11.9 and 13.0; 64 tokens 12.3, 30
+// and 13.0 against 9.5, 17.4 and 19.9.
+bool f8_few(int64_t n, int64_t M) { return n <= kFewTokens || (n <= kSomeTokens && M <= 8192); }
+
+// The tile by what a product's blocks of k take: rounds of tiles over the CUs
+// times the measured time of a round and block.  us a block with every CU at
+// work: e4m3 MFMA 256 x 256 2.0, 256 x 128 1.2, 128 x 128 0.71, 64 x 64 0.40
+// (one a CU), 0.54 (two), 0.80 (three); float16 MFMA 256 x 128 2.1, 128 x 128
+// 1.44 (one a CU), 2.3 (two), 64 x 64 0.60, 0.90, 1.45.  At 4096 x 4096
+// weights, e4m3: 256 tokens 13.0 us in 64 x 64 tiles, 29 in 256 x 128; 1024
+// tokens 23 in 128 x 128, 31 in both neighbours; 4096 tokens 66 in 256 x 256,
+// 76 in 256 x 128, 112 in 64 x 64.
+template <typename T, bool kHalf>
+hipError_t matmul_typed(const MmArgs& m, hipStream_t s) {
+    TimedLaunch t(K_F8_MATMUL, s);
+    if (f8_few(m.n, m.M)) return few_launch<T, 1>(m, t, s);
+    TileArgs a = {};
+    a.m = m;
+    const int64_t cus = device_cu_count();
+    if (cus <= 0) return hipErrorInvalidDevice;
+    auto rounds = [&](int64_t tm, int64_t tn, int64_t each) {
+        return (((m.M + tm - 1) / tm) * ((m.n + tn - 1) / tn) + cus * each - 1) / (cus * each);
+    };
+    const bool one = rounds(64, 64, 1) == 1, two = rounds(64, 64, 2) == 1;
+    if constexpr (kHalf) {
+        const double t64 = one ? 0.60 : two ? 0.90 : 1.45 * rounds(64, 64, 3);
+        const double t128 = rounds(128, 128, 1) == 1 ? 1.44 : 2.3 * rounds(128, 128, 2);
+        const double t256 = 2.1 * rounds(256, 128, 1);
+        if (t64 <= t128 && t64 <= t256) return tile_launch<T, 64, 64, 2, 2, 3, false, true>(a, t, s);
+        if (t128 <= t256) return tile_launch<T, 128, 128, 2, 2, 2, false, true>(a, t, s);
+        return tile_launch<T, 256, 128, 4, 2, 2, false, true>(a, t, s);
+    } else {
+        const double t64 = one ? 0.40 : two ? 0.54 : 0.80 * rounds(64, 64, 3);
+        const double t128 = 0.71 * rounds(128, 128, 1), t256 = 1.2 * rounds(256, 128, 1), t512 = 2.0 * rounds(256, 256, 1);
+        if (t64 <= t128 && t64 <= t256 && t64 <= t512) return tile_launch<T, 64, 64, 2, 2, 3, false, false>(a, t, s);
+        if (t128 <= t256 && t128 <= t512) return tile_launch<T, 128, 128, 4, 2, 3, false, false>(a, t, s);
+        if (t256 <= t512) return tile_launch<T, 256, 128, 4, 2, 3, false, false>(a, t, s);
+        return tile_launch<T, 256, 256, 2, 4, 2, false, false>(a, t, s);
+    }
+}
 
 }  // namespace
 
 hipError_t launch_f8_matmul(const F8Product& c, int y_dtype, hipStream_t s) {
     MmArgs a = {{c.wq[0], nullptr}, {c.ws[0], nullptr}, c.xq, c.xs, c.y, c.ldw, c.ldws, c.ldx, c.ldxs, c.ldy, c.M, c.n,
                 (int)((c.K + kF8Block - 1) / kF8Block), c.channel_major, c.relu};
-    TimedLaunch t(K_F8_MATMUL, s);
-    if (y_dtype == 0) return few_launch<half_t, 1>(a, t, s);
-    if (y_dtype == 1) return few_launch<float, 1>(a, t, s);
-    return few_launch<bf16_t, 1>(a, t, s);
+    if (y_dtype == 0) return matmul_typed<half_t, false>(a, s);
+    if (y_dtype == 1) return matmul_typed<float, true>(a, s);
+    return matmul_typed<bf16_t, false>(a, s);
 }
 
 size_t f8_gated_workspace_bytes(int64_t n, int64_t d_ff) {
+    if (n > kFewTokens) return 0;
     return (size_t)(n * ((d_ff + kF8Block - 1) / kF8Block) * kF8Block) * sizeof(float);
 }
 
+// Up to 32 tokens: the few-token kernel leaves the products in float32 and the
+// activations' quantizer writes them in 8 bits (11008 channels, 32 tokens: 26
+// us, the tile kernel 36; 64 tokens: 37 against 36).  More: the tile kernel,
+// 64 tokens wide while that leaves CUs idle (128 tokens 39 us against 60 us
+// 128 wide; 256 tokens 69 against 61).
 hipError_t launch_f8_gated(const F8Product& c, uint8_t* q, int64_t ldq, float* scales, int64_t lds, void* ws,
                            hipStream_t s) {
+    if (c.n > kFewTokens) {
+        TileArgs t = {};
+        t.m = {{c.wq[0], c.wq[1]}, {c.ws[0], c.ws[1]}, c.xq, c.xs, nullptr, c.ldw, c.ldws, c.ldx, c.ldxs, 0, c.M, c.n,
+               (int)((c.K + kF8Block - 1) / kF8Block), 0, 0};
+        t.q = q;
+        t.qs = scales;
+        t.ldq = ldq;
+        t.ldqs = lds;
+        const TimedLaunch k(K_F8_GATED, s);
+        if (((c.M + kF8Block - 1) / kF8Block) * ((c.n + 63) / 64) <= device_cu_count())
+            return tile_launch<float, 256, 64, 4, 2, 3, true, true>(t, k, s);
+        return tile_launch<float, 256, 128, 4, 2, 2, true, true>(t, k, s);
+    }
     const int64_t ldh = (c.M + kF8Block - 1) / kF8Block * kF8Block;
     MmArgs a = {{c.wq[0], c.wq[1]}, {c.ws[0], c.ws[1]}, c.xq, c.xs, ws, c.ldw, c.ldws, c.ldx, c.ldxs, ldh, c.M, c.n,
                 (int)((c.K + kF8Block - 1) / kF8Block), 0, 0};

@@ -91,6 +91,7 @@ def test_matmul_refusals(clib):
     for bad in (dict(wq=ODD), dict(xq=ODD), dict(ldw=264), dict(ldx=264), dict(ldw=big), dict(ldx=big),
                 dict(m=(1 << 24) + 1, ldy=1 << 25), dict(n=(1 << 24) + 1, ldxs=1 << 25)):
         assert mm(clib, **bad) == EUNSUPPORTED, bad
+    assert mm(clib, m=1 << 24, n=1 << 24, ldy=1 << 24, ldxs=1 << 24) == EUNSUPPORTED
     assert mm(clib, n=0, wq=None, ws=None, xq=None, xs=None, Y=None) == OK
     assert mm(clib, m=0, wq=None, ws=None, xq=None, xs=None, Y=None) == OK
 
