@@ -321,151 +321,171 @@ def obq_quantize(W, U, dead, bits: int, codes, scales, zeros, order=None, loss=N
 # 8-bit operands: e4m3 values [rows, ld] (ld a multiple of 16, zeros behind
 # the columns up to a multiple of 128) and float32 scales, as include/gptq.h
 # lays them out.  `values` may be float8_e4m3fn or uint8.
+#
+# One decoded token's kernel takes 3 to 6 us, so these calls are written to
+# cost the host less: tensors are read once each, by the accessors that do not
+# build new objects.
 # ---------------------------------------------------------------------------
-def _fp8_dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return GPTQ_BF16
-    return _dtype_code(t)
+_fp8_torch = None  # set by the first call: (type codes, 8-bit types, float32, current device, its current stream)
 
 
-def _fp8_where(device, stream):
-    """The stream to enqueue on: the given one, or the current one of
-    ``device`` (which the library's launches need to be the current device)."""
+def _fp8_types():
+    global _fp8_torch
     import torch
-    if torch.cuda.current_device() != device.index:
-        raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
+    _fp8_torch = ({torch.float16: GPTQ_F16, torch.float32: GPTQ_F32, torch.bfloat16: GPTQ_BF16},
+                  (torch.float8_e4m3fn, torch.uint8), torch.float32, torch._C._cuda_getDevice,
+                  torch._C._cuda_getCurrentRawStream)
+    return _fp8_torch
+
+
+def _fp8_dtype(t) -> int:
+    code = (_fp8_torch or _fp8_types())[0].get(t.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    return code
+
+
+def _fp8_device(t) -> int:
+    """Index of the device of ``t``, which has to be the current one (the
+    library launches there)."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("device tensor expected")
+    current = (_fp8_torch or _fp8_types())[3]()
+    if dev != current:
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{current}")
+    return dev
+
+
+def _fp8_stream(dev: int, stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    if stream.device != device:
-        raise ValueError(f"tensors on {device}, stream on {stream.device}")
+        return (_fp8_torch or _fp8_types())[4](dev)
+    if stream.device.index != dev:
+        raise ValueError(f"tensors on cuda:{dev}, stream on {stream.device}")
     return stream.cuda_stream
 
 
-def _fp8_matrix(t, device, what: str):
-    """(pointer, row stride) of a 2-D device view with unit column stride."""
-    if t.dim() != 2 or t.device != device or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} must be a 2-D view on {device} with unit column stride")
-    return t.data_ptr(), _row_stride(t)
-
-
-def _row_stride(t) -> int:
+def _fp8_matrix(t, dev: int, what: str):
+    """(pointer, row stride, rows, columns) of a 2-D view on device ``dev``
+    with unit column stride."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or t.get_device() != dev or (stride[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{what} must be a 2-D view on cuda:{dev} with unit column stride")
+    rows, cols = shape
     # the stride of a single row is never used, and torch leaves it arbitrary
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return t.data_ptr(), stride[0] if rows > 1 else max(stride[0], cols), rows, cols
 
 
-def _fp8_operand(values, scales, cols: int, lead: int, along: int, device, what: str):
-    """(values pointer, ld, scales pointer, lds), with the layout checked."""
-    import torch
-    if values.dtype != torch.float8_e4m3fn and values.dtype != torch.uint8:
-        raise ValueError(f"{what}: values must be float8_e4m3fn")
-    if scales.dtype != torch.float32:
-        raise ValueError(f"{what}: scales must be float32")
-    vp, ld = _fp8_matrix(values, device, what)
-    sp, lds = _fp8_matrix(scales, device, what)
-    if values.shape[1] < (cols + 127) // 128 * 128:
-        raise ValueError(f"{what}: {values.shape[1]} stored columns hold fewer than {cols} rounded up to 128")
-    if scales.shape[0] < lead or scales.shape[1] < along:
-        raise ValueError(f"{what}: scales {tuple(scales.shape)}, expected [{lead}, {along}]")
-    return vp, ld, sp, lds
-
-
-def _blocks(d: int) -> int:
-    return (d + 127) // 128
-
-
-def _device_of(t):
-    if not t.is_cuda:
-        raise ValueError("device tensor expected")
-    return t.device
+def _fp8_operand(values, scales, cols: int, by_row: bool, dev: int, what: str):
+    """(values pointer, ld, scales pointer, lds, rows) of an 8-bit matrix of
+    ``cols`` columns: a scale per row and 128 columns (``by_row``), or per 128
+    x 128 block."""
+    _, eights, f32, _, _ = _fp8_torch or _fp8_types()
+    if values.dtype not in eights or scales.dtype != f32:
+        raise ValueError(f"{what}: values must be float8_e4m3fn, scales float32")
+    vp, ld, rows, held = _fp8_matrix(values, dev, what)
+    sp, lds, lead, along = _fp8_matrix(scales, dev, what)
+    nb = (cols + 127) >> 7
+    if held < nb << 7:
+        raise ValueError(f"{what}: {held} stored columns hold fewer than {cols} rounded up to 128")
+    if (lead < nb or along < rows) if by_row else (lead < (rows + 127) >> 7 or along < nb):
+        raise ValueError(f"{what}: scales {(lead, along)} for {rows} x {cols}")
+    return vp, ld, sp, lds, rows
 
 
 def fp8_weight(W, values, scales, stream=None) -> None:
     """``W [d_out, d_in]`` to 8 bits, a scale per 128 x 128 block."""
-    dev = _device_of(W)
-    wp, ldw = _fp8_matrix(W, dev, "W")
-    d_out, d_in = W.shape
-    if values.shape[0] != d_out:
+    dev = _fp8_device(W)
+    wp, ldw, d_out, d_in = _fp8_matrix(W, dev, "W")
+    vp, ld, sp, lds, rows = _fp8_operand(values, scales, d_in, False, dev, "out")
+    if rows != d_out:
         raise ValueError("rows of the output")
-    vp, ld, sp, lds = _fp8_operand(values, scales, d_in, _blocks(d_out), _blocks(d_in), dev, "out")
-    _check("gptq_fp8_weight", load().gptq_fp8_weight(wp, _fp8_dtype_code(W), d_out, d_in, ldw, vp, ld, sp, lds,
-                                                     _fp8_where(dev, stream)))
+    rc = load().gptq_fp8_weight(wp, _fp8_dtype(W), d_out, d_in, ldw, vp, ld, sp, lds, _fp8_stream(dev, stream))
+    if rc:
+        _check("gptq_fp8_weight", rc)
 
 
 def fp8_activations(X, values, scales, channel_major: bool = False, stream=None) -> None:
     """``X [n, d]`` (or ``[d, n]`` with ``channel_major``) to 8 bits, a scale
     per token and 128 channels."""
-    dev = _device_of(X)
-    xp, ldx = _fp8_matrix(X, dev, "X")
-    n, d = (X.shape[1], X.shape[0]) if channel_major else X.shape
-    if values.shape[0] != n:
+    dev = _fp8_device(X)
+    xp, ldx, n, d = _fp8_matrix(X, dev, "X")
+    if channel_major:
+        n, d = d, n
+    vp, ld, sp, lds, rows = _fp8_operand(values, scales, d, True, dev, "out")
+    if rows != n:
         raise ValueError("rows of the output")
-    vp, ld, sp, lds = _fp8_operand(values, scales, d, _blocks(d), n, dev, "out")
-    _check("gptq_fp8_activations",
-           load().gptq_fp8_activations(xp, _fp8_dtype_code(X), n, d, ldx, int(bool(channel_major)), vp, ld, sp, lds,
-                                       _fp8_where(dev, stream)))
+    rc = load().gptq_fp8_activations(xp, _fp8_dtype(X), n, d, ldx, 1 if channel_major else 0, vp, ld, sp, lds,
+                                     _fp8_stream(dev, stream))
+    if rc:
+        _check("gptq_fp8_activations", rc)
 
 
 def fp8_rms_norm(x, gain, eps: float, values, scales, residual=None, sum_out=None, stream=None) -> None:
     """``h = x + residual``; ``h / sqrt(mean(h^2) + eps) * gain`` to 8 bits;
     ``sum_out = h``."""
-    dev = _device_of(x)
-    xp, ldx = _fp8_matrix(x, dev, "x")
-    n, d = x.shape
+    dev = _fp8_device(x)
+    xp, ldx, n, d = _fp8_matrix(x, dev, "x")
+    kind, shape = x.dtype, x.shape
     rp, ldr, op, ldo = None, 0, None, 0
     if residual is not None:
-        rp, ldr = _fp8_matrix(residual, dev, "residual")
-        if residual.shape != x.shape or residual.dtype != x.dtype:
+        if residual.shape != shape or residual.dtype != kind:
             raise ValueError("residual must have the shape and type of x")
+        rp, ldr, _, _ = _fp8_matrix(residual, dev, "residual")
     if sum_out is not None:
-        op, ldo = _fp8_matrix(sum_out, dev, "sum_out")
-        if sum_out.shape != x.shape or sum_out.dtype != x.dtype:
+        if sum_out.shape != shape or sum_out.dtype != kind:
             raise ValueError("sum_out must have the shape and type of x")
-    if gain.shape != (d,) or gain.dtype != x.dtype or gain.device != dev or not gain.is_contiguous():
+        op, ldo, _, _ = _fp8_matrix(sum_out, dev, "sum_out")
+    if gain.shape != shape[1:] or gain.dtype != kind or gain.get_device() != dev or not gain.is_contiguous():
         raise ValueError("gain must be a contiguous vector of x's type, one value per channel")
-    if values.shape[0] != n:
+    vp, ld, sp, lds, rows = _fp8_operand(values, scales, d, True, dev, "out")
+    if rows != n:
         raise ValueError("rows of the output")
-    vp, ld, sp, lds = _fp8_operand(values, scales, d, _blocks(d), n, dev, "out")
-    _check("gptq_fp8_rms_norm",
-           load().gptq_fp8_rms_norm(xp, ldx, rp, ldr, op, ldo, gain.data_ptr(), _fp8_dtype_code(x), n, d, float(eps),
-                                    vp, ld, sp, lds, _fp8_where(dev, stream)))
+    rc = load().gptq_fp8_rms_norm(xp, ldx, rp, ldr, op, ldo, gain.data_ptr(), _fp8_dtype(x), n, d, eps, vp, ld, sp,
+                                  lds, _fp8_stream(dev, stream))
+    if rc:
+        _check("gptq_fp8_rms_norm", rc)
 
 
 def fp8_matmul(wq, ws, xq, xs, d_in: int, Y, channel_major: bool = False, activation: int = 0, stream=None) -> None:
     """``Y = act(X W^T)`` of 8-bit operands; ``Y [n, d_out]``, or ``[d_out,
     n]`` with ``channel_major``; activation 0 none, 1 ReLU."""
-    dev = _device_of(Y)
-    yp, ldy = _fp8_matrix(Y, dev, "Y")
-    d_out, n = wq.shape[0], xq.shape[0]
-    wp, ldw, wsp, ldws = _fp8_operand(wq, ws, d_in, _blocks(d_out), _blocks(d_in), dev, "weights")
-    xp, ldx, xsp, ldxs = _fp8_operand(xq, xs, d_in, _blocks(d_in), n, dev, "activations")
-    if Y.shape != ((d_out, n) if channel_major else (n, d_out)):
+    dev = _fp8_device(Y)
+    yp, ldy, y0, y1 = _fp8_matrix(Y, dev, "Y")
+    wp, ldw, wsp, ldws, d_out = _fp8_operand(wq, ws, d_in, False, dev, "weights")
+    xp, ldx, xsp, ldxs, n = _fp8_operand(xq, xs, d_in, True, dev, "activations")
+    if (y0 != d_out or y1 != n) if channel_major else (y0 != n or y1 != d_out):
         raise ValueError("shape of Y")
-    _check("gptq_fp8_matmul",
-           load().gptq_fp8_matmul(wp, ldw, wsp, ldws, d_out, d_in, xp, ldx, xsp, ldxs, n, yp, _fp8_dtype_code(Y), ldy,
-                                  int(bool(channel_major)), int(activation), _fp8_where(dev, stream)))
+    rc = load().gptq_fp8_matmul(wp, ldw, wsp, ldws, d_out, d_in, xp, ldx, xsp, ldxs, n, yp, _fp8_dtype(Y), ldy,
+                                1 if channel_major else 0, activation, _fp8_stream(dev, stream))
+    if rc:
+        _check("gptq_fp8_matmul", rc)
 
 
 def fp8_gated_workspace(n: int, d_ff: int) -> int:
-    return int(load().gptq_fp8_gated_workspace(n, d_ff))
+    return load().gptq_fp8_gated_workspace(n, d_ff)
 
 
 def fp8_gated(gq, gs, uq, us, xq, xs, d_in: int, values, scales, workspace=None, stream=None) -> None:
     """``silu(X G^T) * (X U^T)`` of 8-bit operands, written in 8 bits."""
-    dev = _device_of(values)
-    d_ff, n = gq.shape[0], xq.shape[0]
-    gp, ldw, gsp, ldws = _fp8_operand(gq, gs, d_in, _blocks(d_ff), _blocks(d_in), dev, "gate")
-    up, ldu, usp, ldus = _fp8_operand(uq, us, d_in, _blocks(d_ff), _blocks(d_in), dev, "up")
-    if uq.shape[0] != d_ff or (d_ff > 1 and ldu != ldw) or (ldus != ldws and d_ff > 128):
+    dev = _fp8_device(values)
+    gp, ldw, gsp, ldws, d_ff = _fp8_operand(gq, gs, d_in, False, dev, "gate")
+    up, ldu, usp, ldus, up_rows = _fp8_operand(uq, us, d_in, False, dev, "up")
+    if up_rows != d_ff or (ldu != ldw and d_ff > 1) or (ldus != ldws and d_ff > 128):
         raise ValueError("gate and up must have one shape and strides")
-    xp, ldx, xsp, ldxs = _fp8_operand(xq, xs, d_in, _blocks(d_in), n, dev, "activations")
-    if values.shape[0] != n:
+    xp, ldx, xsp, ldxs, n = _fp8_operand(xq, xs, d_in, True, dev, "activations")
+    vp, ld, sp, lds, rows = _fp8_operand(values, scales, d_ff, True, dev, "out")
+    if rows != n:
         raise ValueError("rows of the output")
-    vp, ld, sp, lds = _fp8_operand(values, scales, d_ff, _blocks(d_ff), n, dev, "out")
-    _check("gptq_fp8_gated",
-           load().gptq_fp8_gated(gp, gsp, up, usp, ldw, ldws, d_ff, d_in, xp, ldx, xsp, ldxs, n, vp, ld, sp, lds,
-                                 _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None
-                                 else 0, _fp8_where(dev, stream)))
+    room = 0
+    if workspace is not None:
+        if workspace.get_device() != dev:
+            raise ValueError("workspace on another device")
+        room = workspace.numel() * workspace.element_size()
+    rc = load().gptq_fp8_gated(gp, gsp, up, usp, ldw, ldws, d_ff, d_in, xp, ldx, xsp, ldxs, n, vp, ld, sp, lds,
+                               _ptr(workspace), room, _fp8_stream(dev, stream))
+    if rc:
+        _check("gptq_fp8_gated", rc)
 
 
 # ---------------------------------------------------------------------------

@@ -238,10 +238,10 @@ def fp8_rms_norm(x, gain, eps: float = 1e-6, residual=None, out: Optional[Fp8] =
     """``h = x + residual`` and ``h / sqrt(mean(h^2) + eps) * gain`` in 8 bits
     (``gptq_fp8_rms_norm``): returns the 8-bit activations and ``h`` in x's
     type (None without a residual).  ``sum_out`` may be ``x`` or ``residual``."""
-    import torch
     n, d = x.shape
     out = (_fp8_cols(out, d) if out is not None else _fp8_out(n, d, ((d + 127) // 128, n), x.device, stream))
     if residual is not None and sum_out is None:
+        import torch
         with _on(stream):
             sum_out = torch.empty((n, d), dtype=x.dtype, device=x.device)
     _lib.fp8_rms_norm(x, gain, eps, out.data, out.scales, residual=residual, sum_out=sum_out, stream=stream)
@@ -252,10 +252,10 @@ def fp8_matmul(w: Fp8, x: Fp8, dtype=None, relu: bool = False, channel_major: bo
     """``act(X W^T)`` of an 8-bit weight and 8-bit activations
     (``gptq_fp8_matmul``): ``[n, d_out]``, or ``[d_out, n]`` with
     ``channel_major``, as ``dtype`` (float16 by default)."""
-    import torch
     if w.cols != x.cols:
         raise ValueError(f"weights of {w.cols} columns, activations of {x.cols}")
     if out is None:
+        import torch
         shape = (w.data.shape[0], x.data.shape[0])
         with _on(stream):
             out = torch.empty(shape if channel_major else shape[::-1], dtype=dtype or torch.float16,
@@ -271,7 +271,6 @@ def fp8_gated(gate: Fp8, up: Fp8, x: Fp8, ws: Optional[Workspace] = None, out: O
     """``silu(X G^T) * (X U^T)`` in 8 bits (``gptq_fp8_gated``): the input of
     the down projection.  Few tokens need scratch memory: that of ``ws``, or
     memory of the call's own."""
-    import torch
     if gate.cols != x.cols or up.cols != x.cols:
         raise ValueError(f"weights of {gate.cols} and {up.cols} columns, activations of {x.cols}")
     n, d_ff = x.data.shape[0], gate.data.shape[0]
@@ -280,6 +279,7 @@ def fp8_gated(gate: Fp8, up: Fp8, x: Fp8, ws: Optional[Workspace] = None, out: O
     need = _lib.fp8_gated_workspace(n, d_ff)
     buf = None
     if need:
+        import torch
         with _on(stream):
             buf = ws.get(need) if ws is not None else torch.empty(need, dtype=torch.uint8, device=x.data.device)
     _lib.fp8_gated(gate.data, gate.scales, up.data, up.scales, x.data, x.scales, gate.cols, out.data, out.scales, buf,
