@@ -22,8 +22,9 @@ __device__ __forceinline__ float to_f32(half_t v) { return (float)v; }
 __device__ __forceinline__ float to_f32(bf16_t v) { return (float)v; }
 
 // v[0..8) = p[0..8) as float32, zeros from index `valid` on.  kVec: p is
-// 16-byte aligned and valid is 8 or <= 0.
-template <typename T, bool kVec>
+// 16-byte aligned and valid is 8 or <= 0.  kOnce: the data is not kept in the
+// caches (nontemporal).
+template <typename T, bool kVec, bool kOnce = false>
 __device__ __forceinline__ void load8(float (&v)[8], const T* __restrict__ p, int64_t valid) {
     if (kVec) {
         if (valid <= 0) {
@@ -36,7 +37,7 @@ __device__ __forceinline__ void load8(float (&v)[8], const T* __restrict__ p, in
         const uint4v* src = reinterpret_cast<const uint4v*>(p);
         uint4v* dst = reinterpret_cast<uint4v*>(raw);
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) dst[i] = src[i];
+        for (int i = 0; i < kPieces; ++i) dst[i] = kOnce ? __builtin_nontemporal_load(src + i) : src[i];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = to_f32(raw[e]);
     } else {
