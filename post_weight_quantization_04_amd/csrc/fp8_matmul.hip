@@ -18,6 +18,8 @@
 // MFMA in the tile kernel; float32 outputs and the gated block, whose scales
 // are float32, from the float16 one, and so does everything the few-token
 // kernel computes, which HBM bounds either way.
+#include <algorithm>
+
 #include "fp8_common.hpp"
 #include "kernels.hpp"
 
@@ -103,15 +105,18 @@ __device__ __forceinline__ void copy4(__amdgpu_buffer_rsrc_t r, float* lds, uint
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 4, off, base, 0, 0);
 }
 
-// The fragment of sixteen rows at p that lane (l16, kg) holds: chunks 2 kg and
-// 2 kg + 1 of row l16 (swz0, swz1: where they lie in a row).
-__device__ __forceinline__ int8v f8_fragment(const uint8_t* p, int l16, int swz0, int swz1) {
+// The fragment of sixteen rows at byte `at` of an LDS array that lane (l16, kg)
+// holds: chunks 2 kg and 2 kg + 1 of row l16, which lie at at0 and at1 of the
+// sixteen rows.  (The offsets are summed before they meet the array: the
+// compiler tells arrays apart through a few steps of address arithmetic only,
+// and where it cannot, a read waits for every copy in flight.)
+__device__ __forceinline__ int8v f8_fragment(const uint8_t* lds, int at, int at0, int at1) {
     union {
         uint4v h[2];
         int8v v;
     } u;
-    u.h[0] = *reinterpret_cast<const uint4v*>(p + l16 * kF8Block + swz0);
-    u.h[1] = *reinterpret_cast<const uint4v*>(p + l16 * kF8Block + swz1);
+    u.h[0] = *reinterpret_cast<const uint4v*>(lds + (at + at0));
+    u.h[1] = *reinterpret_cast<const uint4v*>(lds + (at + at1));
     return u.v;
 }
 
@@ -126,31 +131,29 @@ struct MmArgs {
 };
 
 // ---------------------------------------------------------------------------
-// Few tokens: 16 kTm weight rows and 16 kTn tokens a workgroup.  The waves
+// Few tokens: sixteen weight rows and 16 kTn tokens a workgroup.  The waves
 // share the blocks of k and work on their own, without barriers: a wave copies
-// its next kStages - 1 blocks to its own part of LDS (eight rows of 128 bytes
+// its next two blocks to its own part of LDS (eight rows of 128 bytes
 // an instruction; loads into registers would ask for 64 separate pieces of 16
 // bytes, since neighbouring lanes of a fragment hold different rows, and the
 // address unit bounds them: 16 us at 24 tokens of 11008 x 4096).  The waves'
 // sums meet in LDS, added in wave order.  kOctets: rows of tokens that are
 // copied, in eights (the others' columns are computed from whatever lies there
-// and never stored).
+// and never stored).  Three or four blocks ahead: no faster (24 tokens of 11008 x
+// 4096: 10.8 us, 11.2 and 10.7).
 // ---------------------------------------------------------------------------
-template <typename T, int kWaves, int kTm, int kOctets, int kMats, int kStages>
+template <typename T, int kWaves, int kOctets, int kMats>
 __global__ __launch_bounds__(kWaves* kWave) void f8_few_kernel(MmArgs a) {
     constexpr int kTn = (kOctets + 1) / 2;
-    constexpr int kA = kTm * kMats;  // fragments of weights: row tiles of the first matrix, then of the second
-    constexpr int kLoads = 2 * kA + kOctets + kTn + kMats;  // vector memory instructions a block
-    constexpr int kPart = (16 * kA + 16 * kTn) * kF8Block;  // a wave's part of a stage
-    static_assert(kStages >= 2 && kStages <= 4 && (kStages - 1) * kLoads < 64, "stages; the wait counts to 63");
-    static_assert(kA * kTn * 1024 <= kPart, "the sums meet in the first stage");
+    constexpr int kLoads = 2 * kMats + kOctets + kTn + kMats;  // vector memory instructions a block
+    constexpr int kPart = 2048 * (kMats + kTn);                // a wave's part of a stage
+    static_assert(kLoads < 64, "the wait counts to 63");
+    static_assert(kMats * kTn * 1024 <= kPart, "the sums meet in the first stage");
     __shared__ __align__(16) uint8_t stage0[kWaves * kPart];
     __shared__ __align__(16) uint8_t stage1[kWaves * kPart];
-    __shared__ __align__(16) uint8_t stage2[kStages > 2 ? kWaves * kPart : 16];
-    __shared__ __align__(16) uint8_t stage3[kStages > 3 ? kWaves * kPart : 16];
     const int tid = threadIdx.x, lane = tid % kWave, w = wave_id();
-    const int64_t r0 = (int64_t)blockIdx.x * (16 * kTm), t0 = (int64_t)blockIdx.y * (16 * kTn);
-    const int rows = (int)min(a.M - r0, (int64_t)(16 * kTm)), toks = (int)min(a.n - t0, (int64_t)(16 * kTn));
+    const int64_t r0 = (int64_t)blockIdx.x * 16, t0 = (int64_t)blockIdx.y * (16 * kTn);
+    const int rows = (int)min(a.M - r0, (int64_t)16), toks = (int)min(a.n - t0, (int64_t)(16 * kTn));
     const int nb = a.nb, l16 = lane % 16, kg = lane / 16;
     const uint32_t wbytes = (uint32_t)((rows - 1) * a.ldw + nb * kF8Block);
     const __amdgpu_buffer_rsrc_t rw = f8_rsrc(a.wq[0] + r0 * a.ldw, wbytes);
@@ -160,9 +163,9 @@ __global__ __launch_bounds__(kWaves* kWave) void f8_few_kernel(MmArgs a) {
     const __amdgpu_buffer_rsrc_t rus =
         kMats == 2 ? f8_rsrc(a.ws[1] + (r0 / kF8Block) * a.ldws, (uint32_t)(4 * nb)) : rws;
 
-    uint32_t ao[2 * kTm], bo[kOctets], so[kTn];
+    uint32_t ao[2], bo[kOctets], so[kTn];
 #pragma unroll
-    for (int i = 0; i < 2 * kTm; ++i) {
+    for (int i = 0; i < 2; ++i) {
         const int r = 8 * i + lane / 8;
         ao[i] = r < rows ? (uint32_t)(r * a.ldw + 16 * ((lane % 8) ^ f8_swizzle(r))) : kF8Out;
     }
@@ -173,11 +176,12 @@ __global__ __launch_bounds__(kWaves* kWave) void f8_few_kernel(MmArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < kTn; ++j) so[j] = 16 * j + l16 < toks ? (uint32_t)(4 * (16 * j + l16)) : kF8Out;
-    const int swz0 = 16 * ((2 * kg) ^ f8_swizzle(l16)), swz1 = 16 * ((2 * kg + 1) ^ f8_swizzle(l16));
+    const int at0 = l16 * kF8Block + 16 * ((2 * kg) ^ f8_swizzle(l16));
+    const int at1 = l16 * kF8Block + 16 * ((2 * kg + 1) ^ f8_swizzle(l16));
 
-    float4v acc[kA][kTn];
+    float4v acc[kMats][kTn];
 #pragma unroll
-    for (int m = 0; m < kA; ++m)
+    for (int m = 0; m < kMats; ++m)
 #pragma unroll
         for (int j = 0; j < kTn; ++j) acc[m][j] = (float4v){};
 
@@ -185,18 +189,17 @@ __global__ __launch_bounds__(kWaves* kWave) void f8_few_kernel(MmArgs a) {
     // do not all ask for the same lines of X at once
     const int shift = nb > 0 ? (int)(blockIdx.x * 5u % (unsigned)nb) : 0;
     const int mine = w < nb ? (nb - w + kWaves - 1) / kWaves : 0;
-    float xs[kStages][kTn], ws[kStages][kMats];
+    float xs[2][kTn], ws[2][kMats];
     auto copy = [&](uint8_t* stage, float (&x)[kTn], float (&s)[kMats], int i) {
         int b = w + min(i, mine - 1) * kWaves + shift;  // past the wave's last block, that one again, never used
         b = b >= nb ? b - nb : b;
         const uint32_t ko = (uint32_t)(b * kF8Block);
-        uint8_t* p = stage + w * kPart;
 #pragma unroll
         for (int m = 0; m < kMats; ++m)
 #pragma unroll
-            for (int c = 0; c < 2 * kTm; ++c) copy16(m ? ru : rw, p + 1024 * (2 * kTm * m + c), ao[c], ko);
+            for (int c = 0; c < 2; ++c) copy16(m ? ru : rw, stage + (w * kPart + 2048 * m + 1024 * c), ao[c], ko);
 #pragma unroll
-        for (int c = 0; c < kOctets; ++c) copy16(rx, p + 2048 * kA + 1024 * c, bo[c], ko);
+        for (int c = 0; c < kOctets; ++c) copy16(rx, stage + (w * kPart + 2048 * kMats + 1024 * c), bo[c], ko);
         const __amdgpu_buffer_rsrc_t rs = f8_rsrc(a.xs + b * a.ldxs + t0, (uint32_t)(4 * toks));
 #pragma unroll
         for (int j = 0; j < kTn; ++j) x[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, so[j], 0, 0));
@@ -204,74 +207,68 @@ __global__ __launch_bounds__(kWaves* kWave) void f8_few_kernel(MmArgs a) {
         if (kMats == 2) s[kMats - 1] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rus, 4 * b, 0, 0));
     };
     auto step = [&](uint8_t* stage, float (&x)[kTn], float (&s)[kMats], int i) {
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kStages - 1) * kLoads) : "memory");
-        const uint8_t* p = stage + w * kPart;
-        int8v av[kA], bv[kTn];
+        // (the next step's scales, multiplied here, would wait for every load in flight)
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+        int8v av[kMats], bv[kTn];
 #pragma unroll
-        for (int m = 0; m < kA; ++m) av[m] = f8_fragment(p + 2048 * m, l16, swz0, swz1);
+        for (int m = 0; m < kMats; ++m) av[m] = f8_fragment(stage, w * kPart + 2048 * m, at0, at1);
 #pragma unroll
-        for (int j = 0; j < kTn; ++j) bv[j] = f8_fragment(p + 2048 * (kA + j), l16, swz0, swz1);
+        for (int j = 0; j < kTn; ++j) bv[j] = f8_fragment(stage, w * kPart + 2048 * (kMats + j), at0, at1);
         float sc[kMats][kTn];
 #pragma unroll
         for (int m = 0; m < kMats; ++m)
 #pragma unroll
             for (int j = 0; j < kTn; ++j) sc[m][j] = x[j] * s[m];
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read, before it is copied over
-        copy(stage, x, s, i + kStages);
+        copy(stage, x, s, i + 2);
         Halves bh[kTn];
 #pragma unroll
         for (int j = 0; j < kTn; ++j) bh[j] = to_halves(bv[j]);
 #pragma unroll
-        for (int m = 0; m < kA; ++m) {
+        for (int m = 0; m < kMats; ++m) {
             const Halves ah = to_halves(av[m]);
 #pragma unroll
             for (int j = 0; j < kTn; ++j) {
                 const float4v q = block_product(ah, bh[j]);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) acc[m][j][v] = fmaf(q[v], sc[m / kTm][j], acc[m][j][v]);
+                for (int v = 0; v < 4; ++v) acc[m][j][v] = fmaf(q[v], sc[m][j], acc[m][j][v]);
             }
         }
     };
     if (mine > 0) {
         copy(stage0, xs[0], ws[0], 0);
         copy(stage1, xs[1], ws[1], 1);
-        if (kStages > 2) copy(stage2, xs[kStages > 2 ? 2 : 0], ws[kStages > 2 ? 2 : 0], 2);
-        if (kStages > 3) copy(stage3, xs[kStages > 3 ? 3 : 0], ws[kStages > 3 ? 3 : 0], 3);
         int i = 0;
-        for (; i + kStages <= mine; i += kStages) {
+        for (; i + 2 <= mine; i += 2) {
             step(stage0, xs[0], ws[0], i);
             step(stage1, xs[1], ws[1], i + 1);
-            if (kStages > 2) step(stage2, xs[kStages > 2 ? 2 : 0], ws[kStages > 2 ? 2 : 0], i + 2);
-            if (kStages > 3) step(stage3, xs[kStages > 3 ? 3 : 0], ws[kStages > 3 ? 3 : 0], i + 3);
         }
         if (i < mine) step(stage0, xs[0], ws[0], i);
-        if (i + 1 < mine) step(stage1, xs[1], ws[1], i + 1);
-        if (kStages > 3 && i + 2 < mine) step(stage2, xs[kStages > 2 ? 2 : 0], ws[kStages > 2 ? 2 : 0], i + 2);
     }
     // every copy has landed before the memory is used for the sums
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __syncthreads();
-    float* part = reinterpret_cast<float*>(stage0);  // [kWaves][kA kTn][4][kWave]
+    float* part = reinterpret_cast<float*>(stage0);  // [kWaves][kMats kTn][4][kWave]
 #pragma unroll
-    for (int m = 0; m < kA; ++m)
+    for (int m = 0; m < kMats; ++m)
 #pragma unroll
         for (int j = 0; j < kTn; ++j)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) part[((w * kA * kTn + m * kTn + j) * 4 + v) * kWave + lane] = acc[m][j][v];
+            for (int v = 0; v < 4; ++v) part[((w * kMats * kTn + m * kTn + j) * 4 + v) * kWave + lane] = acc[m][j][v];
     __syncthreads();
-    // value i of the 256 kTm kTn: row tile, token tile, register, lane
+    // value i of the 256 kTn: token tile, register, lane
 #pragma unroll
-    for (int i = tid; i < 256 * kTm * kTn; i += kWaves * kWave) {
-        const int mj = i / 256, v = (i / kWave) % 4, l = i % kWave;
+    for (int i = tid; i < 256 * kTn; i += kWaves * kWave) {
+        const int j = i / 256, v = (i / kWave) % 4, l = i % kWave;
         float sum[kMats];
 #pragma unroll
         for (int m = 0; m < kMats; ++m) {
             sum[m] = 0.0f;
 #pragma unroll
-            for (int ww = 0; ww < kWaves; ++ww)
-                sum[m] += part[((ww * kA * kTn + m * kTm * kTn + mj) * 4 + v) * kWave + l];
+            for (int ww = 0; ww < kWaves; ++ww) sum[m] += part[((ww * kMats * kTn + m * kTn + j) * 4 + v) * kWave + l];
         }
-        const int t = 16 * (mj % kTn) + l % 16, r = 16 * (mj / kTn) + 4 * (l / 16) + v;
+        const int t = 16 * j + l % 16, r = 4 * (l / 16) + v;
         if (t < toks && r < rows) {
             const float y = kMats == 2 ? gated(sum[0], sum[kMats - 1]) : relu_if(sum[0], a.relu);
             T* o = static_cast<T*>(a.y);
@@ -281,23 +278,24 @@ __global__ __launch_bounds__(kWaves* kWave) void f8_few_kernel(MmArgs a) {
     }
 }
 
-template <typename T, int kWaves, int kTm, int kOctets, int kMats, int kStages>
+template <typename T, int kWaves, int kOctets, int kMats>
 hipError_t few_go(const MmArgs& a, TimedLaunch t, hipStream_t s) {
     constexpr int kTn = (kOctets + 1) / 2;
-    const dim3 grid((unsigned)((a.M + 16 * kTm - 1) / (16 * kTm)), (unsigned)((a.n + 16 * kTn - 1) / (16 * kTn)));
-    GPTQ_LAUNCH(t, (f8_few_kernel<T, kWaves, kTm, kOctets, kMats, kStages>), grid, dim3(kWaves * kWave), 0, s, a);
+    const dim3 grid((unsigned)((a.M + 15) / 16), (unsigned)((a.n + 16 * kTn - 1) / (16 * kTn)));
+    GPTQ_LAUNCH(t, (f8_few_kernel<T, kWaves, kOctets, kMats>), grid, dim3(kWaves * kWave), 0, s, a);
     return hipGetLastError();
 }
 
 // Eight waves share k where a workgroup has a CU to itself and blocks enough
 // for them, four otherwise (two workgroups a CU then hide each other's ends):
-// 11008 x 4096 weights, 24 tokens, 10.9 against 12.3 us; 4096 x 11008, one
-// token, 9.7 against 9.5 us, 24 tokens 14.3 against 11.8 us.
+// 11008 x 4096 weights, 24 tokens, 10.8 against 11.9 us; 4096 x 11008, one
+// token, 9.8 against 9.5 us, 24 tokens 14.4 against 11.7 us; both projections
+// of the gated block, one token, 22.2 against 18.9 us.
 template <typename T, int kOctets, int kMats>
 hipError_t few_waves(const MmArgs& a, TimedLaunch t, hipStream_t s) {
-    if constexpr (kMats == 1 && kOctets <= 4)
-        if ((a.M + 15) / 16 <= device_cu_count() && a.nb >= 16) return few_go<T, 8, 1, kOctets, kMats, 2>(a, t, s);
-    return few_go<T, 4, 1, kOctets, kMats, 2>(a, t, s);
+    if constexpr (kMats == 1)
+        if ((a.M + 15) / 16 <= device_cu_count() && a.nb >= 16) return few_go<T, 8, kOctets, kMats>(a, t, s);
+    return few_go<T, 4, kOctets, kMats>(a, t, s);
 }
 
 template <typename T, int kMats>
@@ -312,7 +310,8 @@ hipError_t few_launch(const MmArgs& a, TimedLaunch t, hipStream_t s) {
 
 // ---------------------------------------------------------------------------
 // Many tokens: a workgroup computes kTM weight rows by kTN tokens, its waves
-// (kWM x kWN) a rectangle each.  One block of k (128 bytes a row) of both
+// (kWM x kWN) a rectangle each; kSplit groups of such waves share k, each with
+// stages of its own, and add their sums at the end.  One block of k (128 bytes a row) of both
 // operands is a stage; stages are copied from memory to LDS without passing
 // registers, kStages - 1 ahead of the one in use, one barrier a stage.
 //
@@ -350,32 +349,36 @@ __device__ __forceinline__ void f8_tile_of(unsigned id, unsigned mt, unsigned nt
     ni = in / rows;
 }
 
-template <typename T, int kTM, int kTN, int kWM, int kWN, int kStages, bool kGated, bool kHalf, bool kChannels>
-__global__ __launch_bounds__(kWM* kWN* kWave) void f8_tile_kernel(TileArgs a) {
-    constexpr int kWaves = kWM * kWN, kThreads = kWaves * kWave;
+template <typename T, int kTM, int kTN, int kWM, int kWN, int kStages, int kSplit, bool kGated, bool kHalf, bool kChannels>
+__global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileArgs a) {
+    constexpr int kWaves = kWM * kWN, kThreads = kWaves * kWave;  // of one group
     constexpr int kMt = kTM / kWM / 16, kNt = kTN / kWN / 16;
     constexpr int kAi = kTM / 8 / kWaves, kBi = kTN / 8 / kWaves;  // copy instructions of a wave and stage
     constexpr int kLoads = kAi + kBi + 1;                          // and one for the token scales
     static_assert(kTM % (8 * kWaves) == 0 && kTN % (8 * kWaves) == 0 && kTN % 64 == 0, "whole copies");
     static_assert(kTN / 64 <= kWaves && kWaves % (kTN / 64) == 0, "every wave copies one run of scales");
     static_assert(!kGated || kTM == 256, "a gated tile holds one block of channels of both matrices");
-    static_assert(kStages >= 2 && kStages <= 4 && kMt >= 2 && kNt >= 2, "stages, tiles of a wave");
+    static_assert(kMt >= 2 && kNt >= 2, "tiles of a wave");
     constexpr int kABytes = kTM * kF8Block, kBBytes = kTN * kF8Block, kBytes = kABytes + kBBytes + 4 * kTN;
     // separate arrays: the compiler then knows that a read of one does not wait for copies into another
-    __shared__ __align__(16) uint8_t stage0[kBytes];
-    __shared__ __align__(16) uint8_t stage1[kBytes];
-    __shared__ __align__(16) uint8_t stage2[kStages > 2 ? kBytes : 16];
-    __shared__ __align__(16) uint8_t stage3[kStages > 3 ? kBytes : 16];
+    __shared__ __align__(16) uint8_t lds0[kSplit * kBytes];
+    __shared__ __align__(16) uint8_t lds1[kSplit * kBytes];
+    __shared__ __align__(16) uint8_t lds2[kStages > 2 ? kSplit * kBytes : 16];
+    static_assert(kStages == 2 || kStages == 3, "stages");
+    static_assert(kSplit == 1 || !kGated, "the gated block is not split");
 
     const MmArgs& m = a.m;
-    const int tid = threadIdx.x, lane = tid % kWave, w = wave_id();
+    const int tid = threadIdx.x, lane = tid % kWave;
+    const int group = kSplit > 1 ? wave_id() / kWaves : 0, w = wave_id() - group * kWaves;
+    const int base = kSplit > 1 ? group * kBytes : 0;  // of the group's part of a stage
     const int wm = w / kWN, wn = w % kWN, l16 = lane % 16, kg = lane / 16;
     unsigned mi, ni;
     f8_tile_of(blockIdx.x, a.mt, a.nt, mi, ni);
     constexpr int kRows = kGated ? kTM / 2 : kTM;  // rows of one matrix
     const int64_t m0 = (int64_t)mi * kRows, t0 = (int64_t)ni * kTN;
     const int rows = (int)min(m.M - m0, (int64_t)kRows), toks = (int)min(m.n - t0, (int64_t)kTN);
-    const int nb = m.nb;
+    // the group's blocks of k: every kSplit-th, as many steps for every group
+    const int nb = m.nb, steps = (nb + kSplit - 1) / kSplit;
 
     const __amdgpu_buffer_rsrc_t rw = f8_rsrc(m.wq[0] + m0 * m.ldw, (uint32_t)((rows - 1) * m.ldw + nb * kF8Block));
     const __amdgpu_buffer_rsrc_t ru =
@@ -398,15 +401,15 @@ __global__ __launch_bounds__(kWM* kWN* kWave) void f8_tile_kernel(TileArgs a) {
     const uint32_t so = sr + lane < toks ? (uint32_t)(4 * (sr + lane)) : kF8Out;
     const bool up = kGated && w >= kWaves / 2;  // rows of the up matrix (whole waves)
 
-    // copy c of the wave's kLoads into stage st: block b of k (past the last block, that one again, never used)
-    auto copy = [&](uint8_t* st, int b, int c) {
-        b = min(b, nb - 1);
+    // copy c of the wave's kLoads into stage st: the block of step i (past the last block, that one again, counted zero)
+    auto copy = [&](uint8_t* st, int i, int c) {
+        const int b = min(i * kSplit + group, nb - 1);
         const uint32_t ko = (uint32_t)(b * kF8Block);
-        if (c < kAi) copy16(up ? ru : rw, st + 1024 * (kAi * w + c), ao[c < kAi ? c : 0], ko);
-        else if (c < kAi + kBi) copy16(rx, st + kABytes + 1024 * (kBi * w + c - kAi), bo[c < kAi + kBi ? c - kAi : 0], ko);
+        if (c < kAi) copy16(up ? ru : rw, st + (base + 1024 * (kAi * w + c)), ao[c < kAi ? c : 0], ko);
+        else if (c < kAi + kBi) copy16(rx, st + (base + kABytes + 1024 * (kBi * w + c - kAi)), bo[c < kAi + kBi ? c - kAi : 0], ko);
         else {
             const __amdgpu_buffer_rsrc_t rs = f8_rsrc(m.xs + b * m.ldxs + t0, (uint32_t)(4 * toks));
-            copy4(rs, reinterpret_cast<float*>(st + kABytes + kBBytes) + sr, so, 0);
+            copy4(rs, reinterpret_cast<float*>(st + (base + kABytes + kBBytes + 4 * sr)), so, 0);
         }
     };
 
@@ -427,8 +430,12 @@ __global__ __launch_bounds__(kWM* kWN* kWave) void f8_tile_kernel(TileArgs a) {
         if (!kGated) return wm * kWaveRows + 16 * i;
         return i < kMt / 2 ? wm * (kRows / kWM) + 16 * i : kRows + wm * (kRows / kWM) + 16 * (i - kMt / 2);
     };
-    const int swz0 = 16 * ((2 * kg) ^ f8_swizzle(l16)), swz1 = 16 * ((2 * kg + 1) ^ f8_swizzle(l16));
-    auto fragment = [&](const uint8_t* p, int row) { return f8_fragment(p + row * kF8Block, l16, swz0, swz1); };
+    const int at0 = base + l16 * kF8Block + 16 * ((2 * kg) ^ f8_swizzle(l16));
+    const int at1 = base + l16 * kF8Block + 16 * ((2 * kg + 1) ^ f8_swizzle(l16));
+    auto rows_fragment = [&](const uint8_t* st, int i) { return f8_fragment(st, row_of(i) * kF8Block, at0, at1); };
+    auto toks_fragment = [&](const uint8_t* st, int j) {
+        return f8_fragment(st, kABytes + (wn * kNt + j) * 16 * kF8Block, at0, at1);
+    };
 
     // What a step starts with, read from its stage while the step before ends:
     // the token fragments, the first weight fragment and the token scales.
@@ -438,11 +445,12 @@ __global__ __launch_bounds__(kWM* kWN* kWave) void f8_tile_kernel(TileArgs a) {
     int8v raw;
     float sx[kNt][kPer];
     auto read_scales = [&](const uint8_t* st) {
-        const float* S = reinterpret_cast<const float*>(st + kABytes + kBBytes);
 #pragma unroll
         for (int j = 0; j < kNt; ++j)
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) sx[j][e] = S[(wn * kNt + j) * 16 + (kChannels ? 4 * kg + e : l16)];
+            for (int e = 0; e < kPer; ++e) 
+                sx[j][e] = *reinterpret_cast<const float*>(
+                    st + (base + kABytes + kBBytes + 4 * ((wn * kNt + j) * 16 + (kChannels ? 4 * kg + e : l16))));
     };
     // products that are still to be scaled and added: two MFMAs old when that
     // happens, the last two of a step in the next one
@@ -482,7 +490,7 @@ __global__ __launch_bounds__(kWM* kWN* kWave) void f8_tile_kernel(TileArgs a) {
         for (int i = 0; i < kMt; ++i) {
             const op_t af = Operand<kHalf>::of(raw);
             if (i + 1 < kMt) {
-                raw = fragment(st, row_of(i + 1));
+                raw = rows_fragment(st, i + 1);
                 constexpr int kLast = kMt - 2;
 #pragma unroll
                 for (int c = 0; c < kLoads; ++c)
@@ -494,8 +502,8 @@ __global__ __launch_bounds__(kWM* kWN* kWave) void f8_tile_kernel(TileArgs a) {
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
 #pragma unroll
-                for (int j = 0; j < kNt; ++j) nraw[j] = fragment(nx + kABytes, (wn * kNt + j) * 16);
-                raw = fragment(nx, row_of(0));
+                for (int j = 0; j < kNt; ++j) nraw[j] = toks_fragment(nx, j);
+                raw = rows_fragment(nx, 0);
                 if (!kChannels) read_scales(nx);  // four times as many: too many registers to hold ahead
 #pragma unroll
                 for (int c = 0; c < kPre; ++c) copy(st, b + 1 + kAhead, c);
@@ -519,44 +527,40 @@ __global__ __launch_bounds__(kWM* kWN* kWave) void f8_tile_kernel(TileArgs a) {
 #pragma unroll
         for (int d = 0; d < kAhead; ++d)
 #pragma unroll
-            for (int c = 0; c < kLoads; ++c) copy(d == 0 ? stage0 : d == 1 ? stage1 : stage2, d, c);
+            for (int c = 0; c < kLoads; ++c) copy(d == 0 ? lds0 : lds1, d, c);
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((kAhead - 1) * kLoads) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        uint8_t* const last = kStages == 2 ? stage1 : kStages == 3 ? stage2 : stage3;
+        uint8_t* const last = kStages == 2 ? lds1 : lds2;
 #pragma unroll
-        for (int j = 0; j < kNt; ++j) bf[j] = Operand<kHalf>::of(fragment(stage0 + kABytes, (wn * kNt + j) * 16));
-        raw = fragment(stage0, row_of(0));
-        read_scales(stage0);
+        for (int j = 0; j < kNt; ++j) bf[j] = Operand<kHalf>::of(toks_fragment(lds0, j));
+        raw = rows_fragment(lds0, 0);
+        read_scales(lds0);
 #pragma unroll
         for (int c = 0; c < kPre; ++c) copy(last, kAhead, c);
 
-        // the weight scales of kRun blocks at a time, one a lane
+        // the weight scales of kMany steps at a time, one a lane
         constexpr int kMany = 64 / kStages * kStages;
-        for (int b0 = 0; b0 < nb; b0 += kMany) {
-            const int run = min(kMany, nb - b0);
-            const int at = b0 + min(lane, run - 1);
-            const int wl = __builtin_bit_cast(int, wsr[at]);
-            const int ul = kGated ? __builtin_bit_cast(int, usr[at]) : 0;
-            auto go = [&](uint8_t* st, uint8_t* nx, uint8_t* to, int b) {
-                step(st, nx, to, b0 + b, __builtin_bit_cast(float, __builtin_amdgcn_readlane(wl, b)),
-                     kGated ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(ul, b)) : 0.0f);
+        for (int i0 = 0; i0 < steps; i0 += kMany) {
+            const int run = min(kMany, steps - i0);
+            const int at = (i0 + lane) * kSplit + group;
+            const int wl = __builtin_bit_cast(int, at < nb ? wsr[at] : 0.0f);
+            const int ul = kGated ? __builtin_bit_cast(int, at < nb ? usr[at] : 0.0f) : 0;
+            auto go = [&](uint8_t* st, uint8_t* nx, uint8_t* to, int i) {
+                step(st, nx, to, i0 + i, __builtin_bit_cast(float, __builtin_amdgcn_readlane(wl, i)),
+                     kGated ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(ul, i)) : 0.0f);
             };
-            uint8_t* const after0 = stage1;
-            uint8_t* const after1 = kStages > 2 ? stage2 : stage0;
-            uint8_t* const after2 = kStages > 3 ? stage3 : stage0;
+            uint8_t* const after1 = kStages > 2 ? lds2 : lds0;
             // no branch between the steps of the loop: the compiler would move
             // the scaling of products past it and keep them all in registers
-            int b = 0;
-            for (; b + kStages <= run; b += kStages) {
-                go(stage0, after0, last, b);
-                go(stage1, after1, stage0, b + 1);
-                if (kStages > 2) go(stage2, after2, stage1, b + 2);
-                if (kStages > 3) go(stage3, stage0, stage2, b + 3);
+            int i = 0;
+            for (; i + kStages <= run; i += kStages) {
+                go(lds0, lds1, last, i);
+                go(lds1, after1, lds0, i + 1);
+                if (kStages > 2) go(lds2, lds0, lds1, i + 2);
             }
-            if (b < run) go(stage0, after0, last, b);
-            if (kStages > 2 && b + 1 < run) go(stage1, after1, stage0, b + 1);
-            if (kStages > 3 && b + 2 < run) go(stage2, after2, stage1, b + 2);
+            if (i < run) go(lds0, lds1, last, i);
+            if (kStages > 2 && i + 1 < run) go(lds1, after1, lds0, i + 1);
         }
         add(acc[kMt - 1][kNt - 2], late[0], late_s[0]);
         add(acc[kMt - 1][kNt - 1], late[1], late_s[1]);
@@ -567,9 +571,36 @@ __global__ __launch_bounds__(kWM* kWN* kWave) void f8_tile_kernel(TileArgs a) {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 
+    if (kSplit > 1) {
+        // the groups' sums, added in group order
+        constexpr int kOne = kWaves * kMt * kNt * 4 * kWave;
+        static_assert(kSplit == 1 || 4 * (kSplit - 1) * kOne <= kSplit * kBytes, "the sums in the second stages");
+        float* sums = reinterpret_cast<float*>(lds1);
+        auto at = [&](int g, int i, int j, int v) -> float& {
+            return sums[(g - 1) * kOne + (((w * kMt + i) * kNt + j) * 4 + v) * kWave + lane];
+        };
+        if (group > 0) {
+#pragma unroll
+            for (int i = 0; i < kMt; ++i)
+#pragma unroll
+                for (int j = 0; j < kNt; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) at(group, i, j, v) = acc[i][j][v];
+        }
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int g = 1; g < kSplit; ++g)
+#pragma unroll
+            for (int i = 0; i < kMt; ++i)
+#pragma unroll
+                for (int j = 0; j < kNt; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[i][j][v] += at(g, i, j, v);
+    }
     if (kGated) {
-        uint32_t* peaks = reinterpret_cast<uint32_t*>(stage1);  // [kWM][kTN]
-        uint32_t* codes = reinterpret_cast<uint32_t*>(stage0);  // [kTN][kCodePitch]
+        uint32_t* peaks = reinterpret_cast<uint32_t*>(lds1);  // [kWM][kTN]
+        uint32_t* codes = reinterpret_cast<uint32_t*>(lds0);  // [kTN][kCodePitch]
         constexpr int kCodePitch = kF8Block / 4 + 1;
         static_assert(4 * kTN * kCodePitch <= kABytes + kBBytes && 4 * kWM * kTN <= kABytes, "epilogue's LDS");
         uint32_t pk[kNt];
@@ -617,11 +648,11 @@ __global__ __launch_bounds__(kWM* kWN* kWave) void f8_tile_kernel(TileArgs a) {
     constexpr int kRun = kChannels ? 16 * kNt : 16 * kMt, kOuter = kChannels ? kMt : kNt, kInner = kChannels ? kNt : kMt;
     constexpr int kPitch = kRun * (int)sizeof(T) + 16, kVec = 16 / (int)sizeof(T);
     static_assert(kGated || kWaves * 16 * kPitch <= kBytes, "the lines of every wave in the first stage");
-    uint8_t* lines = stage0 + w * 16 * kPitch;
+    uint8_t* lines = lds0 + w * 16 * kPitch;
     T* y = static_cast<T*>(m.y);
     const int first = kChannels ? wn * kRun : wm * kRun;           // of the run, within the tile
     const int left = (kChannels ? toks : rows) - first;            // of the run, within Y
-    const int64_t at0 = (kChannels ? t0 : m0) + first;
+    const int64_t start = (kChannels ? t0 : m0) + first;
 #pragma unroll
     for (int o = 0; o < kOuter; ++o) {
 #pragma unroll
@@ -635,7 +666,7 @@ __global__ __launch_bounds__(kWM* kWN* kWave) void f8_tile_kernel(TileArgs a) {
         __builtin_amdgcn_wave_barrier();
         const int line0 = kChannels ? wm * kWaveRows + 16 * o : (wn * kNt + o) * 16;
         const int count = (kChannels ? rows : toks) - line0;       // lines within Y
-        T* base = y + ((kChannels ? m0 : t0) + line0) * m.ldy + at0;
+        T* base = y + ((kChannels ? m0 : t0) + line0) * m.ldy + start;
         if (a.wide) {
             constexpr int kPer = kRun / kVec;
 #pragma unroll
@@ -661,17 +692,17 @@ __global__ __launch_bounds__(kWM* kWN* kWave) void f8_tile_kernel(TileArgs a) {
     }
 }
 
-template <typename T, int kTM, int kTN, int kWM, int kWN, int kStages, bool kGated, bool kHalf>
+template <typename T, int kTM, int kTN, int kWM, int kWN, int kStages, bool kGated, bool kHalf, int kSplit = 1>
 hipError_t tile_launch(TileArgs a, TimedLaunch t, hipStream_t s) {
     constexpr int kRows = kGated ? kTM / 2 : kTM;
     a.mt = (unsigned)((a.m.M + kRows - 1) / kRows);
     a.nt = (unsigned)((a.m.n + kTN - 1) / kTN);
     a.wide = a.m.ldy * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(a.m.y) % 16 == 0;
-    const dim3 grid(a.mt * a.nt), block(kWM * kWN * kWave);
+    const dim3 grid(a.mt * a.nt), block(kSplit * kWM * kWN * kWave);
     if (!kGated && a.m.channel_major)
-        GPTQ_LAUNCH(t, (f8_tile_kernel<T, kTM, kTN, kWM, kWN, kStages, kGated, kHalf, !kGated>), grid, block, 0, s, a);
+        GPTQ_LAUNCH(t, (f8_tile_kernel<T, kTM, kTN, kWM, kWN, kStages, kSplit, kGated, kHalf, !kGated>), grid, block, 0, s, a);
     else
-        GPTQ_LAUNCH(t, (f8_tile_kernel<T, kTM, kTN, kWM, kWN, kStages, kGated, kHalf, false>), grid, block, 0, s, a);
+        GPTQ_LAUNCH(t, (f8_tile_kernel<T, kTM, kTN, kWM, kWN, kStages, kSplit, kGated, kHalf, false>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
@@ -686,12 +717,15 @@ bool f8_few(int64_t n, int64_t M) { return n <= kFewTokens || (n <= kSomeTokens 
 
 // The tile by what a product's blocks of k take: rounds of tiles over the CUs
 // times the measured time of a round and block.  us a block with every CU at
-// work: e4m3 MFMA 256 x 256 2.0, 256 x 128 1.2, 128 x 128 0.71, 64 x 64 0.40
-// (one a CU), 0.54 (two), 0.80 (three); float16 MFMA 256 x 128 2.1, 128 x 128
-// 1.44 (one a CU), 2.3 (two), 64 x 64 0.60, 0.90, 1.45.  At 4096 x 4096
-// weights, e4m3: 256 tokens 13.0 us in 64 x 64 tiles, 29 in 256 x 128; 1024
-// tokens 23 in 128 x 128, 31 in both neighbours; 4096 tokens 66 in 256 x 256,
-// 76 in 256 x 128, 112 in 64 x 64.
+// work: e4m3 MFMA 256 x 256 2.0, 256 x 128 1.2, 128 x 128 0.68, 128 x 64 with
+// two groups of waves sharing k 0.43, 64 x 64 0.31 (one a CU, two groups), 0.52
+// (two a CU), 0.80 (three); float16 MFMA 256 x 128 2.1, 128 x 128 1.38 (one a
+// CU), 2.3 (two), 128 x 64 in two groups 0.68, 64 x 64 0.47 (one, two groups),
+// 0.88, 1.45.  At 4096 x 4096 weights, e4m3: 256 tokens 10.7 us in 64 x 64
+// tiles (13.4 in one group), 13.4 in 128 x 64, 29 in 256 x 128; 512 tokens
+// 14.6 in 128 x 64, 16.5 in 64 x 64; 1024 tokens 22 in 128 x 128, 28 in 128 x
+// 64, 31 in 256 x 128; 4096 tokens 66 in 256 x 256, 76 in 256 x 128, 112 in 64
+// x 64.
 template <typename T, bool kHalf>
 hipError_t matmul_typed(const MmArgs& m, hipStream_t s) {
     TimedLaunch t(K_F8_MATMUL, s);
@@ -699,24 +733,28 @@ hipError_t matmul_typed(const MmArgs& m, hipStream_t s) {
     TileArgs a = {};
     a.m = m;
     const int64_t cus = device_cu_count();
-    if (cus <= 0) return hipErrorInvalidDevice;
     auto rounds = [&](int64_t tm, int64_t tn, int64_t each) {
         return (((m.M + tm - 1) / tm) * ((m.n + tn - 1) / tn) + cus * each - 1) / (cus * each);
     };
     const bool one = rounds(64, 64, 1) == 1, two = rounds(64, 64, 2) == 1;
     if constexpr (kHalf) {
-        const double t64 = one ? 0.60 : two ? 0.90 : 1.45 * rounds(64, 64, 3);
-        const double t128 = rounds(128, 128, 1) == 1 ? 1.44 : 2.3 * rounds(128, 128, 2);
-        const double t256 = 2.1 * rounds(256, 128, 1);
-        if (t64 <= t128 && t64 <= t256) return tile_launch<T, 64, 64, 2, 2, 3, false, true>(a, t, s);
-        if (t128 <= t256) return tile_launch<T, 128, 128, 2, 2, 2, false, true>(a, t, s);
+        const double t64 = one ? 0.47 : two ? 0.88 : 1.45 * rounds(64, 64, 3), t96 = 0.68 * rounds(128, 64, 1);
+        const double t128 = rounds(128, 128, 1) == 1 ? 1.38 : 2.3 * rounds(128, 128, 2);
+        const double t256 = 2.1 * rounds(256, 128, 1), least = std::min(std::min(t64, t96), std::min(t128, t256));
+        if (t64 == least && one) return tile_launch<T, 64, 64, 2, 2, 3, false, true, 2>(a, t, s);
+        if (t64 == least) return tile_launch<T, 64, 64, 2, 2, 3, false, true>(a, t, s);
+        if (t96 == least) return tile_launch<T, 128, 64, 2, 2, 3, false, true, 2>(a, t, s);
+        if (t128 == least) return tile_launch<T, 128, 128, 2, 2, 2, false, true>(a, t, s);
         return tile_launch<T, 256, 128, 4, 2, 2, false, true>(a, t, s);
     } else {
-        const double t64 = one ? 0.40 : two ? 0.54 : 0.80 * rounds(64, 64, 3);
-        const double t128 = 0.71 * rounds(128, 128, 1), t256 = 1.2 * rounds(256, 128, 1), t512 = 2.0 * rounds(256, 256, 1);
-        if (t64 <= t128 && t64 <= t256 && t64 <= t512) return tile_launch<T, 64, 64, 2, 2, 3, false, false>(a, t, s);
-        if (t128 <= t256 && t128 <= t512) return tile_launch<T, 128, 128, 4, 2, 3, false, false>(a, t, s);
-        if (t256 <= t512) return tile_launch<T, 256, 128, 4, 2, 3, false, false>(a, t, s);
+        const double t64 = one ? 0.31 : two ? 0.52 : 0.80 * rounds(64, 64, 3), t96 = 0.43 * rounds(128, 64, 1);
+        const double t128 = 0.68 * rounds(128, 128, 1), t256 = 1.2 * rounds(256, 128, 1), t512 = 2.0 * rounds(256, 256, 1);
+        const double least = std::min(std::min(t64, t96), std::min(t128, std::min(t256, t512)));
+        if (t64 == least && one) return tile_launch<T, 64, 64, 2, 2, 3, false, false, 2>(a, t, s);
+        if (t64 == least) return tile_launch<T, 64, 64, 2, 2, 3, false, false>(a, t, s);
+        if (t96 == least) return tile_launch<T, 128, 64, 2, 2, 3, false, false, 2>(a, t, s);
+        if (t128 == least) return tile_launch<T, 128, 128, 4, 2, 3, false, false>(a, t, s);
+        if (t256 == least) return tile_launch<T, 256, 128, 4, 2, 3, false, false>(a, t, s);
         return tile_launch<T, 256, 256, 2, 4, 2, false, false>(a, t, s);
     }
 }
