@@ -349,7 +349,7 @@ __device__ __forceinline__ void f8_tile_of(unsigned id, unsigned mt, unsigned nt
     ni = in / rows;
 }
 
-template <typename T, int kTM, int kTN, int kWM, int kWN, int kStages, int kSplit, bool kGated, bool kHalf, bool kChannels>
+template <typename T, int kTM, int kTN, int kWM, int kWN, int kStages, int kSplit, bool kGated, bool kHalf, bool kChannels, bool kEarly, bool kCarry>
 __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileArgs a) {
     constexpr int kWaves = kWM * kWN, kThreads = kWaves * kWave;  // of one group
     constexpr int kMt = kTM / kWM / 16, kNt = kTN / kWN / 16;
@@ -385,18 +385,20 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
         kGated ? f8_rsrc(m.wq[1] + m0 * m.ldw, (uint32_t)((rows - 1) * m.ldw + nb * kF8Block)) : rw;
     const __amdgpu_buffer_rsrc_t rx = f8_rsrc(m.xq + t0 * m.ldx, (uint32_t)((toks - 1) * m.ldx + nb * kF8Block));
 
-    // sources of this lane's copies: wave w copies rows 8 kAi w .. of A and 8 kBi w .. of B
-    uint32_t ao[kAi], bo[kBi];
-#pragma unroll
-    for (int i = 0; i < kAi; ++i) {
-        const int r = 8 * (kAi * w + i) + lane / 8, rr = kGated ? r % kRows : r;
-        ao[i] = rr < rows ? (uint32_t)(rr * m.ldw + 16 * ((lane % 8) ^ f8_swizzle(r))) : kF8Out;
-    }
-#pragma unroll
-    for (int i = 0; i < kBi; ++i) {
-        const int r = 8 * (kBi * w + i) + lane / 8;
-        bo[i] = r < toks ? (uint32_t)(r * m.ldx + 16 * ((lane % 8) ^ f8_swizzle(r))) : kF8Out;
-    }
+    // Sources of this lane's copies: wave w copies rows 8 kAi w .. of A and 8 kBi
+    // w .. of B, eight an instruction.  Every second instruction has the same
+    // swizzle, so the first two offsets lead to all.  Rows past the last need no
+    // test: a row's stride covers what is read of it, so they lie past the end
+    // of the buffer, and load zero.
+    auto source = [&](int r, int64_t ld) { return (uint32_t)(r * ld + 16 * ((lane % 8) ^ f8_swizzle(r))); };
+    const int ar = 8 * kAi * w % kRows + lane / 8, br = 8 * kBi * w + lane / 8;
+    const uint32_t ao[2] = {source(ar, m.ldw), source(ar + 8, m.ldw)};
+    const uint32_t bo[2] = {source(br, m.ldx), source(br + 8, m.ldx)};
+    auto advance = [](uint32_t off, int64_t ld, int c) {
+        uint32_t by = (uint32_t)(16 * (c / 2) * ld);
+        if (!kCarry) asm volatile("" : "+s"(by));  // added where it is used: kept over the loop, the sums cost registers
+        return c < 2 ? off : off + by;
+    };
     const int sr = 64 * (w % (kTN / 64));  // this wave's run of token scales
     const uint32_t so = sr + lane < toks ? (uint32_t)(4 * (sr + lane)) : kF8Out;
     const bool up = kGated && w >= kWaves / 2;  // rows of the up matrix (whole waves)
@@ -405,8 +407,8 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
     auto copy = [&](uint8_t* st, int i, int c) {
         const int b = min(i * kSplit + group, nb - 1);
         const uint32_t ko = (uint32_t)(b * kF8Block);
-        if (c < kAi) copy16(up ? ru : rw, st + (base + 1024 * (kAi * w + c)), ao[c < kAi ? c : 0], ko);
-        else if (c < kAi + kBi) copy16(rx, st + (base + kABytes + 1024 * (kBi * w + c - kAi)), bo[c < kAi + kBi ? c - kAi : 0], ko);
+        if (c < kAi) copy16(up ? ru : rw, st + (base + 1024 * (kAi * w + c)), advance(ao[c % 2], m.ldw, c), ko);
+        else if (c < kAi + kBi) copy16(rx, st + (base + kABytes + 1024 * (kBi * w + c - kAi)), advance(bo[(c - kAi) & 1], m.ldx, c - kAi), ko);
         else {
             const __amdgpu_buffer_rsrc_t rs = f8_rsrc(m.xs + b * m.ldxs + t0, (uint32_t)(4 * toks));
             copy4(rs, reinterpret_cast<float*>(st + (base + kABytes + kBBytes + 4 * sr)), so, 0);
@@ -438,7 +440,8 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
     };
 
     // What a step starts with, read from its stage while the step before ends:
-    // the token fragments, the first weight fragment and the token scales.
+    // the token fragments, the first weight fragment (kEarly; otherwise as the
+    // step begins, for want of registers) and the token scales.
     constexpr int kMats = kGated ? 2 : 1, kPer = kChannels ? 4 : 1;  // a lane holds one token, or four of a channel
     typedef typename Operand<kHalf>::type op_t;
     op_t bf[kNt];
@@ -453,7 +456,7 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
                     st + (base + kABytes + kBBytes + 4 * ((wn * kNt + j) * 16 + (kChannels ? 4 * kg + e : l16))));
     };
     // products that are still to be scaled and added: two MFMAs old when that
-    // happens, the last two of a step in the next one
+    // happens, the last two of a step in the next one (kCarry)
     float4v late[2];
     float late_s[2][kPer];
 #pragma unroll
@@ -485,7 +488,12 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
                 sc[0][j][e] = sx[j][e] * sw;
                 if (kGated) sc[kMats - 1][j][e] = sx[j][e] * su;
             }
-        int8v nraw[kNt];
+        int8v nraw[kEarly ? kNt : 1];
+        if (!kEarly) {
+            raw = rows_fragment(st, 0);
+#pragma unroll
+            for (int j = 0; j < kNt; ++j) bf[j] = Operand<kHalf>::of(toks_fragment(st, j));
+        }
 #pragma unroll
         for (int i = 0; i < kMt; ++i) {
             const op_t af = Operand<kHalf>::of(raw);
@@ -502,8 +510,8 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
 #pragma unroll
-                for (int j = 0; j < kNt; ++j) nraw[j] = toks_fragment(nx, j);
-                raw = rows_fragment(nx, 0);
+                for (int j = 0; kEarly && j < kNt; ++j) nraw[kEarly ? j : 0] = toks_fragment(nx, j);
+                if (kEarly) raw = rows_fragment(nx, 0);
                 if (!kChannels) read_scales(nx);  // four times as many: too many registers to hold ahead
 #pragma unroll
                 for (int c = 0; c < kPre; ++c) copy(st, b + 1 + kAhead, c);
@@ -514,13 +522,18 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
                 const int g = kGated && i >= kMt / 2 ? kMats - 1 : 0;
                 const int q = i * kNt + j;
                 // the one two back: of this step or, for its first two, of the step before
-                add(q >= 2 ? acc[(q - 2) / kNt][(q - 2) % kNt] : acc[kMt - 1][kNt - 2 + q], late[q % 2], late_s[q % 2]);
+                if (kCarry || q >= 2)
+                    add(q >= 2 ? acc[(q - 2) / kNt][(q - 2) % kNt] : acc[kMt - 1][kNt - 2 + q], late[q % 2], late_s[q % 2]);
                 late[q % 2] = p;
 #pragma unroll
                 for (int e = 0; e < kPer; ++e) late_s[q % 2][e] = sc[g][j][e];
-                if (i == kMt - 1) bf[j] = Operand<kHalf>::of(nraw[j]);
+                if (kEarly && i == kMt - 1) bf[j] = Operand<kHalf>::of(nraw[kEarly ? j : 0]);
             }
             __builtin_amdgcn_sched_barrier(0);  // left alone, the scheduler reads every fragment first and spills
+        }
+        if (!kCarry) {
+            add(acc[kMt - 1][kNt - 2], late[0], late_s[0]);
+            add(acc[kMt - 1][kNt - 1], late[1], late_s[1]);
         }
     };
     if (nb > 0) {
@@ -562,8 +575,10 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
             if (i < run) go(lds0, lds1, last, i);
             if (kStages > 2 && i + 1 < run) go(lds1, after1, lds0, i + 1);
         }
-        add(acc[kMt - 1][kNt - 2], late[0], late_s[0]);
-        add(acc[kMt - 1][kNt - 1], late[1], late_s[1]);
+        if (kCarry) {
+            add(acc[kMt - 1][kNt - 2], late[0], late_s[0]);
+            add(acc[kMt - 1][kNt - 1], late[1], late_s[1]);
+        }
     }
     // copies still in flight would land in memory that the epilogue (or the
     // next workgroup) uses
@@ -692,7 +707,7 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
     }
 }
 
-template <typename T, int kTM, int kTN, int kWM, int kWN, int kStages, bool kGated, bool kHalf, int kSplit = 1>
+template <typename T, int kTM, int kTN, int kWM, int kWN, int kStages, bool kGated, bool kHalf, int kSplit = 1, bool kEarly = true, bool kCarry = true>
 hipError_t tile_launch(TileArgs a, TimedLaunch t, hipStream_t s) {
     constexpr int kRows = kGated ? kTM / 2 : kTM;
     a.mt = (unsigned)((a.m.M + kRows - 1) / kRows);
@@ -700,9 +715,9 @@ hipError_t tile_launch(TileArgs a, TimedLaunch t, hipStream_t s) {
     a.wide = a.m.ldy * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(a.m.y) % 16 == 0;
     const dim3 grid(a.mt * a.nt), block(kSplit * kWM * kWN * kWave);
     if (!kGated && a.m.channel_major)
-        GPTQ_LAUNCH(t, (f8_tile_kernel<T, kTM, kTN, kWM, kWN, kStages, kSplit, kGated, kHalf, !kGated>), grid, block, 0, s, a);
+        GPTQ_LAUNCH(t, (f8_tile_kernel<T, kTM, kTN, kWM, kWN, kStages, kSplit, kGated, kHalf, !kGated, kEarly, kCarry && kTN < 256>), grid, block, 0, s, a);
     else
-        GPTQ_LAUNCH(t, (f8_tile_kernel<T, kTM, kTN, kWM, kWN, kStages, kSplit, kGated, kHalf, false>), grid, block, 0, s, a);
+        GPTQ_LAUNCH(t, (f8_tile_kernel<T, kTM, kTN, kWM, kWN, kStages, kSplit, kGated, kHalf, false, kEarly, kCarry>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
@@ -719,9 +734,8 @@ bool f8_few(int64_t n, int64_t M) { return n <= kFewTokens || (n <= kSomeTokens 
 // times the measured time of a round and block.  us a block with every CU at
 // work: e4m3 MFMA 256 x 256 2.0, 256 x 128 1.2, 128 x 128 0.68, 128 x 64 with
 // two groups of waves sharing k 0.43, 64 x 64 0.31 (one a CU, two groups), 0.52
-// (two a CU), 0.80 (three); float16 MFMA 256 x 128 2.1, 128 x 128 1.38 (one a
-// CU), 2.3 (two), 128 x 64 in two groups 0.68, 64 x 64 0.47 (one, two groups),
-// 0.88, 1.45.  At 4096 x 4096 weights, e4m3: 256 tokens 10.7 us in 64 x 64
+// (two a CU), 0.80 (three); float16 MFMA 256 x 128 2.1, 128 x 64 in two groups
+// 0.68, 64 x 64 0.47 (one, two groups), 0.88, 1.45.  At 4096 x 4096 weights, e4m3: 256 tokens 10.7 us in 64 x 64
 // tiles (13.4 in one group), 13.4 in 128 x 64, 29 in 256 x 128; 512 tokens
 // 14.6 in 128 x 64, 16.5 in 64 x 64; 1024 tokens 22 in 128 x 128, 28 in 128 x
 // 64, 31 in 256 x 128; 4096 tokens 66 in 256 x 256, 76 in 256 x 128, 112 in 64
@@ -739,12 +753,10 @@ hipError_t matmul_typed(const MmArgs& m, hipStream_t s) {
     const bool one = rounds(64, 64, 1) == 1, two = rounds(64, 64, 2) == 1;
     if constexpr (kHalf) {
         const double t64 = one ? 0.47 : two ? 0.88 : 1.45 * rounds(64, 64, 3), t96 = 0.68 * rounds(128, 64, 1);
-        const double t128 = rounds(128, 128, 1) == 1 ? 1.38 : 2.3 * rounds(128, 128, 2);
-        const double t256 = 2.1 * rounds(256, 128, 1), least = std::min(std::min(t64, t96), std::min(t128, t256));
+        const double t256 = 2.1 * rounds(256, 128, 1), least = std::min(std::min(t64, t96), t256);
         if (t64 == least && one) return tile_launch<T, 64, 64, 2, 2, 3, false, true, 2>(a, t, s);
         if (t64 == least) return tile_launch<T, 64, 64, 2, 2, 3, false, true>(a, t, s);
         if (t96 == least) return tile_launch<T, 128, 64, 2, 2, 3, false, true, 2>(a, t, s);
-        if (t128 == least) return tile_launch<T, 128, 128, 2, 2, 2, false, true>(a, t, s);
         return tile_launch<T, 256, 128, 4, 2, 2, false, true>(a, t, s);
     } else {
         const double t64 = one ? 0.31 : two ? 0.52 : 0.80 * rounds(64, 64, 3), t96 = 0.43 * rounds(128, 64, 1);
@@ -775,10 +787,13 @@ size_t f8_gated_workspace_bytes(int64_t n, int64_t d_ff) {
 }
 
 // Up to 32 tokens: the few-token kernel leaves the products in float32 and the
-// activations' quantizer writes them in 8 bits (11008 channels, 32 tokens: 26
-// us, the tile kernel 36; 64 tokens: 37 against 36).  More: the tile kernel,
-// 64 tokens wide while that leaves CUs idle (128 tokens 39 us against 60 us
-// 128 wide; 256 tokens 69 against 61).
+// activations' quantizer writes them in 8 bits (11008 channels, 32 tokens: 24
+// us, the tile kernel 36).  More: the tile kernel, as wide as makes rounds of
+// tiles over the CUs times a round's time least: 1.16 us a block of k for 64
+// tokens, 1.9 for 128, 3.3 for 256 (11008 channels, k 4096: 128 tokens 40, 61
+// and 106 us, 1024 tokens 208, 174 and 204, 4096 tokens 776, 640 and 616).
+// At 256 tokens a wave converts fewer values for its products (160 an m-tile
+// and token tile against 192), but holds no registers for fragments ahead.
 hipError_t launch_f8_gated(const F8Product& c, uint8_t* q, int64_t ldq, float* scales, int64_t lds, void* ws,
                            hipStream_t s) {
     if (c.n > kFewTokens) {
@@ -790,9 +805,13 @@ hipError_t launch_f8_gated(const F8Product& c, uint8_t* q, int64_t ldq, float* s
         t.ldq = ldq;
         t.ldqs = lds;
         const TimedLaunch k(K_F8_GATED, s);
-        if (((c.M + kF8Block - 1) / kF8Block) * ((c.n + 63) / 64) <= device_cu_count())
-            return tile_launch<float, 256, 64, 4, 2, 3, true, true>(t, k, s);
-        return tile_launch<float, 256, 128, 4, 2, 2, true, true>(t, k, s);
+        const int64_t cus = device_cu_count(), blocks = (c.M + kF8Block - 1) / kF8Block;
+        if (cus <= 0) return hipErrorInvalidDevice;
+        auto rounds = [&](int64_t tn) { return (blocks * ((c.n + tn - 1) / tn) + cus - 1) / cus; };
+        const double t64 = 1.16 * rounds(64), t128 = 1.9 * rounds(128), t256 = 3.3 * rounds(256);
+        if (t64 <= t128 && t64 <= t256) return tile_launch<float, 256, 64, 4, 2, 3, true, true>(t, k, s);
+        if (t128 <= t256) return tile_launch<float, 256, 128, 4, 2, 2, true, true>(t, k, s);
+        return tile_launch<float, 256, 256, 2, 4, 2, true, true, 1, false, false>(t, k, s);
     }
     const int64_t ldh = (c.M + kF8Block - 1) / kF8Block * kF8Block;
     MmArgs a = {{c.wq[0], c.wq[1]}, {c.ws[0], c.ws[1]}, c.xq, c.xs, ws, c.ldw, c.ldws, c.ldx, c.ldxs, ldh, c.M, c.n,
