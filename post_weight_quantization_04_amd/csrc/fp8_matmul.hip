@@ -537,6 +537,17 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
         }
     };
     if (nb > 0) {
+        // the weight scales of kMany steps at a time, one a lane (the first ones
+        // ahead of the copies: loads return in order)
+        constexpr int kMany = 64 / kStages * kStages;
+        int wl, ul;
+        auto load_scales = [&](int i0) {
+            const int at = (i0 + lane) * kSplit + group;
+            wl = __builtin_bit_cast(int, at < nb ? wsr[at] : 0.0f);
+            ul = kGated ? __builtin_bit_cast(int, at < nb ? usr[at] : 0.0f) : 0;
+        };
+        load_scales(0);
+        asm volatile("" ::: "memory");
 #pragma unroll
         for (int d = 0; d < kAhead; ++d)
 #pragma unroll
@@ -552,13 +563,9 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
 #pragma unroll
         for (int c = 0; c < kPre; ++c) copy(last, kAhead, c);
 
-        // the weight scales of kMany steps at a time, one a lane
-        constexpr int kMany = 64 / kStages * kStages;
         for (int i0 = 0; i0 < steps; i0 += kMany) {
             const int run = min(kMany, steps - i0);
-            const int at = (i0 + lane) * kSplit + group;
-            const int wl = __builtin_bit_cast(int, at < nb ? wsr[at] : 0.0f);
-            const int ul = kGated ? __builtin_bit_cast(int, at < nb ? usr[at] : 0.0f) : 0;
+            if (i0 > 0) load_scales(i0);
             auto go = [&](uint8_t* st, uint8_t* nx, uint8_t* to, int i) {
                 step(st, nx, to, i0 + i, __builtin_bit_cast(float, __builtin_amdgcn_readlane(wl, i)),
                      kGated ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(ul, i)) : 0.0f);
