@@ -441,7 +441,7 @@ int gptq_obq_quantize(const void* W, int w_dtype, int64_t d_out, int64_t d_in, c
  *           [ceil(d_out/128), lds].
  * Errors: GPTQ_EINVAL (negative size, ldw < d_in, ldq or lds too small,
  * unknown dtype, null pointer), GPTQ_EUNSUPPORTED (q or ldq not 16-byte
- * aligned, d_out or d_in above 2^24, 2^31 blocks or more).
+ * aligned, d_out or d_in above 2^24, 2^24 blocks or more).
  */
 int gptq_fp8_weight(const void* W, int w_dtype, int64_t d_out, int64_t d_in, int64_t ldw, uint8_t* q,
                     int64_t ldq, float* scales, int64_t lds, void* stream);
@@ -452,8 +452,9 @@ int gptq_fp8_weight(const void* W, int w_dtype, int64_t d_out, int64_t d_in, int
  *           the calibration inputs), of x_dtype, row stride ldx elements.
  *   q, scales  the outputs: values [n_tokens, ldq], scales [ceil(d/128), lds].
  * Errors: as gptq_fp8_weight, and GPTQ_EINVAL for channel_major not 0 or 1;
- * the limits are n_tokens below 2^31, d at most 2^24 and fewer than 2^31
- * (token, block) pairs.
+ * the limits are n_tokens below 2^31, d at most 2^24 and fewer than 2^28
+ * (token, block of 128) pairs (channel_major: 2^24 pieces of 128 channels by
+ * 64 tokens).
  */
 int gptq_fp8_activations(const void* X, int x_dtype, int64_t n_tokens, int64_t d, int64_t ldx, int channel_major,
                          uint8_t* q, int64_t ldq, float* scales, int64_t lds, void* stream);
@@ -476,7 +477,7 @@ int gptq_fp8_activations(const void* X, int x_dtype, int64_t n_tokens, int64_t d
  * Errors: GPTQ_EINVAL (negative size, a row stride below d, ldq or lds too
  * small, unknown dtype, eps outside its range or NaN, sum_out without
  * residual, null pointer), GPTQ_EUNSUPPORTED (q or ldq not 16-byte aligned,
- * d above 2^24, n_tokens above 2^31 - 1).
+ * d above 2^24, n_tokens of 2^23 or more).
  */
 int gptq_fp8_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* sum_out, int64_t ldo,
                       const void* gain, int dtype, int64_t n_tokens, int64_t d, double eps, uint8_t* q,
@@ -503,7 +504,7 @@ int gptq_fp8_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t 
  * Errors: GPTQ_EINVAL (negative size, a stride too small, unknown dtype,
  * activation or channel_major, null pointer), GPTQ_EUNSUPPORTED (xq, wq or
  * their strides not 16-byte aligned, a value stride above 2^22 (so d_in too),
- * d_out or n_tokens above 2^24, 2^31 or more 64 x 64 tiles of Y).
+ * d_out or n_tokens above 2^24, more than 2^22 256 x 256 tiles of Y).
  */
 int gptq_fp8_matmul(const uint8_t* wq, int64_t ldwq, const float* ws, int64_t ldws, int64_t d_out, int64_t d_in,
                     const uint8_t* xq, int64_t ldxq, const float* xs, int64_t ldxs, int64_t n_tokens, void* Y,
@@ -522,7 +523,8 @@ int gptq_fp8_matmul(const uint8_t* wq, int64_t ldwq, const float* ws, int64_t ld
  *   workspace device memory of at least gptq_fp8_gated_workspace(n_tokens,
  *             d_ff) bytes (0 for many tokens: then it may be NULL), 256-byte
  *             aligned; clobbered.
- * Errors: as gptq_fp8_matmul, and GPTQ_EWORKSPACE.
+ * Errors: as gptq_fp8_matmul (more than 2^22 tiles of 128 channels by 256
+ * tokens), and GPTQ_EWORKSPACE.
  */
 size_t gptq_fp8_gated_workspace(int64_t n_tokens, int64_t d_ff);
 int gptq_fp8_gated(const uint8_t* gq, const float* gs, const uint8_t* uq, const float* us, int64_t ldwq,

@@ -363,6 +363,11 @@ inline bool f8_short(int64_t ldq, int64_t d, int64_t lds, int64_t along) {
 }
 constexpr int64_t kF8MaxLd = (int64_t)1 << 22;  // 256 rows of a tile stay within 2^30 bytes
 constexpr int64_t kF8MaxRows = (int64_t)1 << 24;
+// a launch has fewer than 2^32 threads: 16 a (token, block) pair, 256 a block
+// of weights or 128 x 64 piece of channel-major activations, up to 512 a
+// normed row, 512 a 256 x 256 tile
+constexpr int64_t kF8MaxPairs = ((int64_t)1 << 28) - 1, kF8MaxPieces = ((int64_t)1 << 24) - 1;
+constexpr int64_t kF8MaxNormRows = ((int64_t)1 << 23) - 1, kF8MaxTiles = (int64_t)1 << 22;
 }  // namespace
 
 int gptq_fp8_weight(const void* W, int w_dtype, int64_t d_out, int64_t d_in, int64_t ldw, uint8_t* q, int64_t ldq,
@@ -372,7 +377,7 @@ int gptq_fp8_weight(const void* W, int w_dtype, int64_t d_out, int64_t d_in, int
     if (d_out == 0 || d_in == 0) return GPTQ_OK;
     if (!W || !q || !scales) return GPTQ_EINVAL;
     if (!f8_aligned(q, ldq) || d_out > kF8MaxRows || d_in > ((int64_t)1 << 24)) return GPTQ_EUNSUPPORTED;
-    if (f8_blocks(d_out) * f8_blocks(d_in) > (int64_t)INT32_MAX) return GPTQ_EUNSUPPORTED;
+    if (f8_blocks(d_out) * f8_blocks(d_in) > kF8MaxPieces) return GPTQ_EUNSUPPORTED;
     return hip_status(launch_f8_weight(W, w_dtype, d_out, d_in, ldw, q, ldq, scales, lds, as_stream(stream)));
 }
 
@@ -383,7 +388,8 @@ int gptq_fp8_activations(const void* X, int x_dtype, int64_t n, int64_t d, int64
     if (n == 0 || d == 0) return GPTQ_OK;
     if (!X || !q || !scales) return GPTQ_EINVAL;
     if (!f8_aligned(q, ldq) || n > (int64_t)INT32_MAX || d > ((int64_t)1 << 24)) return GPTQ_EUNSUPPORTED;
-    if (n * f8_blocks(d) > (int64_t)INT32_MAX) return GPTQ_EUNSUPPORTED;
+    if (channel_major ? ((n + 63) / 64) * f8_blocks(d) > kF8MaxPieces : n * f8_blocks(d) > kF8MaxPairs)
+        return GPTQ_EUNSUPPORTED;
     return hip_status(
         launch_f8_activations(X, x_dtype, n, d, ldx, channel_major, q, ldq, scales, lds, as_stream(stream)));
 }
@@ -396,7 +402,7 @@ int gptq_fp8_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t 
     if (!(eps >= 1e-20 && eps <= 1e20) || f8_short(ldq, d, lds, n)) return GPTQ_EINVAL;
     if (n == 0 || d == 0) return GPTQ_OK;
     if (!x || !gain || !q || !scales) return GPTQ_EINVAL;
-    if (!f8_aligned(q, ldq) || n > (int64_t)INT32_MAX || d > ((int64_t)1 << 24)) return GPTQ_EUNSUPPORTED;
+    if (!f8_aligned(q, ldq) || n > kF8MaxNormRows || d > ((int64_t)1 << 24)) return GPTQ_EUNSUPPORTED;
     const RmsNormCall c = {x, residual, gain, sum_out, q, scales, ldx, ldr, ldo, ldq, lds, n, d, eps};
     return hip_status(launch_f8_rms_norm(c, dtype, as_stream(stream)));
 }
@@ -413,7 +419,7 @@ int gptq_fp8_matmul(const uint8_t* wq, int64_t ldwq, const float* ws, int64_t ld
     if (d_in > 0 && (!f8_aligned(wq, ldwq) || !f8_aligned(xq, ldxq))) return GPTQ_EUNSUPPORTED;
     if (ldwq > kF8MaxLd || ldxq > kF8MaxLd) return GPTQ_EUNSUPPORTED;
     if (d_out > kF8MaxRows || n > kF8MaxRows) return GPTQ_EUNSUPPORTED;
-    if (((d_out + 63) / 64) * ((n + 63) / 64) > (int64_t)INT32_MAX) return GPTQ_EUNSUPPORTED;
+    if (((d_out + 255) / 256) * ((n + 255) / 256) > kF8MaxTiles) return GPTQ_EUNSUPPORTED;
     const F8Product c = {{wq, nullptr}, {ws, nullptr}, xq, xs, Y, ldwq, ldws, ldxq, ldxs, ldy, d_out, d_in, n,
                          channel_major, activation};
     return hip_status(launch_f8_matmul(c, y_dtype, as_stream(stream)));
@@ -436,7 +442,7 @@ int gptq_fp8_gated(const uint8_t* gq, const float* gs, const uint8_t* uq, const 
     if (d_in > 0 && (!f8_aligned(gq, ldwq) || !f8_aligned(uq, ldwq) || !f8_aligned(xq, ldxq))) return GPTQ_EUNSUPPORTED;
     if (!f8_aligned(q, ldq)) return GPTQ_EUNSUPPORTED;
     if (ldwq > kF8MaxLd || ldxq > kF8MaxLd || d_ff > kF8MaxRows || n > kF8MaxRows) return GPTQ_EUNSUPPORTED;
-    if (n * f8_blocks(d_ff) > (int64_t)INT32_MAX) return GPTQ_EUNSUPPORTED;
+    if (f8_blocks(d_ff) * ((n + 255) / 256) > kF8MaxTiles) return GPTQ_EUNSUPPORTED;
     const size_t need = f8_gated_workspace_bytes(n, d_ff);
     if (need > 0 && (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256 != 0))
         return GPTQ_EWORKSPACE;

@@ -29,16 +29,27 @@ class Quantized:
 
 
 class Workspace:
-    """Grow-only device scratch buffer shared by the calls of one stream."""
+    """Grow-only device scratch buffer shared by the calls of one stream.
+
+    A buffer that a captured graph uses is kept when the workspace grows: the
+    graph goes on writing to it whenever it is replayed.  Replays and calls
+    that share a workspace have to run one after the other."""
 
     def __init__(self, device="cuda"):
         self.device = device
         self.buf = None
+        self._captured = False  # handed out while a graph was being captured
+        self._kept = []
 
     def get(self, nbytes: int):
         import torch
         if self.buf is None or self.buf.numel() < nbytes:
+            if self._captured:
+                self._kept.append(self.buf)
+                self._captured = False
             self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+        if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+            self._captured = True
         return self.buf
 
 

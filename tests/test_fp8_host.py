@@ -44,7 +44,7 @@ def test_weight_refusals(clib):
                 dict(W=None), dict(q=None), dict(s=None)):
         assert weight(clib, **bad) == EINVAL, bad
     for bad in (dict(q=ODD), dict(ldq=264), dict(m=(1 << 24) + 1), dict(k=(1 << 24) + 1, ldw=1 << 25, ldq=1 << 25, lds=1 << 20),
-                dict(m=1 << 24, k=1 << 24, ldw=1 << 24, ldq=1 << 24, lds=1 << 20)):
+                dict(m=1 << 19, k=1 << 19, ldw=1 << 19, ldq=1 << 19, lds=1 << 12)):
         assert weight(clib, **bad) == EUNSUPPORTED, bad
     assert weight(clib, m=0, W=None, q=None, s=None) == OK
     assert weight(clib, k=0, W=None, q=None, s=None, ldw=0, ldq=0, lds=0) == OK
@@ -58,7 +58,8 @@ def test_activations_refusals(clib):
     for bad in (dict(n=-1), dict(d=-1), dict(ldx=199), dict(cm=1, ldx=7), dict(cm=2), dict(ldq=255), dict(lds=7), dict(dt=3),
                 dict(X=None), dict(q=None), dict(s=None)):
         assert acts(clib, **bad) == EINVAL, bad
-    for bad in (dict(q=ODD), dict(ldq=264), dict(n=1 << 31, lds=1 << 31), dict(n=1 << 30, lds=1 << 30)):
+    for bad in (dict(q=ODD), dict(ldq=264), dict(n=1 << 31, lds=1 << 31), dict(n=1 << 27, lds=1 << 27),
+                dict(n=1 << 29, lds=1 << 29, ldx=1 << 29, cm=1)):
         assert acts(clib, **bad) == EUNSUPPORTED, bad
     assert acts(clib, n=0, X=None, q=None, s=None) == OK
 
@@ -73,7 +74,7 @@ def test_rms_norm_refusals(clib):
                 dict(eps=1e-21), dict(eps=nan), dict(eps=inf), dict(ldq=255), dict(lds=7), dict(dt=3), dict(x=None),
                 dict(g=None), dict(q=None), dict(s=None)):
         assert norm(clib, **bad) == EINVAL, bad
-    for bad in (dict(q=ODD), dict(ldq=264), dict(n=1 << 31, lds=1 << 31)):
+    for bad in (dict(q=ODD), dict(ldq=264), dict(n=1 << 23, lds=1 << 23)):
         assert norm(clib, **bad) == EUNSUPPORTED, bad
     assert norm(clib, n=0, x=None, g=None, q=None, s=None) == OK
 
@@ -106,7 +107,8 @@ def test_gated_refusals(clib):
                 dict(ldq=130), dict(lds=4), dict(q=None), dict(s=None), dict(gq=None), dict(gs=None), dict(uq=None),
                 dict(us=None), dict(xq=None), dict(xs=None)):
         assert gated(clib, **bad) == EINVAL, bad
-    for bad in (dict(gq=ODD), dict(uq=ODD), dict(xq=ODD), dict(q=ODD), dict(ldw=264), dict(ldx=264), dict(ldq=264)):
+    for bad in (dict(gq=ODD), dict(uq=ODD), dict(xq=ODD), dict(q=ODD), dict(ldw=264), dict(ldx=264), dict(ldq=264),
+                dict(m=1 << 24, n=1 << 24, ldq=1 << 24, ldxs=1 << 24, lds=1 << 24)):
         assert gated(clib, **bad) == EUNSUPPORTED, bad
     need = clib.gptq_fp8_gated_workspace(5, 130)
     assert need > 0
