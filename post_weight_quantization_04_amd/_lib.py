@@ -120,6 +120,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    _fp8_names()
     _lib = lib
     return lib
 
@@ -324,22 +325,27 @@ def obq_quantize(W, U, dead, bits: int, codes, scales, zeros, order=None, loss=N
 #
 # One decoded token's kernel takes 3 to 6 us, so these calls are written to
 # cost the host less: tensors are read once each, by the accessors that do not
-# build new objects.
+# build new objects, and the names used by every call are set by load().
 # ---------------------------------------------------------------------------
-_fp8_torch = None  # set by the first call: (type codes, 8-bit types, float32, current device, its current stream)
+_fp8_codes = {}          # torch type -> gptq_dtype
+_fp8_eights = ()         # types of the 8-bit values
+_fp8_scale = None        # type of the scales
+_fp8_current = None      # () -> index of the current device
+_fp8_current_stream = None  # (device index) -> handle of its current stream
 
 
-def _fp8_types():
-    global _fp8_torch
+def _fp8_names() -> None:
+    global _fp8_codes, _fp8_eights, _fp8_scale, _fp8_current, _fp8_current_stream
     import torch
-    _fp8_torch = ({torch.float16: GPTQ_F16, torch.float32: GPTQ_F32, torch.bfloat16: GPTQ_BF16},
-                  (torch.float8_e4m3fn, torch.uint8), torch.float32, torch._C._cuda_getDevice,
-                  torch._C._cuda_getCurrentRawStream)
-    return _fp8_torch
+    _fp8_codes = {torch.float16: GPTQ_F16, torch.float32: GPTQ_F32, torch.bfloat16: GPTQ_BF16}
+    _fp8_eights = (torch.float8_e4m3fn, torch.uint8)
+    _fp8_scale = torch.float32
+    _fp8_current = torch._C._cuda_getDevice
+    _fp8_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _fp8_dtype(t) -> int:
-    code = (_fp8_torch or _fp8_types())[0].get(t.dtype)
+    code = _fp8_codes.get(t.dtype)
     if code is None:
         raise ValueError(f"unsupported dtype {t.dtype}")
     return code
@@ -351,15 +357,14 @@ def _fp8_device(t) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError("device tensor expected")
-    current = (_fp8_torch or _fp8_types())[3]()
-    if dev != current:
-        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{current}")
+    if dev != _fp8_current():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{_fp8_current()}")
     return dev
 
 
 def _fp8_stream(dev: int, stream) -> int:
     if stream is None:
-        return (_fp8_torch or _fp8_types())[4](dev)
+        return _fp8_current_stream(dev)
     if stream.device.index != dev:
         raise ValueError(f"tensors on cuda:{dev}, stream on {stream.device}")
     return stream.cuda_stream
@@ -380,27 +385,33 @@ def _fp8_operand(values, scales, cols: int, by_row: bool, dev: int, what: str):
     """(values pointer, ld, scales pointer, lds, rows) of an 8-bit matrix of
     ``cols`` columns: a scale per row and 128 columns (``by_row``), or per 128
     x 128 block."""
-    _, eights, f32, _, _ = _fp8_torch or _fp8_types()
-    if values.dtype not in eights or scales.dtype != f32:
-        raise ValueError(f"{what}: values must be float8_e4m3fn, scales float32")
-    vp, ld, rows, held = _fp8_matrix(values, dev, what)
-    sp, lds, lead, along = _fp8_matrix(scales, dev, what)
+    shape, stride, sshape, sstride = values.shape, values.stride(), scales.shape, scales.stride()
+    if (values.dtype not in _fp8_eights or scales.dtype != _fp8_scale or len(shape) != 2 or len(sshape) != 2
+            or values.get_device() != dev or scales.get_device() != dev or (stride[1] != 1 and shape[1] > 1)
+            or (sstride[1] != 1 and sshape[1] > 1)):
+        raise ValueError(f"{what}: values must be a 2-D float8_e4m3fn view and scales a 2-D float32 view on cuda:{dev}, "
+                         f"both with unit column stride")
+    rows, held = shape
+    lead, along = sshape
     nb = (cols + 127) >> 7
     if held < nb << 7:
         raise ValueError(f"{what}: {held} stored columns hold fewer than {cols} rounded up to 128")
     if (lead < nb or along < rows) if by_row else (lead < (rows + 127) >> 7 or along < nb):
         raise ValueError(f"{what}: scales {(lead, along)} for {rows} x {cols}")
-    return vp, ld, sp, lds, rows
+    # (single rows: as above)
+    return (values.data_ptr(), stride[0] if rows > 1 else max(stride[0], held), scales.data_ptr(),
+            sstride[0] if lead > 1 else max(sstride[0], along), rows)
 
 
 def fp8_weight(W, values, scales, stream=None) -> None:
     """``W [d_out, d_in]`` to 8 bits, a scale per 128 x 128 block."""
+    lib = _lib or load()
     dev = _fp8_device(W)
     wp, ldw, d_out, d_in = _fp8_matrix(W, dev, "W")
     vp, ld, sp, lds, rows = _fp8_operand(values, scales, d_in, False, dev, "out")
     if rows != d_out:
         raise ValueError("rows of the output")
-    rc = load().gptq_fp8_weight(wp, _fp8_dtype(W), d_out, d_in, ldw, vp, ld, sp, lds, _fp8_stream(dev, stream))
+    rc = lib.gptq_fp8_weight(wp, _fp8_dtype(W), d_out, d_in, ldw, vp, ld, sp, lds, _fp8_stream(dev, stream))
     if rc:
         _check("gptq_fp8_weight", rc)
 
@@ -408,6 +419,7 @@ def fp8_weight(W, values, scales, stream=None) -> None:
 def fp8_activations(X, values, scales, channel_major: bool = False, stream=None) -> None:
     """``X [n, d]`` (or ``[d, n]`` with ``channel_major``) to 8 bits, a scale
     per token and 128 channels."""
+    lib = _lib or load()
     dev = _fp8_device(X)
     xp, ldx, n, d = _fp8_matrix(X, dev, "X")
     if channel_major:
@@ -415,8 +427,8 @@ def fp8_activations(X, values, scales, channel_major: bool = False, stream=None)
     vp, ld, sp, lds, rows = _fp8_operand(values, scales, d, True, dev, "out")
     if rows != n:
         raise ValueError("rows of the output")
-    rc = load().gptq_fp8_activations(xp, _fp8_dtype(X), n, d, ldx, 1 if channel_major else 0, vp, ld, sp, lds,
-                                     _fp8_stream(dev, stream))
+    rc = lib.gptq_fp8_activations(xp, _fp8_dtype(X), n, d, ldx, 1 if channel_major else 0, vp, ld, sp, lds,
+                                  _fp8_stream(dev, stream))
     if rc:
         _check("gptq_fp8_activations", rc)
 
@@ -424,6 +436,7 @@ def fp8_activations(X, values, scales, channel_major: bool = False, stream=None)
 def fp8_rms_norm(x, gain, eps: float, values, scales, residual=None, sum_out=None, stream=None) -> None:
     """``h = x + residual``; ``h / sqrt(mean(h^2) + eps) * gain`` to 8 bits;
     ``sum_out = h``."""
+    lib = _lib or load()
     dev = _fp8_device(x)
     xp, ldx, n, d = _fp8_matrix(x, dev, "x")
     kind, shape = x.dtype, x.shape
@@ -441,8 +454,8 @@ def fp8_rms_norm(x, gain, eps: float, values, scales, residual=None, sum_out=Non
     vp, ld, sp, lds, rows = _fp8_operand(values, scales, d, True, dev, "out")
     if rows != n:
         raise ValueError("rows of the output")
-    rc = load().gptq_fp8_rms_norm(xp, ldx, rp, ldr, op, ldo, gain.data_ptr(), _fp8_dtype(x), n, d, eps, vp, ld, sp,
-                                  lds, _fp8_stream(dev, stream))
+    rc = lib.gptq_fp8_rms_norm(xp, ldx, rp, ldr, op, ldo, gain.data_ptr(), _fp8_dtype(x), n, d, eps, vp, ld, sp,
+                               lds, _fp8_stream(dev, stream))
     if rc:
         _check("gptq_fp8_rms_norm", rc)
 
@@ -450,14 +463,15 @@ def fp8_rms_norm(x, gain, eps: float, values, scales, residual=None, sum_out=Non
 def fp8_matmul(wq, ws, xq, xs, d_in: int, Y, channel_major: bool = False, activation: int = 0, stream=None) -> None:
     """``Y = act(X W^T)`` of 8-bit operands; ``Y [n, d_out]``, or ``[d_out,
     n]`` with ``channel_major``; activation 0 none, 1 ReLU."""
+    lib = _lib or load()
     dev = _fp8_device(Y)
     yp, ldy, y0, y1 = _fp8_matrix(Y, dev, "Y")
     wp, ldw, wsp, ldws, d_out = _fp8_operand(wq, ws, d_in, False, dev, "weights")
     xp, ldx, xsp, ldxs, n = _fp8_operand(xq, xs, d_in, True, dev, "activations")
     if (y0 != d_out or y1 != n) if channel_major else (y0 != n or y1 != d_out):
         raise ValueError("shape of Y")
-    rc = load().gptq_fp8_matmul(wp, ldw, wsp, ldws, d_out, d_in, xp, ldx, xsp, ldxs, n, yp, _fp8_dtype(Y), ldy,
-                                1 if channel_major else 0, activation, _fp8_stream(dev, stream))
+    rc = lib.gptq_fp8_matmul(wp, ldw, wsp, ldws, d_out, d_in, xp, ldx, xsp, ldxs, n, yp, _fp8_dtype(Y), ldy,
+                             1 if channel_major else 0, activation, _fp8_stream(dev, stream))
     if rc:
         _check("gptq_fp8_matmul", rc)
 
@@ -468,6 +482,7 @@ def fp8_gated_workspace(n: int, d_ff: int) -> int:
 
 def fp8_gated(gq, gs, uq, us, xq, xs, d_in: int, values, scales, workspace=None, stream=None) -> None:
     """``silu(X G^T) * (X U^T)`` of 8-bit operands, written in 8 bits."""
+    lib = _lib or load()
     dev = _fp8_device(values)
     gp, ldw, gsp, ldws, d_ff = _fp8_operand(gq, gs, d_in, False, dev, "gate")
     up, ldu, usp, ldus, up_rows = _fp8_operand(uq, us, d_in, False, dev, "up")
@@ -482,8 +497,8 @@ def fp8_gated(gq, gs, uq, us, xq, xs, d_in: int, values, scales, workspace=None,
         if workspace.get_device() != dev:
             raise ValueError("workspace on another device")
         room = workspace.numel() * workspace.element_size()
-    rc = load().gptq_fp8_gated(gp, gsp, up, usp, ldw, ldws, d_ff, d_in, xp, ldx, xsp, ldxs, n, vp, ld, sp, lds,
-                               _ptr(workspace), room, _fp8_stream(dev, stream))
+    rc = lib.gptq_fp8_gated(gp, gsp, up, usp, ldw, ldws, d_ff, d_in, xp, ldx, xsp, ldxs, n, vp, ld, sp, lds,
+                            _ptr(workspace), room, _fp8_stream(dev, stream))
     if rc:
         _check("gptq_fp8_gated", rc)
 

@@ -73,12 +73,14 @@ def quantize_tiles(w):
 
 
 def rows_values(codes, scales, d):
-    return (decode(codes) * np.repeat(scales.astype(np.float64).T, BLOCK, axis=1))[:, :d]
+    with np.errstate(invalid="ignore"):
+        return (decode(codes) * np.repeat(scales.astype(np.float64).T, BLOCK, axis=1))[:, :d]
 
 
 def tiles_values(codes, scales, d):
     s = np.repeat(np.repeat(scales.astype(np.float64), BLOCK, axis=0)[:codes.shape[0]], BLOCK, axis=1)
-    return (decode(codes) * s)[:, :d]
+    with np.errstate(invalid="ignore"):
+        return (decode(codes) * s)[:, :d]
 
 
 def cuts(n, m, dtype):
