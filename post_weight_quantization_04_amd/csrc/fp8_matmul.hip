@@ -286,15 +286,17 @@ hipError_t few_go(const MmArgs& a, TimedLaunch t, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Workgroups of the few-token kernel.
+int64_t f8_few_groups(int64_t n, int64_t M) { return ((M + 15) / 16) * ((n + 31) / 32); }
+
 // Eight waves share k where a workgroup has a CU to itself and blocks enough
-// for them, four otherwise (two workgroups a CU then hide each other's ends):
-// 11008 x 4096 weights, 24 tokens, 10.8 against 11.9 us; 4096 x 11008, one
-// token, 9.8 against 9.5 us, 24 tokens 14.4 against 11.7 us; both projections
-// of the gated block, one token, 22.2 against 18.9 us.
+// for them, four otherwise (two or three workgroups a CU then hide each other's
+// ends): 11008 x 4096 weights, 24 tokens, 10.8 against 11.9 us; 4096 x 11008,
+// one token, 9.8 against 9.5 us, 24 tokens 14.4 against 11.7 us; both
+// projections of the gated block, one token, 22.2 against 18.9 us.
 template <typename T, int kOctets, int kMats>
 hipError_t few_waves(const MmArgs& a, TimedLaunch t, hipStream_t s) {
-    if constexpr (kMats == 1)
-        if ((a.M + 15) / 16 <= device_cu_count() && a.nb >= 16) return few_go<T, 8, kOctets, kMats>(a, t, s);
+    if (f8_few_groups(a.n, a.M) <= device_cu_count() && a.nb >= 16) return few_go<T, 8, kOctets, kMats>(a, t, s);
     return few_go<T, 4, kOctets, kMats>(a, t, s);
 }
 
@@ -303,9 +305,7 @@ hipError_t few_launch(const MmArgs& a, TimedLaunch t, hipStream_t s) {
     if (a.n <= 8) return few_waves<T, 1, kMats>(a, t, s);
     if (a.n <= 16) return few_waves<T, 2, kMats>(a, t, s);
     if (a.n <= 24) return few_waves<T, 3, kMats>(a, t, s);
-    if (a.n <= 32) return few_waves<T, 4, kMats>(a, t, s);
-    if constexpr (kMats == 1) return few_waves<T, 8, kMats>(a, t, s);
-    return hipErrorInvalidValue;  // not reached: the gated block comes here with at most 32 tokens
+    return few_waves<T, 4, kMats>(a, t, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -330,7 +330,6 @@ struct TileArgs {
     float* qs;
     int64_t ldq, ldqs;
     unsigned mt, nt;  // tiles along the weight rows and the tokens
-    int wide;         // Y's lines may be stored 16 bytes at a time
 };
 
 constexpr int kXcd = 8;
@@ -689,25 +688,21 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
         const int line0 = kChannels ? wm * kWaveRows + 16 * o : (wn * kNt + o) * 16;
         const int count = (kChannels ? rows : toks) - line0;       // lines within Y
         T* base = y + ((kChannels ? m0 : t0) + line0) * m.ldy + start;
-        if (a.wide) {
-            constexpr int kPer = kRun / kVec;
+        // (16 bytes at a time; Y's lines need no more than their type's alignment)
+        constexpr int kPer = kRun / kVec;
 #pragma unroll
-            for (int q = 0; q < 16 * kPer / kWave; ++q) {
-                const int line = (q * kWave + lane) / kPer, at = (q * kWave + lane) % kPer * kVec;
-                const uint4v v = *reinterpret_cast<const uint4v*>(lines + line * kPitch + at * sizeof(T));
-                if (line >= count) continue;
-                if (at + kVec <= left) *reinterpret_cast<uint4v*>(base + line * m.ldy + at) = v;
-                else {
+        for (int q = 0; q < 16 * kPer / kWave; ++q) {
+            const int line = (q * kWave + lane) / kPer, at = (q * kWave + lane) % kPer * kVec;
+            const uint4v v = *reinterpret_cast<const uint4v*>(lines + line * kPitch + at * sizeof(T));
+            if (line >= count) continue;
+            T* o = base + line * m.ldy + at;
+            if (at + kVec <= left) __builtin_memcpy(o, &v, 16);
+            else {
+                T e[kVec];
+                __builtin_memcpy(e, &v, 16);
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e)
-                        if (at + e < left) base[line * m.ldy + at + e] = reinterpret_cast<const T*>(&v)[e];
-                }
-            }
-        } else {
-            for (int q = 0; q < 16 * kRun / kWave; ++q) {
-                const int line = (q * kWave + lane) / kRun, at = (q * kWave + lane) % kRun;
-                if (line < count && at < left)
-                    base[line * m.ldy + at] = *reinterpret_cast<const T*>(lines + line * kPitch + at * sizeof(T));
+                for (int k = 0; k < kVec - 1; ++k)
+                    if (at + k < left) o[k] = e[k];
             }
         }
         __builtin_amdgcn_wave_barrier();
@@ -719,7 +714,6 @@ hipError_t tile_launch(TileArgs a, TimedLaunch t, hipStream_t s) {
     constexpr int kRows = kGated ? kTM / 2 : kTM;
     a.mt = (unsigned)((a.m.M + kRows - 1) / kRows);
     a.nt = (unsigned)((a.m.n + kTN - 1) / kTN);
-    a.wide = a.m.ldy * sizeof(T) % 16 == 0 && reinterpret_cast<uintptr_t>(a.m.y) % 16 == 0;
     const dim3 grid(a.mt * a.nt), block(kSplit * kWM * kWN * kWave);
     if (!kGated && a.m.channel_major)
         GPTQ_LAUNCH(t, (f8_tile_kernel<T, kTM, kTN, kWM, kWN, kStages, kSplit, kGated, kHalf, !kGated, kEarly, kCarry && kTN < 256>), grid, block, 0, s, a);
@@ -728,29 +722,26 @@ hipError_t tile_launch(TileArgs a, TimedLaunch t, hipStream_t s) {
     return hipGetLastError();
 }
 
-constexpr int64_t kFewTokens = 32;      // the few-token kernel up to here,
-constexpr int64_t kSomeTokens = 64;     // and up to here for weights of few rows
+constexpr int64_t kFewTokens = 32;  // the few-token kernel always, up to here
 
-// Few tokens or many?  The tile kernel at its smallest tile against the
-// few-token one, us on 4096 x 4096, 11008 (k) x 4096 and 4096 x 11008 weights:
-// 32 tokens 12.0, 30 and 12.5 against 6.8, 11.9 and 13.0; 64 tokens 12.3, 30
-// and 13.0 against 9.5, 17.4 and 19.9.
-bool f8_few(int64_t n, int64_t M) { return n <= kFewTokens || (n <= kSomeTokens && M <= 8192); }
-
-// The tile by what a product's blocks of k take: rounds of tiles over the CUs
-// times the measured time of a round and block.  us a block with every CU at
-// work: e4m3 MFMA 256 x 256 2.0, 256 x 128 1.2, 128 x 128 0.68, 128 x 64 with
-// two groups of waves sharing k 0.43, 64 x 64 0.31 (one a CU, two groups), 0.52
-// (two a CU), 0.80 (three); float16 MFMA 256 x 128 2.1, 128 x 64 in two groups
-// 0.68, 64 x 64 0.47 (one, two groups), 0.88, 1.45.  At 4096 x 4096 weights, e4m3: 256 tokens 10.7 us in 64 x 64
-// tiles (13.4 in one group), 13.4 in 128 x 64, 29 in 256 x 128; 512 tokens
+// Which kernel and tile, by estimated time.  Tiles: rounds of tiles over the
+// CUs, 2.5 us each (its first copies, its epilogue) and, for each block of k, us
+// with every CU at work: e4m3 MFMA, 256 x 256 1.8, 256 x 128 1.05, 128 x 128
+// 0.6, 128 x 64 with two groups of waves sharing k 0.35, 64 x 64 0.2 (one a CU,
+// two groups), 0.41 (two a CU), 0.5 (three); float16 MFMA 256 x 128 2.0, 128 x
+// 64 in two groups 0.6, 64 x 64 0.35, 0.76, 1.3.  The few-token kernel, which
+// runs workgroups of sixteen rows by 32 tokens: 1.3 us, 0.002 a workgroup and,
+// a block, 0.07 and 0.0003 a workgroup.  At 4096 x 4096 weights, e4m3: 256 tokens 10.7 us in 64
+// x 64 tiles (13.4 in one group), 13.4 in 128 x 64, 29 in 256 x 128; 512 tokens
 // 14.6 in 128 x 64, 16.5 in 64 x 64; 1024 tokens 22 in 128 x 128, 28 in 128 x
 // 64, 31 in 256 x 128; 4096 tokens 66 in 256 x 256, 76 in 256 x 128, 112 in 64
-// x 64.
+// x 64.  The few-token kernel against 64 x 64 tiles: 512 rows, k 4096, 100
+// tokens 5.4 against 8.1 us (float32 13.6); 1363 rows, 200 tokens 12.0 against
+// 10.4 (15.2); 5376 rows, 64 tokens 12.0 against 9.6 (14.4).
 template <typename T, bool kHalf>
 hipError_t matmul_typed(const MmArgs& m, hipStream_t s) {
     TimedLaunch t(K_F8_MATMUL, s);
-    if (f8_few(m.n, m.M)) return few_launch<T, 1>(m, t, s);
+    if (m.n <= kFewTokens) return few_launch<T, 1>(m, t, s);
     TileArgs a = {};
     a.m = m;
     const int64_t cus = device_cu_count();
@@ -758,17 +749,24 @@ hipError_t matmul_typed(const MmArgs& m, hipStream_t s) {
         return (((m.M + tm - 1) / tm) * ((m.n + tn - 1) / tn) + cus * each - 1) / (cus * each);
     };
     const bool one = rounds(64, 64, 1) == 1, two = rounds(64, 64, 2) == 1;
+    auto cost = [&](int64_t rounds, double block) { return rounds * (2.5 + block * m.nb); };
+    const double groups = (double)f8_few_groups(m.n, m.M);
+    const double few = 1.3 + 0.002 * groups + (0.07 + 0.0003 * groups) * m.nb;
     if constexpr (kHalf) {
-        const double t64 = one ? 0.47 : two ? 0.88 : 1.45 * rounds(64, 64, 3), t96 = 0.68 * rounds(128, 64, 1);
-        const double t256 = 2.1 * rounds(256, 128, 1), least = std::min(std::min(t64, t96), t256);
+        const double t64 = one ? cost(1, 0.35) : two ? cost(1, 0.76) : cost(rounds(64, 64, 3), 1.3);
+        const double t96 = cost(rounds(128, 64, 1), 0.6), t256 = cost(rounds(256, 128, 1), 2.0);
+        const double least = std::min(std::min(t64, t96), t256);
+        if (few <= least) return few_launch<T, 1>(m, t, s);
         if (t64 == least && one) return tile_launch<T, 64, 64, 2, 2, 3, false, true, 2>(a, t, s);
         if (t64 == least) return tile_launch<T, 64, 64, 2, 2, 3, false, true>(a, t, s);
         if (t96 == least) return tile_launch<T, 128, 64, 2, 2, 3, false, true, 2>(a, t, s);
         return tile_launch<T, 256, 128, 4, 2, 2, false, true>(a, t, s);
     } else {
-        const double t64 = one ? 0.31 : two ? 0.52 : 0.80 * rounds(64, 64, 3), t96 = 0.43 * rounds(128, 64, 1);
-        const double t128 = 0.68 * rounds(128, 128, 1), t256 = 1.2 * rounds(256, 128, 1), t512 = 2.0 * rounds(256, 256, 1);
+        const double t64 = one ? cost(1, 0.2) : two ? cost(1, 0.41) : cost(rounds(64, 64, 3), 0.5);
+        const double t96 = cost(rounds(128, 64, 1), 0.35), t128 = cost(rounds(128, 128, 1), 0.6);
+        const double t256 = cost(rounds(256, 128, 1), 1.05), t512 = cost(rounds(256, 256, 1), 1.8);
         const double least = std::min(std::min(t64, t96), std::min(t128, std::min(t256, t512)));
+        if (few <= least) return few_launch<T, 1>(m, t, s);
         if (t64 == least && one) return tile_launch<T, 64, 64, 2, 2, 3, false, false, 2>(a, t, s);
         if (t64 == least) return tile_launch<T, 64, 64, 2, 2, 3, false, false>(a, t, s);
         if (t96 == least) return tile_launch<T, 128, 64, 2, 2, 3, false, false, 2>(a, t, s);
@@ -777,6 +775,14 @@ hipError_t matmul_typed(const MmArgs& m, hipStream_t s) {
         return tile_launch<T, 256, 256, 2, 4, 2, false, false>(a, t, s);
     }
 }
+
+// The gated block takes the few-token kernel for up to 32 tokens, and for up
+// to 1024 of its workgroups (a rule without k: the workspace's size goes by
+// it): 128 rows, k 4096, 100 tokens 8.5 us against 33.6 in the tile kernel;
+// 1363 rows, 200 tokens 20.6 against 34.8; 5376 rows, 100 tokens (1344
+// workgroups) 31 against 34, k 1024 16 against 13.
+constexpr int64_t kFewGatedGroups = 1024;
+bool f8_few_gated(int64_t n, int64_t M) { return n <= kFewTokens || f8_few_groups(n, M) <= kFewGatedGroups; }
 
 }  // namespace
 
@@ -789,21 +795,22 @@ hipError_t launch_f8_matmul(const F8Product& c, int y_dtype, hipStream_t s) {
 }
 
 size_t f8_gated_workspace_bytes(int64_t n, int64_t d_ff) {
-    if (n > kFewTokens) return 0;
+    if (!f8_few_gated(n, d_ff)) return 0;
     return (size_t)(n * ((d_ff + kF8Block - 1) / kF8Block) * kF8Block) * sizeof(float);
 }
 
-// Up to 32 tokens: the few-token kernel leaves the products in float32 and the
+// Few tokens: the few-token kernel leaves the products in float32 and the
 // activations' quantizer writes them in 8 bits (11008 channels, 32 tokens: 24
-// us, the tile kernel 36).  More: the tile kernel, as wide as makes rounds of
-// tiles over the CUs times a round's time least: 1.16 us a block of k for 64
-// tokens, 1.9 for 128, 3.3 for 256 (11008 channels, k 4096: 128 tokens 40, 61
+// us, the tile kernel 36).  Many: the tile kernel, as wide as makes rounds of
+// tiles over the CUs times a round's time least: 3 us and, a block of k, 1.05
+// for 64 tokens, 1.75 for 128, 3.15 for 256 (11008 channels, k 4096: 128 tokens 40, 61
 // and 106 us, 1024 tokens 208, 174 and 204, 4096 tokens 776, 640 and 616).
-// At 256 tokens a wave converts fewer values for its products (160 an m-tile
-// and token tile against 192), but holds no registers for fragments ahead.
+// At 256 tokens a wave converts fewer values for its products (192 an m-tile
+// for four token tiles of twice the rows, against 128), but holds no registers
+// for fragments ahead.
 hipError_t launch_f8_gated(const F8Product& c, uint8_t* q, int64_t ldq, float* scales, int64_t lds, void* ws,
                            hipStream_t s) {
-    if (c.n > kFewTokens) {
+    if (!f8_few_gated(c.n, c.M)) {
         TileArgs t = {};
         t.m = {{c.wq[0], c.wq[1]}, {c.ws[0], c.ws[1]}, c.xq, c.xs, nullptr, c.ldw, c.ldws, c.ldx, c.ldxs, 0, c.M, c.n,
                (int)((c.K + kF8Block - 1) / kF8Block), 0, 0};
@@ -814,8 +821,10 @@ hipError_t launch_f8_gated(const F8Product& c, uint8_t* q, int64_t ldq, float* s
         const TimedLaunch k(K_F8_GATED, s);
         const int64_t cus = device_cu_count(), blocks = (c.M + kF8Block - 1) / kF8Block;
         if (cus <= 0) return hipErrorInvalidDevice;
-        auto rounds = [&](int64_t tn) { return (blocks * ((c.n + tn - 1) / tn) + cus - 1) / cus; };
-        const double t64 = 1.16 * rounds(64), t128 = 1.9 * rounds(128), t256 = 3.3 * rounds(256);
+        auto cost = [&](int64_t tn, double block) {
+            return ((blocks * ((c.n + tn - 1) / tn) + cus - 1) / cus) * (3.0 + block * t.m.nb);
+        };
+        const double t64 = cost(64, 1.05), t128 = cost(128, 1.75), t256 = cost(256, 3.15);
         if (t64 <= t128 && t64 <= t256) return tile_launch<float, 256, 64, 4, 2, 3, true, true>(t, k, s);
         if (t128 <= t256) return tile_launch<float, 256, 128, 4, 2, 2, true, true>(t, k, s);
         return tile_launch<float, 256, 256, 2, 4, 2, true, true, 1, false, false>(t, k, s);

@@ -19,39 +19,44 @@ inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 1
 
 // ---------------------------------------------------------------------------
 // weights: one workgroup per 128 x 128 block; thread t holds columns
-// 8 (t % 16) .. +8 of rows t / 16 + 16 i.  The codes are stored nontemporally
+// 8 (t % 16) .. +8 of rows t / 16 + 64 i.  The codes are stored nontemporally
 // (a layer is quantized once and read much later): 11008 x 4096 float16 in
-// 26.1 us, 5190 GB/s, the rate of a large copy, against 32.1 us.
+// 24.4 us, 5540 GB/s, the rate of a large copy; 32.1 us with plain stores; 512
+// and 256 threads 24.7 and 26.6 us, 128 x 248 bfloat16 3.2 us against 3.4 and
+// 4.3.
 // ---------------------------------------------------------------------------
+constexpr int kWThreads = 1024;
+constexpr int kWRows = 128 * 16 / kWThreads;  // rows a thread
+
 template <typename T, bool kVec>
-__global__ __launch_bounds__(kQThreads) void f8_weight_kernel(const T* __restrict__ W, int64_t M, int64_t K, int64_t ldw,
+__global__ __launch_bounds__(kWThreads) void f8_weight_kernel(const T* __restrict__ W, int64_t M, int64_t K, int64_t ldw,
                                                               uint8_t* __restrict__ q, int64_t ldq,
                                                               float* __restrict__ scales, int64_t lds, unsigned nb) {
-    __shared__ uint32_t peaks[kQThreads / kWave];
+    __shared__ uint32_t peaks[kWThreads / kWave];
     const int tid = threadIdx.x;
     const int64_t bi = blockIdx.x / nb, bj = blockIdx.x % nb;
     const int64_t row0 = bi * kF8Block, col = bj * kF8Block + 8 * (tid % 16);
-    float v[8][8];
+    float v[kWRows][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t r = row0 + tid / 16 + 16 * i;
+    for (int i = 0; i < kWRows; ++i) {
+        const int64_t r = row0 + tid / 16 + kWThreads / 16 * i;
         load8<T, kVec>(v[i], W + r * ldw + col, r < M ? K - col : 0);
     }
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, peak8(v[i]));
+    for (int i = 0; i < kWRows; ++i) m = max(m, peak8(v[i]));
     m = row16_max(m);
     m = max(m, (uint32_t)__shfl_xor((int)m, 16, kWave));
     m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
     if (tid % kWave == 0) peaks[tid / kWave] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kQThreads / kWave; ++w) m = max(m, peaks[w]);
+    for (int w = 0; w < kWThreads / kWave; ++w) m = max(m, peaks[w]);
     const float s = f8_scale(m), inv = 1.0f / s;
     if (tid == 0) scales[bi * lds + bj] = s;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t r = row0 + tid / 16 + 16 * i;
+    for (int i = 0; i < kWRows; ++i) {
+        const int64_t r = row0 + tid / 16 + kWThreads / 16 * i;
         if (r < M) __builtin_nontemporal_store(f8_pack8(v[i], inv), reinterpret_cast<uint2v*>(q + r * ldq + col));
     }
 }
@@ -322,9 +327,9 @@ hipError_t weight_typed(const void* W, int64_t M, int64_t K, int64_t ldw, uint8_
     const unsigned nb = (unsigned)((K + kF8Block - 1) / kF8Block), rb = (unsigned)((M + kF8Block - 1) / kF8Block);
     TimedLaunch t(K_F8_WEIGHT, s);
     if (aligned16(W) && K % 8 == 0 && ldw * sizeof(T) % 16 == 0)
-        GPTQ_LAUNCH(t, (f8_weight_kernel<T, true>), dim3(nb * rb), dim3(kQThreads), 0, s, w, M, K, ldw, q, ldq, scales, lds, nb);
+        GPTQ_LAUNCH(t, (f8_weight_kernel<T, true>), dim3(nb * rb), dim3(kWThreads), 0, s, w, M, K, ldw, q, ldq, scales, lds, nb);
     else
-        GPTQ_LAUNCH(t, (f8_weight_kernel<T, false>), dim3(nb * rb), dim3(kQThreads), 0, s, w, M, K, ldw, q, ldq, scales, lds, nb);
+        GPTQ_LAUNCH(t, (f8_weight_kernel<T, false>), dim3(nb * rb), dim3(kWThreads), 0, s, w, M, K, ldw, q, ldq, scales, lds, nb);
     return hipGetLastError();
 }
 

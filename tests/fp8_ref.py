@@ -83,10 +83,9 @@ def tiles_values(codes, scales, d):
         return (decode(codes) * s)[:, :d]
 
 
-def cuts(n, m, dtype):
-    """Whether a product of n tokens and m weight rows runs on the e4m3 MFMA:
-    many tokens and a 16-bit output."""
-    return dtype != "float32" and not (n <= 32 or (n <= 64 and m <= 8192))
+def cuts(n, dtype):
+    """Whether a product of n tokens may run on the e4m3 MFMA."""
+    return dtype != "float32" and n > 32
 
 
 def product(x, w, cut=False):

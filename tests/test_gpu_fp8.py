@@ -266,7 +266,7 @@ def test_matmul(lib, n, m, d, name, channel_major):
     buf = torch.full((shape[0] + 1, shape[1] + 5), 3.0, dtype=getattr(torch, name), device="cuda")
     y = layer.fp8_matmul(w8, x8, relu=relu, channel_major=channel_major, out=buf[:shape[0], :shape[1]])
     got = y.float().cpu().numpy().astype(np.float64)
-    want, dy = ref.product(xv, wv, ref.cuts(n, m, name))
+    want, dy = ref.product(xv, wv, ref.cuts(n, name))
     if relu:
         want = np.maximum(want, 0)
     if channel_major:
@@ -295,7 +295,7 @@ def test_matmul_tiles(lib, n, m, d, name, channel_major):
     x8, w8, xv, wv = operands(rng, n, m, d)
     y = layer.fp8_matmul(w8, x8, dtype=getattr(torch, name), channel_major=channel_major)
     got = (y.t() if channel_major else y).float().cpu().numpy()
-    want, dy = ref.product(xv, wv, ref.cuts(n, m, name))
+    want, dy = ref.product(xv, wv, ref.cuts(n, name))
     most = dy + ref.HALF[name] * (np.abs(want) + dy) + ref.TINY[name]
     off = np.abs(got - want)
     assert np.all(off <= most), float(np.max(off / most))
@@ -431,7 +431,7 @@ def test_a_feed_forward_block(lib):
         hv, dh = ref.silu_gate(g, u, dg, du)
         ref.check_quantized(codes_of(h), h.scales.cpu().numpy(), hv, dh)
         got_h = ref.rows_values(codes_of(h), h.scales.cpu().numpy(), ff)
-        yv, dy = ref.product(got_h, ref.tiles_values(codes_of(down), down.scales.cpu().numpy(), ff), ref.cuts(n, d, "bfloat16"))
+        yv, dy = ref.product(got_h, ref.tiles_values(codes_of(down), down.scales.cpu().numpy(), ff), ref.cuts(n, "bfloat16"))
         off = np.abs(y.float().cpu().numpy() - yv)
         assert np.all(off <= dy + 2.0 ** -8 * (np.abs(yv) + dy) + 2.0 ** -134)
         s2 = stream.float().cpu().numpy() + y.float().cpu().numpy()
@@ -449,7 +449,7 @@ def test_propagate_fp8_feeds_the_next_hessian(lib):
     assert Y.shape == (144, 264) and Y.dtype == torch.float16
     xq, xs = ref.quantize_rows(np.ascontiguousarray(Xf.T))
     want, dy = ref.product(ref.rows_values(xq, xs, 200), ref.tiles_values(codes_of(w8), w8.scales.cpu().numpy(), 200),
-                           ref.cuts(264, 144, "float16"))
+                           ref.cuts(264, "float16"))
     want = np.maximum(want, 0)
     got = Y.float().cpu().numpy().T
     assert np.all(np.abs(got - want) <= dy + 2.0 ** -11 * (np.abs(want) + dy) + 2.0 ** -25)
@@ -546,7 +546,7 @@ def test_offsets_past_32_bits(lib):
     from post_weight_quantization_04_amd import layer
     torch = _t()
     gen = torch.Generator(device="cuda").manual_seed(1)
-    # (4096 tokens: like the long call, in a tile that does not share k among groups of waves)
+    # (4096 tokens: like the long call, in a tile that does not share k among groups of waves, and not few)
     n, d, m, tail = 1_100_000, 4096, 2048, 4096
     w8 = layer.fp8_weight(torch.randn((m, d), generator=gen, device="cuda").half())
     x = torch.zeros((n, d), dtype=torch.float16, device="cuda")
