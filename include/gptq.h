@@ -416,7 +416,7 @@ int gptq_obq_quantize(const void* W, int w_dtype, int64_t d_out, int64_t d_in, c
  *           infinity, largest value 448), one byte each, row stride ldq
  *           bytes, 16-byte aligned, ldq a multiple of 16 and at least d
  *           rounded up to a multiple of 128; the bytes from d up to that
- *           multiple are zero;
+ *           multiple are zero (products read them);
  *   scales  float32.  Activations (a row per token): [ceil(d/128), lds], one
  *           scale per 128 channels and token, tokens along the row
  *           (lds >= rows).  Weights (a row per output channel):
@@ -427,7 +427,8 @@ int gptq_obq_quantize(const void* W, int w_dtype, int64_t d_out, int64_t d_in, c
  *     s = max(largest |x|, 2^-96) / 448,   value = e4m3(fl32(x * fl32(1/s)))
  * to nearest even, with x in float32, and zero the bytes behind d.  A block
  * that holds an infinity or a NaN gets an infinite or NaN scale and codes of
- * which every one stands for NaN after the multiplication.  Bytes of a row
+ * which every one stands for NaN after the multiplication (the bytes behind d
+ * of such a block too: they may be NaN codes).  Bytes of a row
  * behind the multiple of 128, and rows behind the last, are left as they
  * were.  Outputs must not overlap inputs unless a call says so.  Sizes of 0
  * are empty problems.  Sums are float32 throughout.

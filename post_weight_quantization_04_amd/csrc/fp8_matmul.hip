@@ -751,7 +751,8 @@ hipError_t matmul_typed(const MmArgs& m, hipStream_t s) {
     const bool one = rounds(64, 64, 1) == 1, two = rounds(64, 64, 2) == 1;
     auto cost = [&](int64_t rounds, double block) { return rounds * (2.5 + block * m.nb); };
     const double groups = (double)f8_few_groups(m.n, m.M);
-    const double few = 1.3 + 0.002 * groups + (0.07 + 0.0003 * groups) * m.nb;
+    // (its grid's second dimension, 32 tokens each, holds less than 2^16)
+    const double few = m.n > ((int64_t)1 << 20) ? 1e30 : 1.3 + 0.002 * groups + (0.07 + 0.0003 * groups) * m.nb;
     if constexpr (kHalf) {
         const double t64 = one ? cost(1, 0.35) : two ? cost(1, 0.76) : cost(rounds(64, 64, 3), 1.3);
         const double t96 = cost(rounds(128, 64, 1), 0.6), t256 = cost(rounds(256, 128, 1), 2.0);
