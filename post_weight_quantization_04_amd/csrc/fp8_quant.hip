@@ -21,9 +21,9 @@ inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 1
 // weights: one workgroup per 128 x 128 block; thread t holds columns
 // 8 (t % 16) .. +8 of rows t / 16 + 64 i.  The codes are stored nontemporally
 // (a layer is quantized once and read much later): 11008 x 4096 float16 in
-// 24.4 us, 5540 GB/s, the rate of a large copy; 32.1 us with plain stores; 512
-// and 256 threads 24.7 and 26.6 us, 128 x 248 bfloat16 3.2 us against 3.4 and
-// 4.3.
+// 22.0 us, 6150 GB/s, where a large copy reaches 5230.  Timed together: 24.4 us,
+// 32.1 with plain stores; 512 and 256 threads 24.7 and 26.6 us, at 128 x 248
+// bfloat16 3.4 and 4.3 us against 3.2.
 // ---------------------------------------------------------------------------
 constexpr int kWThreads = 1024;
 constexpr int kWRows = 128 * 16 / kWThreads;  // rows a thread
@@ -88,9 +88,9 @@ __global__ __launch_bounds__(kQThreads) void f8_rows_kernel(const T* __restrict_
 // 8 (t % kCmEights) .. +8.  The peaks meet in LDS, and the codes turn there: a
 // thread's four channels of a token are one 32-bit word, stored where the
 // lanes of a wave write 64 distinct banks, read back as 32 bytes of a token.
-// X is loaded nontemporally: 4096 x 16384 float16 in 44.2 us, 4600 GB/s, 49.2
-// without; 128 tokens a workgroup, or tokens before channels in the order of
-// the workgroups, 46 us.
+// X is loaded nontemporally.  4096 x 16384 float16 in 36.9 us, 5520 GB/s, past
+// the rate of a large copy; 128 tokens a workgroup 44.2 us (49.2 with X kept in
+// the caches), or tokens before channels in the order of the workgroups 46 us.
 // ---------------------------------------------------------------------------
 constexpr int kCmTokens = 64;
 constexpr int kCmEights = kCmTokens / 8;
@@ -154,7 +154,8 @@ __global__ __launch_bounds__(kCmThreads) void f8_columns_kernel(const T* __restr
 // so that sixteen neighbouring lanes hold one block of 128.  kJ chunks a
 // thread stay in registers between the sum and the conversion; kJ = 0 is the
 // form for rows past that, which reads x and r a second time (and writes h
-// only then, so that h may overwrite x or r).
+// only then, so that h may overwrite x or r).  Bound by HBM: 16384 x 4096
+// bfloat16 with a residual in 89.7 us, 5260 GB/s, the rate of a large copy.
 // ---------------------------------------------------------------------------
 template <typename T>
 struct NormArgs {

@@ -5,6 +5,7 @@ the library calls; it performs no arithmetic of its own.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 from typing import Iterable, Optional
 
@@ -214,9 +215,10 @@ def _fp8_out(rows: int, cols: int, scales, device, stream) -> Fp8:
 
 def _on(stream):
     """Memory made inside belongs to the stream that the call runs on."""
-    import contextlib
+    if stream is None:
+        return contextlib.nullcontext()
     import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return torch.cuda.stream(stream)
 
 
 def _fp8_cols(out: Fp8, cols: int) -> Fp8:
@@ -290,9 +292,12 @@ def fp8_gated(gate: Fp8, up: Fp8, x: Fp8, ws: Optional[Workspace] = None, out: O
     need = _lib.fp8_gated_workspace(n, d_ff)
     buf = None
     if need:
-        import torch
         with _on(stream):
-            buf = ws.get(need) if ws is not None else torch.empty(need, dtype=torch.uint8, device=x.data.device)
+            if ws is not None:
+                buf = ws.get(need)
+            else:
+                import torch
+                buf = torch.empty(need, dtype=torch.uint8, device=x.data.device)
     _lib.fp8_gated(gate.data, gate.scales, up.data, up.scales, x.data, x.scales, gate.cols, out.data, out.scales, buf,
                    stream=stream)
     return out
