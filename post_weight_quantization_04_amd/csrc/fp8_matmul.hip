@@ -86,8 +86,13 @@ struct Operand<true> {
 
 __device__ __forceinline__ float relu_if(float y, int relu) { return relu && y < 0.0f ? 0.0f : y; }  // keeps NaN
 
-// silu(g) u; exp overflows to infinity for g below -88, where the result is -0
-__device__ __forceinline__ float gated(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+// silu(g) u = g u / (1 + exp(-g)); exp overflows to infinity for g below -88,
+// where the result is -0.  The hardware's reciprocal (one unit in the last
+// place) takes the place of the division's ten instructions (8320 channels, k 72,
+// 4671 tokens: 54.0 us for 61.6); 2^-64 keeps it a normal number.
+__device__ __forceinline__ float gated(float g, float u) {
+    return g * (__builtin_amdgcn_rcpf((1.0f + __expf(-g)) * 0x1p-64f) * 0x1p-64f) * u;
+}
 
 // Where chunk c of row r goes in the row's 128 bytes of LDS: c ^ f8_swizzle(r).
 // A fragment read takes 16 bytes a lane, row l % 16, and LDS serves it sixteen
@@ -324,9 +329,9 @@ hipError_t few_launch(const MmArgs& a, TimedLaunch t, hipStream_t s) {
 // rows of 128 bytes.  The chunk c of row r is put at c ^ f8_swizzle(r): each lane
 // chooses its source accordingly.
 //
-// The gated form stages 128 gate rows and the same 128 up rows; every wave
-// holds both projections of its channels, and the workgroup holds whole blocks
-// of 128 of the result, which it writes in 8 bits.
+// The gated form stages gate rows and the same up rows, and every wave holds
+// both projections of its channels.  With 128 of each the workgroup holds whole
+// blocks of the result, which it writes in 8 bits; smaller tiles store float32.
 // ---------------------------------------------------------------------------
 struct TileArgs {
     MmArgs m;
@@ -360,7 +365,8 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
     constexpr int kLoads = kAi + kBi + 1;                          // and one for the token scales
     static_assert(kTM % (8 * kWaves) == 0 && kTN % (8 * kWaves) == 0 && kTN % 64 == 0, "whole copies");
     static_assert(kTN / 64 <= kWaves && kWaves % (kTN / 64) == 0, "every wave copies one run of scales");
-    static_assert(!kGated || kTM == 256, "a gated tile holds one block of channels of both matrices");
+    constexpr bool kPack = kGated && kTM == 256;  // whole blocks of channels of both matrices, written in 8 bits
+    static_assert(!kGated || kPack || kF8Block % (kTM / 2) == 0, "channels of one block");
     static_assert(kMt >= 2 && kNt >= 2, "tiles of a wave");
     constexpr int kABytes = kTM * kF8Block, kBBytes = kTN * kF8Block, kBytes = kABytes + kBBytes + 4 * kTN;
     // separate arrays: the compiler then knows that a read of one does not wait for copies into another
@@ -368,7 +374,7 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
     __shared__ __align__(16) uint8_t lds1[kSplit * kBytes];
     __shared__ __align__(16) uint8_t lds2[kStages > 2 ? kSplit * kBytes : 16];
     static_assert(kStages == 2 || kStages == 3, "stages");
-    static_assert(kSplit == 1 || !kGated, "the gated block is not split");
+    static_assert(kSplit == 1 || !kPack, "whole blocks are not split");
 
     const MmArgs& m = a.m;
     const int tid = threadIdx.x, lane = tid % kWave;
@@ -426,7 +432,7 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
 
     constexpr int kWaveRows = kTM / kWM;
     // weight scales: a wave's rows lie in one block of 128 of each matrix
-    const int64_t ob = kGated ? mi : (m0 + wm * kWaveRows) / kF8Block;
+    const int64_t ob = (kGated ? m0 : m0 + wm * kWaveRows) / kF8Block;
     const bool live = kGated || m0 + wm * kWaveRows < m.M;
     const float* wsr = m.ws[0] + (live ? ob : 0) * m.ldws;
     const float* usr = kGated ? m.ws[1] + ob * m.ldws : nullptr;
@@ -611,7 +617,7 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
 #pragma unroll
                     for (int v = 0; v < 4; ++v) acc[i][j][v] += at(g, i, j, v);
     }
-    if (kGated) {
+    if (kPack) {
         uint32_t* peaks = reinterpret_cast<uint32_t*>(lds1);  // [kWM][kTN]
         uint32_t* codes = reinterpret_cast<uint32_t*>(lds0);  // [kTN][kCodePitch]
         constexpr int kCodePitch = kF8Block / 4 + 1;
@@ -662,12 +668,21 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
     // channel: it needs four token scales a product, for which the largest tile
     // has no registers: float32 8192 x 4096 -> 4096 282 us, so 220.  Smaller
     // tiles take the same time either way.)
-    constexpr int kRun = kChannels ? 16 * kNt : 16 * kMt, kOuter = kChannels ? kMt : kNt, kInner = kChannels ? kNt : kMt;
+    if (kGated) {
+#pragma unroll
+        for (int i = 0; i < kMt / 2; ++i)
+#pragma unroll
+            for (int j = 0; j < kNt; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][j][v] = gated(acc[i][j][v], acc[i + kMt / 2][j][v]);
+    }
+    constexpr int kMo = kGated ? kMt / 2 : kMt, kOutRows = kRows / kWM;  // of a wave
+    constexpr int kRun = kChannels ? 16 * kNt : 16 * kMo, kOuter = kChannels ? kMo : kNt, kInner = kChannels ? kNt : kMo;
     constexpr int kPitch = kRun * (int)sizeof(T) + 16, kVec = 16 / (int)sizeof(T);
     // (float32 lines of the largest tile need both stages; in the split form a
     // slower wave may still read its sums from the second)
     constexpr bool kBoth = kWaves * 16 * kPitch > kBytes;
-    static_assert(kGated || !kBoth || (kSplit == 1 && kWaves / 2 * 16 * kPitch <= kBytes), "the lines of every wave");
+    static_assert(kPack || !kBoth || (kSplit == 1 && kWaves / 2 * 16 * kPitch <= kBytes), "the lines of every wave");
     uint8_t* lines = kBoth && w >= kWaves / 2 ? lds1 + (w - kWaves / 2) * 16 * kPitch : lds0 + w * 16 * kPitch;
     T* y = static_cast<T*>(m.y);
     const int first = kChannels ? wn * kRun : wm * kRun;           // of the run, within the tile
@@ -690,7 +705,7 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
             }
         }
         __builtin_amdgcn_wave_barrier();
-        const int line0 = kChannels ? wm * kWaveRows + 16 * o : (wn * kNt + o) * 16;
+        const int line0 = kChannels ? wm * kOutRows + 16 * o : (wn * kNt + o) * 16;
         const int count = (kChannels ? rows : toks) - line0;       // lines within Y
         T* base = y + ((kChannels ? m0 : t0) + line0) * m.ldy + start;
         // (16 bytes at a time; Y's lines need no more than their type's alignment)
@@ -785,13 +800,13 @@ hipError_t matmul_typed(const MmArgs& m, hipStream_t s) {
     }
 }
 
-// The gated block takes the few-token kernel for up to 32 tokens, and for up
-// to 1024 of its workgroups (a rule without k: the workspace's size goes by
-// it): 128 rows, k 4096, 100 tokens 8.5 us against 33.6 in the tile kernel;
-// 1363 rows, 200 tokens 20.6 against 34.8; 5376 rows, 100 tokens (1344
-// workgroups) 31 against 34, k 1024 16 against 13.
-constexpr int64_t kFewGatedGroups = 1024;
-bool f8_few_gated(int64_t n, int64_t M) { return n <= kFewTokens || f8_few_groups(n, M) <= kFewGatedGroups; }
+// Up to here the gated block may leave its products in float32 (a rule without
+// k: the workspace's size goes by it): few tokens, or tiles of 128 channels by
+// 64 tokens that leave half of the CUs idle.
+constexpr int64_t kGatedTiles = 128;
+bool f8_gated_in_two(int64_t n, int64_t M) {
+    return n <= kFewTokens || ((M + kF8Block - 1) / kF8Block) * ((n + 63) / 64) <= kGatedTiles;
+}
 
 }  // namespace
 
@@ -804,46 +819,64 @@ hipError_t launch_f8_matmul(const F8Product& c, int y_dtype, hipStream_t s) {
 }
 
 size_t f8_gated_workspace_bytes(int64_t n, int64_t d_ff) {
-    if (!f8_few_gated(n, d_ff)) return 0;
+    if (!f8_gated_in_two(n, d_ff)) return 0;
     return (size_t)(n * ((d_ff + kF8Block - 1) / kF8Block) * kF8Block) * sizeof(float);
 }
 
-// Few tokens: the few-token kernel leaves the products in float32 and the
-// activations' quantizer writes them in 8 bits (11008 channels, 32 tokens: 24
-// us, the tile kernel 36).  Many: the tile kernel, as wide as makes rounds of
-// tiles over the CUs times a round's time least: 3 us and, a block of k, 1.05
-// for 64 tokens, 1.75 for 128, 3.15 for 256 (11008 channels, k 4096: 128 tokens 40, 61
-// and 106 us, 1024 tokens 208, 174 and 204, 4096 tokens 776, 640 and 616).
-// At 256 tokens a wave converts fewer values for its products (192 an m-tile
-// for four token tiles of twice the rows, against 128), but holds no registers
-// for fragments ahead.
+// In one kernel: tiles of 128 channels, which are whole blocks of the result,
+// 64, 128 or 256 tokens wide.  At 256 a wave converts fewer values for its
+// products (192 an m-tile for four token tiles of twice the rows, against 128),
+// but holds no registers for fragments ahead.  In two: a kernel that leaves the
+// products in float32, the few-token one or tiles of 64 or 32 channels by 64
+// tokens in two groups of waves, and the activations' quantizer.
+//
+// The choice goes by estimated time, as for the product: rounds of tiles over
+// the CUs, each with a part of its own (start, epilogue) and one for a block of
+// k; the forms in two parts 2 us more.  Measured, 11008 channels, k 4096: 64
+// tokens 35.5 us in one kernel, 26.6 in 64-channel tiles, 33.6 in 32-channel
+// ones, 38.6 with the few-token kernel; 128 tokens 40 in one kernel; 1024 tokens
+// 208, 174 and 204 for 64, 128 and 256 tokens wide; 4096 tokens 776, 640 and
+// 616.  1408 channels, k 4096, 100 tokens: 33.8, 22.0, 17.1 and 12.9 with the
+// few-token kernel; 200 tokens 34.1, 22.4, 18.4 and 18.1.  8320 channels, k
+// 128, 4671 tokens: 91, 65 and 50 us for 64, 128 and 256 tokens wide.
 hipError_t launch_f8_gated(const F8Product& c, uint8_t* q, int64_t ldq, float* scales, int64_t lds, void* ws,
                            hipStream_t s) {
-    if (!f8_few_gated(c.n, c.M)) {
-        TileArgs t = {};
-        t.m = {{c.wq[0], c.wq[1]}, {c.ws[0], c.ws[1]}, c.xq, c.xs, nullptr, c.ldw, c.ldws, c.ldx, c.ldxs, 0, c.M, c.n,
-               (int)((c.K + kF8Block - 1) / kF8Block), 0, 0};
-        t.q = q;
-        t.qs = scales;
-        t.ldq = ldq;
-        t.ldqs = lds;
-        const TimedLaunch k(K_F8_GATED, s);
-        const int64_t cus = device_cu_count(), blocks = (c.M + kF8Block - 1) / kF8Block;
-        if (cus <= 0) return hipErrorInvalidDevice;
-        auto cost = [&](int64_t tn, double block) {
-            return ((blocks * ((c.n + tn - 1) / tn) + cus - 1) / cus) * (3.0 + block * t.m.nb);
-        };
-        const double t64 = cost(64, 1.05), t128 = cost(128, 1.75), t256 = cost(256, 3.15);
-        if (t64 <= t128 && t64 <= t256) return tile_launch<float, 256, 64, 4, 2, 3, true, true>(t, k, s);
-        if (t128 <= t256) return tile_launch<float, 256, 128, 4, 2, 2, true, true>(t, k, s);
-        return tile_launch<float, 256, 256, 2, 4, 2, true, true, 1, false, false>(t, k, s);
-    }
+    const int64_t cus = device_cu_count();
+    if (cus <= 0) return hipErrorInvalidDevice;
+    const bool two = f8_gated_in_two(c.n, c.M);
     const int64_t ldh = (c.M + kF8Block - 1) / kF8Block * kF8Block;
-    MmArgs a = {{c.wq[0], c.wq[1]}, {c.ws[0], c.ws[1]}, c.xq, c.xs, ws, c.ldw, c.ldws, c.ldx, c.ldxs, ldh, c.M, c.n,
-                (int)((c.K + kF8Block - 1) / kF8Block), 0, 0};
-    const hipError_t e = few_launch<float, 2>(a, TimedLaunch(K_F8_GATED, s), s);
-    if (e != hipSuccess) return e;
-    return launch_f8_activations(ws, 1, c.n, c.M, ldh, 0, q, ldq, scales, lds, s);
+    TileArgs t = {};
+    t.m = {{c.wq[0], c.wq[1]}, {c.ws[0], c.ws[1]}, c.xq, c.xs, two ? ws : nullptr, c.ldw, c.ldws, c.ldx, c.ldxs,
+           two ? ldh : 0, c.M, c.n, (int)((c.K + kF8Block - 1) / kF8Block), 0, 0};
+    t.q = q;
+    t.qs = scales;
+    t.ldq = ldq;
+    t.ldqs = lds;
+    const int nb = t.m.nb;
+    auto cost = [&](int64_t channels, int64_t tokens, double own, double block) {
+        const int64_t tiles = ((c.M + channels - 1) / channels) * ((c.n + tokens - 1) / tokens);
+        return ((tiles + cus - 1) / cus) * (own + block * nb);
+    };
+    const double w64 = cost(128, 64, 4.0, 0.97), w128 = cost(128, 128, 4.9, 1.73), w256 = cost(128, 256, 7.0, 3.1);
+    const double one = std::min(w64, std::min(w128, w256));
+    const TimedLaunch k(K_F8_GATED, s);
+    if (two) {
+        const double groups = (double)f8_few_groups(c.n, c.M);
+        const double few = 3.4 + 0.0032 * groups + (0.08 + 0.00037 * groups) * nb;
+        const double c32 = cost(32, 64, 4.0, 0.32), c64 = cost(64, 64, 5.0, 0.47);
+        const double least = std::min(few, std::min(c32, c64));
+        if (c.n <= kFewTokens || least + 2.0 < one) {
+            hipError_t e;
+            if (c.n <= kFewTokens || few == least) e = few_launch<float, 2>(t.m, k, s);
+            else if (c32 == least) e = tile_launch<float, 64, 64, 2, 2, 3, true, true, 2>(t, k, s);
+            else e = tile_launch<float, 128, 64, 2, 2, 3, true, true, 2>(t, k, s);
+            if (e != hipSuccess) return e;
+            return launch_f8_activations(ws, 1, c.n, c.M, ldh, 0, q, ldq, scales, lds, s);
+        }
+    }
+    if (w64 == one) return tile_launch<float, 256, 64, 4, 2, 3, true, true>(t, k, s);
+    if (w128 == one) return tile_launch<float, 256, 128, 4, 2, 2, true, true>(t, k, s);
+    return tile_launch<float, 256, 256, 2, 4, 2, true, true, 1, false, false>(t, k, s);
 }
 
 }  // namespace gptq

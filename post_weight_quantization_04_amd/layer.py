@@ -280,7 +280,7 @@ def fp8_matmul(w: Fp8, x: Fp8, dtype=None, relu: bool = False, channel_major: bo
 
 def fp8_gated(gate: Fp8, up: Fp8, x: Fp8, ws: Optional[Workspace] = None, out: Optional[Fp8] = None, stream=None) -> Fp8:
     """``silu(X G^T) * (X U^T)`` in 8 bits (``gptq_fp8_gated``): the input of
-    the down projection.  Few tokens need scratch memory: that of ``ws``, or
+    the down projection.  Small calls need scratch memory: that of ``ws``, or
     memory of the call's own."""
     if gate.cols != x.cols or up.cols != x.cols:
         raise ValueError(f"weights of {gate.cols} and {up.cols} columns, activations of {x.cols}")

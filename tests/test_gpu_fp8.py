@@ -367,7 +367,8 @@ def test_matmul_empty(lib):
 # ---------------------------------------------------------------------------
 GATED = [(1, 1, 1), (1, 128, 256), (1, 1000, 520), (2, 130, 129), (16, 256, 512), (17, 200, 384), (40, 640, 300), (64, 129, 256),
          (65, 384, 640), (130, 257, 200), (256, 256, 384), (300, 700, 513),
-         (200, 5000, 136), (1024, 11008, 128), (4090, 2040, 200), (33, 140, 16600)]
+         (200, 5000, 136), (1024, 11008, 128), (4090, 2040, 200), (33, 140, 16600),
+         (990, 500, 1000), (100, 5590, 1300), (70, 5500, 8300), (200, 5000, 8300)]
 
 
 @pytest.mark.parametrize("n,m,d", GATED)
