@@ -568,9 +568,18 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
                      kGated ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(ul, i)) : 0.0f);
             };
             uint8_t* const after1 = kStages > 2 ? lds2 : lds0;
+            int i = 0;
+            if constexpr (!kCarry && kStages == 2) {
+                // (an odd step of its own, as below, was compiled with many registers spilled)
+                for (; i < run; i += 2) {
+                    go(lds0, lds1, last, i);
+                    if (i + 1 == run) break;
+                    go(lds1, after1, lds0, i + 1);
+                }
+                continue;
+            }
             // no branch between the steps of the loop: the compiler would move
             // the scaling of products past it and keep them all in registers
-            int i = 0;
             for (; i + kStages <= run; i += kStages) {
                 go(lds0, lds1, last, i);
                 go(lds1, after1, lds0, i + 1);
@@ -744,21 +753,24 @@ hipError_t tile_launch(TileArgs a, TimedLaunch t, hipStream_t s) {
 
 constexpr int64_t kFewTokens = 32;  // the few-token kernel always, up to here
 
-// Which kernel and tile, by estimated time.  Tiles: rounds of tiles over the
-// CUs, 2.5 us each (its first copies, its epilogue) and, for each block of k, us
-// with every CU at work: e4m3 MFMA, 256 x 256 1.8, 256 x 128 1.05, 128 x 128
-// 0.6, 128 x 64 with two groups of waves sharing k 0.35, 64 x 64 0.2 (one a CU,
-// two groups), 0.41 (two a CU), 0.5 (three); float16 MFMA 256 x 256 3.2, 256 x
-// 128 2.0, 128 x 64 in two groups 0.6, 64 x 64 0.35, 0.76, 1.3.  The few-token
-// kernel, which runs workgroups of sixteen rows by 32 tokens: 1.3 us, 0.002 a
-// workgroup and, a block, 0.07 and 0.0003 a workgroup.  At 4096 x 4096 weights,
-// e4m3: 256 tokens 10.7 us in 64 x 64 tiles (13.4 in one group), 13.4 in 128 x
-// 64, 29 in 256 x 128; 512 tokens 14.6 in 128 x 64, 16.5 in 64 x 64; 1024 tokens
-// 22 in 128 x 128, 28 in 128 x 64, 31 in 256 x 128; 4096 tokens 59 in 256 x 256
-// (float32 107), 76 in 256 x 128 (float32 119), 112 in 64 x 64.  The few-token
-// kernel against 64 x 64 tiles: 512 rows, k 4096, 100 tokens 5.4 against 8.1 us
-// (float32 13.6); 1363 rows, 200 tokens 12.0 against 10.4 (15.2); 5376 rows, 64
-// tokens 12.0 against 9.6 (14.4).
+// Which kernel and tile, by estimated time: rounds of tiles over the CUs, each
+// with a part of its own (its first copies, its epilogue) and one for a block of
+// k, in us with every CU at work (the time to write Y is the same for all and
+// left out):
+//                   256 x 256   256 x 128   128 x 128   128 x 64*  64 x 64, three a CU  two   one*
+//   e4m3 MFMA       1.3 + 1.8   1.5 + 1.05  1.7 + 0.58  2.6 + 0.33  1.4 + 0.5   2.2 + 0.41  2.5 + 0.2
+//   float16 MFMA    0.4 + 3.0   0.5 + 1.8               2.6 + 0.55  1.4 + 1.3   2.2 + 0.76  2.5 + 0.35
+// (*: two groups of waves share k).  The few-token kernel, which runs
+// workgroups of sixteen rows by 32 tokens: 1.3 us, 0.002 a workgroup and, a
+// block, 0.07 and 0.0003 a workgroup.  Measured, 4096 x 4096 weights, e4m3: 256
+// tokens 10.7 us in 64 x 64 tiles (13.4 in one group), 13.4 in 128 x 64, 29 in
+// 256 x 128; 512 tokens 14.6 in 128 x 64, 16.5 in 64 x 64; 1024 tokens 22 in 128
+// x 128, 28 in 128 x 64, 31 in 256 x 128; 4096 tokens 59 in 256 x 256 (float32
+// 107), 76 in 256 x 128 (float32 119), 112 in 64 x 64.  14919 tokens, k 1024, 1280
+// rows: 36 us in 256 x 256, 35 in 256 x 128, 37 in 128 x 128, 46 in 64 x 64
+// (float32 63, 60, -, 66).  The few-token kernel against 64 x 64 tiles: 512 rows,
+// k 4096, 100 tokens 5.4 against 8.1 us (float32 13.6); 1363 rows, 200 tokens
+// 12.0 against 10.4 (15.2); 5376 rows, 64 tokens 12.0 against 9.6 (14.4).
 template <typename T, bool kHalf>
 hipError_t matmul_typed(const MmArgs& m, hipStream_t s) {
     TimedLaunch t(K_F8_MATMUL, s);
@@ -770,14 +782,14 @@ hipError_t matmul_typed(const MmArgs& m, hipStream_t s) {
         return (((m.M + tm - 1) / tm) * ((m.n + tn - 1) / tn) + cus * each - 1) / (cus * each);
     };
     const bool one = rounds(64, 64, 1) == 1, two = rounds(64, 64, 2) == 1;
-    auto cost = [&](int64_t rounds, double block) { return rounds * (2.5 + block * m.nb); };
+    auto cost = [&](int64_t rounds, double own, double block) { return rounds * (own + block * m.nb); };
     const double groups = (double)f8_few_groups(m.n, m.M);
     // (its grid's second dimension, 32 tokens each, holds less than 2^16)
     const double few = m.n > ((int64_t)1 << 20) ? 1e30 : 1.3 + 0.002 * groups + (0.07 + 0.0003 * groups) * m.nb;
     if constexpr (kHalf) {
-        const double t64 = one ? cost(1, 0.35) : two ? cost(1, 0.76) : cost(rounds(64, 64, 3), 1.3);
-        const double t96 = cost(rounds(128, 64, 1), 0.6), t256 = cost(rounds(256, 128, 1), 2.0);
-        const double t512 = cost(rounds(256, 256, 1), 3.2);
+        const double t64 = one ? cost(1, 2.5, 0.35) : two ? cost(1, 2.2, 0.76) : cost(rounds(64, 64, 3), 1.4, 1.3);
+        const double t96 = cost(rounds(128, 64, 1), 2.6, 0.55), t256 = cost(rounds(256, 128, 1), 0.5, 1.8);
+        const double t512 = cost(rounds(256, 256, 1), 0.4, 3.0);
         const double least = std::min(std::min(t64, t96), std::min(t256, t512));
         if (few <= least) return few_launch<T, 1>(m, t, s);
         if (t64 == least && one) return tile_launch<T, 64, 64, 2, 2, 3, false, true, 2>(a, t, s);
@@ -786,9 +798,9 @@ hipError_t matmul_typed(const MmArgs& m, hipStream_t s) {
         if (t256 == least) return tile_launch<T, 256, 128, 4, 2, 2, false, true>(a, t, s);
         return tile_launch<T, 256, 256, 2, 4, 2, false, true, 1, false, false>(a, t, s);
     } else {
-        const double t64 = one ? cost(1, 0.2) : two ? cost(1, 0.41) : cost(rounds(64, 64, 3), 0.5);
-        const double t96 = cost(rounds(128, 64, 1), 0.35), t128 = cost(rounds(128, 128, 1), 0.6);
-        const double t256 = cost(rounds(256, 128, 1), 1.05), t512 = cost(rounds(256, 256, 1), 1.8);
+        const double t64 = one ? cost(1, 2.5, 0.2) : two ? cost(1, 2.2, 0.41) : cost(rounds(64, 64, 3), 1.4, 0.5);
+        const double t96 = cost(rounds(128, 64, 1), 2.6, 0.33), t128 = cost(rounds(128, 128, 1), 1.7, 0.58);
+        const double t256 = cost(rounds(256, 128, 1), 1.5, 1.05), t512 = cost(rounds(256, 256, 1), 1.3, 1.8);
         const double least = std::min(std::min(t64, t96), std::min(t128, std::min(t256, t512)));
         if (few <= least) return few_launch<T, 1>(m, t, s);
         if (t64 == least && one) return tile_launch<T, 64, 64, 2, 2, 3, false, false, 2>(a, t, s);

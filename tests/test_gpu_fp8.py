@@ -281,7 +281,7 @@ def test_matmul(lib, n, m, d, name, channel_major):
 # every tile: 256 x 256, 256 x 128, 128 x 128, 128 x 64 and 64 x 64, the last of
 # them in ragged sizes too, over k that ends inside a round of 64 scales and past it
 LARGE = [(4090, 4100, 300), (2040, 4096, 200), (1020, 4096, 260), (500, 4096, 128), (700, 4000, 8400), (90, 300, 16520),
-         (1030, 1025, 72)]
+         (1030, 1025, 72), (500, 4096, 1300), (4090, 4096, 600), (4000, 4090, 250)]
 
 
 @pytest.mark.parametrize("name", ("float16", "float32"))
