@@ -323,6 +323,26 @@ def test_matmul_of_whole_numbers_is_exact(lib, n, m, d):
     np.testing.assert_array_equal(y.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("name", ("float16", "float32"))
+@pytest.mark.parametrize("channel_major", [False, True])
+def test_matmul_of_long_rows_is_exact(lib, name, channel_major):
+    """The largest tiles over 65 blocks of k: a round of 64 scales, and one
+    more.  Every sum is exact, and float16 rounds it once."""
+    from post_weight_quantization_04_amd import layer
+    torch = _t()
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    n, m, d = 3840, 4096, 65 * 128
+    say("long rows", n, m, d, name, channel_major)
+    x, w = (torch.randint(-1, 2, (rows, d), generator=gen, device="cuda").float() for rows in (n, m))
+    xs = 2.0 ** torch.randint(-1, 2, (65, n), generator=gen, device="cuda").float()
+    ws = 2.0 ** torch.randint(-1, 2, (m // 128, 65), generator=gen, device="cuda").float()
+    y = layer.fp8_matmul(layer.Fp8(w.to(torch.float8_e4m3fn), ws, d), layer.Fp8(x.to(torch.float8_e4m3fn), xs, d),
+                         dtype=getattr(torch, name), channel_major=channel_major)
+    # every product is a multiple of 1/4 of at most 4, and float32 holds all sums
+    want = (x * xs.t().repeat_interleave(128, 1)) @ (w * ws.repeat_interleave(128, 0).repeat_interleave(128, 1)).t()
+    assert torch.equal(y.t() if channel_major else y, want.to(y.dtype))
+
+
 @pytest.mark.parametrize("n,m", [(3, 200), (300, 300)])
 def test_matmul_carries_bad_values(lib, n, m):
     from post_weight_quantization_04_amd import layer
@@ -368,7 +388,7 @@ def test_matmul_empty(lib):
 GATED = [(1, 1, 1), (1, 128, 256), (1, 1000, 520), (2, 130, 129), (16, 256, 512), (17, 200, 384), (40, 640, 300), (64, 129, 256),
          (65, 384, 640), (130, 257, 200), (256, 256, 384), (300, 700, 513),
          (200, 5000, 136), (1024, 11008, 128), (4090, 2040, 200), (33, 140, 16600),
-         (990, 500, 1000), (100, 5590, 1300), (70, 5500, 8300), (200, 5000, 8300)]
+         (990, 500, 1000), (100, 5590, 1300), (70, 5500, 8300), (200, 5000, 8300), (4090, 2040, 300)]
 
 
 @pytest.mark.parametrize("n,m,d", GATED)
