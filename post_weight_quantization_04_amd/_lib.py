@@ -325,7 +325,9 @@ def obq_quantize(W, U, dead, bits: int, codes, scales, zeros, order=None, loss=N
 #
 # One decoded token's kernel takes 3 to 6 us, so these calls are written to
 # cost the host less: tensors are read once each, by the accessors that do not
-# build new objects, and the names used by every call are set by load().
+# build new objects, the names used by every call are set by load(), and
+# outputs that the caller made for the call (``made``, contiguous, of the right
+# type, shape and device) are not checked.
 # ---------------------------------------------------------------------------
 _fp8_codes = {}          # torch type -> gptq_dtype
 _fp8_eights = ()         # types of the 8-bit values
@@ -403,6 +405,12 @@ def _fp8_operand(values, scales, cols: int, by_row: bool, dev: int, what: str):
             sstride[0] if lead > 1 else max(sstride[0], along), rows)
 
 
+def _fp8_made(values, scales, cols: int, along: int, dev: int):
+    if values.get_device() != dev:
+        raise ValueError(f"outputs on another device than cuda:{dev}")
+    return values.data_ptr(), (cols + 127) >> 7 << 7, scales.data_ptr(), along
+
+
 def fp8_weight(W, values, scales, stream=None) -> None:
     """``W [d_out, d_in]`` to 8 bits, a scale per 128 x 128 block."""
     lib = _lib or load()
@@ -416,7 +424,7 @@ def fp8_weight(W, values, scales, stream=None) -> None:
         _check("gptq_fp8_weight", rc)
 
 
-def fp8_activations(X, values, scales, channel_major: bool = False, stream=None) -> None:
+def fp8_activations(X, values, scales, channel_major: bool = False, stream=None, made: bool = False) -> None:
     """``X [n, d]`` (or ``[d, n]`` with ``channel_major``) to 8 bits, a scale
     per token and 128 channels."""
     lib = _lib or load()
@@ -424,16 +432,20 @@ def fp8_activations(X, values, scales, channel_major: bool = False, stream=None)
     xp, ldx, n, d = _fp8_matrix(X, dev, "X")
     if channel_major:
         n, d = d, n
-    vp, ld, sp, lds, rows = _fp8_operand(values, scales, d, True, dev, "out")
-    if rows != n:
-        raise ValueError("rows of the output")
+    if made:
+        vp, ld, sp, lds = _fp8_made(values, scales, d, n, dev)
+    else:
+        vp, ld, sp, lds, rows = _fp8_operand(values, scales, d, True, dev, "out")
+        if rows != n:
+            raise ValueError("rows of the output")
     rc = lib.gptq_fp8_activations(xp, _fp8_dtype(X), n, d, ldx, 1 if channel_major else 0, vp, ld, sp, lds,
                                   _fp8_stream(dev, stream))
     if rc:
         _check("gptq_fp8_activations", rc)
 
 
-def fp8_rms_norm(x, gain, eps: float, values, scales, residual=None, sum_out=None, stream=None) -> None:
+def fp8_rms_norm(x, gain, eps: float, values, scales, residual=None, sum_out=None, stream=None, made: bool = False,
+                 sum_made: bool = False) -> None:
     """``h = x + residual``; ``h / sqrt(mean(h^2) + eps) * gain`` to 8 bits;
     ``sum_out = h``."""
     lib = _lib or load()
@@ -445,15 +457,20 @@ def fp8_rms_norm(x, gain, eps: float, values, scales, residual=None, sum_out=Non
         if residual.shape != shape or residual.dtype != kind:
             raise ValueError("residual must have the shape and type of x")
         rp, ldr, _, _ = _fp8_matrix(residual, dev, "residual")
-    if sum_out is not None:
+    if sum_made:
+        op, ldo = sum_out.data_ptr(), d
+    elif sum_out is not None:
         if sum_out.shape != shape or sum_out.dtype != kind:
             raise ValueError("sum_out must have the shape and type of x")
         op, ldo, _, _ = _fp8_matrix(sum_out, dev, "sum_out")
     if gain.shape != shape[1:] or gain.dtype != kind or gain.get_device() != dev or not gain.is_contiguous():
         raise ValueError("gain must be a contiguous vector of x's type, one value per channel")
-    vp, ld, sp, lds, rows = _fp8_operand(values, scales, d, True, dev, "out")
-    if rows != n:
-        raise ValueError("rows of the output")
+    if made:
+        vp, ld, sp, lds = _fp8_made(values, scales, d, n, dev)
+    else:
+        vp, ld, sp, lds, rows = _fp8_operand(values, scales, d, True, dev, "out")
+        if rows != n:
+            raise ValueError("rows of the output")
     rc = lib.gptq_fp8_rms_norm(xp, ldx, rp, ldr, op, ldo, gain.data_ptr(), _fp8_dtype(x), n, d, eps, vp, ld, sp,
                                lds, _fp8_stream(dev, stream))
     if rc:
@@ -480,7 +497,8 @@ def fp8_gated_workspace(n: int, d_ff: int) -> int:
     return load().gptq_fp8_gated_workspace(n, d_ff)
 
 
-def fp8_gated(gq, gs, uq, us, xq, xs, d_in: int, values, scales, workspace=None, stream=None) -> None:
+def fp8_gated(gq, gs, uq, us, xq, xs, d_in: int, values, scales, workspace=None, stream=None,
+              made: bool = False) -> None:
     """``silu(X G^T) * (X U^T)`` of 8-bit operands, written in 8 bits."""
     lib = _lib or load()
     dev = _fp8_device(values)
@@ -489,9 +507,12 @@ def fp8_gated(gq, gs, uq, us, xq, xs, d_in: int, values, scales, workspace=None,
     if up_rows != d_ff or (ldu != ldw and d_ff > 1) or (ldus != ldws and d_ff > 128):
         raise ValueError("gate and up must have one shape and strides")
     xp, ldx, xsp, ldxs, n = _fp8_operand(xq, xs, d_in, True, dev, "activations")
-    vp, ld, sp, lds, rows = _fp8_operand(values, scales, d_ff, True, dev, "out")
-    if rows != n:
-        raise ValueError("rows of the output")
+    if made:
+        vp, ld, sp, lds = _fp8_made(values, scales, d_ff, n, dev)
+    else:
+        vp, ld, sp, lds, rows = _fp8_operand(values, scales, d_ff, True, dev, "out")
+        if rows != n:
+            raise ValueError("rows of the output")
     room = 0
     if workspace is not None:
         if workspace.get_device() != dev:

@@ -243,8 +243,9 @@ def fp8_activations(X, channel_major: bool = False, out: Optional[Fp8] = None, s
     layout of the calibration inputs), in 8 bits, one scale per token and 128
     channels (``gptq_fp8_activations``)."""
     n, d = (X.shape[1], X.shape[0]) if channel_major else X.shape
-    out = (_fp8_cols(out, d) if out is not None else _fp8_out(n, d, (d + 127) // 128, n, X.device, stream))
-    _lib.fp8_activations(X, out.data, out.scales, channel_major=channel_major, stream=stream)
+    made = out is None
+    out = _fp8_out(n, d, (d + 127) // 128, n, X.device, stream) if made else _fp8_cols(out, d)
+    _lib.fp8_activations(X, out.data, out.scales, channel_major, stream, made)
     return out
 
 
@@ -253,10 +254,11 @@ def fp8_rms_norm(x, gain, eps: float = 1e-6, residual=None, out: Optional[Fp8] =
     (``gptq_fp8_rms_norm``): returns the 8-bit activations and ``h`` in x's
     type (None without a residual).  ``sum_out`` may be ``x`` or ``residual``."""
     n, d = x.shape
-    out = (_fp8_cols(out, d) if out is not None else _fp8_out(n, d, (d + 127) // 128, n, x.device, stream))
-    if residual is not None and sum_out is None:
+    made, sum_made = out is None, residual is not None and sum_out is None
+    out = _fp8_out(n, d, (d + 127) // 128, n, x.device, stream) if made else _fp8_cols(out, d)
+    if sum_made:
         sum_out = _empty(n, d, x.dtype, x.device, stream)
-    _lib.fp8_rms_norm(x, gain, eps, out.data, out.scales, residual=residual, sum_out=sum_out, stream=stream)
+    _lib.fp8_rms_norm(x, gain, eps, out.data, out.scales, residual, sum_out, stream, made, sum_made)
     return out, sum_out
 
 
@@ -285,8 +287,8 @@ def fp8_gated(gate: Fp8, up: Fp8, x: Fp8, ws: Optional[Workspace] = None, out: O
     if gate.cols != x.cols or up.cols != x.cols:
         raise ValueError(f"weights of {gate.cols} and {up.cols} columns, activations of {x.cols}")
     n, d_ff = x.data.shape[0], gate.data.shape[0]
-    out = (_fp8_cols(out, d_ff) if out is not None else
-           _fp8_out(n, d_ff, (d_ff + 127) // 128, n, x.data.device, stream))
+    made = out is None
+    out = _fp8_out(n, d_ff, (d_ff + 127) // 128, n, x.data.device, stream) if made else _fp8_cols(out, d_ff)
     need = _lib.fp8_gated_workspace(n, d_ff)
     buf = None
     if need:
@@ -299,7 +301,7 @@ def fp8_gated(gate: Fp8, up: Fp8, x: Fp8, ws: Optional[Workspace] = None, out: O
             with torch.cuda.stream(stream):
                 buf = ws.get(need)
     _lib.fp8_gated(gate.data, gate.scales, up.data, up.scales, x.data, x.scales, gate.cols, out.data, out.scales, buf,
-                   stream=stream)
+                   stream, made)
     return out
 
 
