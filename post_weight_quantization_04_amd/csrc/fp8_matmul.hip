@@ -778,6 +778,7 @@ hipError_t matmul_typed(const MmArgs& m, hipStream_t s) {
     TileArgs a = {};
     a.m = m;
     const int64_t cus = device_cu_count();
+    if (cus <= 0) return hipErrorInvalidDevice;
     auto rounds = [&](int64_t tm, int64_t tn, int64_t each) {
         return (((m.M + tm - 1) / tm) * ((m.n + tn - 1) / tn) + cus * each - 1) / (cus * each);
     };

@@ -118,6 +118,20 @@ def test_gated_refusals(clib):
     assert gated(clib, n=0, gq=None, uq=None, xq=None, q=None, ws=None, size=0) == OK
 
 
+@pytest.mark.parametrize("n", [5, 64, 1000])
+def test_calls_without_a_device_return_an_error(clib, n):
+    """Every variant of the products asks for the device's size or launches:
+    without a device both come back as a status."""
+    import torch
+    if torch.cuda.device_count() > 0:
+        pytest.skip("a device is there: the pointers of this test are not")
+    for dt in (0, 1, 2):
+        assert mm(clib, n=n, ldxs=n, dt=dt) == EHIP
+    assert gated(clib, n=n, ldxs=n, lds=n) == EHIP
+    assert gated(clib, n=n, ldxs=n, lds=n, m=20000, ldq=20096) == EHIP
+    assert weight(clib) == EHIP and acts(clib, n=n, lds=n) == EHIP and norm(clib, n=n, lds=n) == EHIP
+
+
 def test_binding_refuses_host_tensors():
     import torch
     from post_weight_quantization_04_amd import layer
