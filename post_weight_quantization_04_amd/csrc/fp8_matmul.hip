@@ -322,8 +322,10 @@ hipError_t few_launch(const MmArgs& a, TimedLaunch t, hipStream_t s) {
 //
 // Bound by MFMA: 16384 x 11008 -> 4096 in 588 us, 2510 TFLOP/s (e4m3 MFMA, 61 %
 // of the cycles busy); float32 8192 x 11008 -> 4096 in 544 us, 1360 TFLOP/s, and
-// the gated block 8192 x 4096 -> 11008 in 1159 us, 1275 TFLOP/s (float16 MFMA,
-// 51 % busy: the conversions and the scaling take the other cycles).
+// the gated block 8192 x 4096 -> 11008 in 1145 us, 1290 TFLOP/s (float16 MFMA,
+// 52 % busy: the conversions and the scaling take the other cycles).  Four waves
+// of twice the size in place of eight read less of LDS, and lose: 8192 x 11008
+// -> 4096, 256 x 128 394 us against 338, 256 x 256 1130 against 297.
 //
 // A copy instruction of a wave places 64 x 16 bytes one after the other: eight
 // rows of 128 bytes.  The chunk c of row r is put at c ^ f8_swizzle(r): each lane
