@@ -325,7 +325,8 @@ def obq_quantize(W, U, dead, bits: int, codes, scales, zeros, order=None, loss=N
 #
 # One decoded token's kernel takes 3 to 6 us, so these calls are written to
 # cost the host less: tensors are read once each, by the accessors that do not
-# build new objects, the names used by every call are set by load(), and
+# build new objects (asking whether a tensor is contiguous costs a third of
+# reading its strides), the names used by every call are set by load(), and
 # outputs that the caller made for the call (``made``, contiguous, of the right
 # type, shape and device) are not checked.
 # ---------------------------------------------------------------------------
@@ -372,25 +373,32 @@ def _fp8_stream(dev: int, stream) -> int:
     return stream.cuda_stream
 
 
+def _fp8_ld(t, rows: int, cols: int, what: str) -> int:
+    """Row stride of a 2-D view with unit column stride."""
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{what} must have unit column stride")
+    # the stride of a single row is never used, and torch leaves it arbitrary
+    return ld if rows > 1 else max(ld, cols)
+
+
 def _fp8_matrix(t, dev: int, what: str):
     """(pointer, row stride, rows, columns) of a 2-D view on device ``dev``
     with unit column stride."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or t.get_device() != dev or (stride[1] != 1 and shape[1] > 1):
+    shape = t.shape
+    if len(shape) != 2 or t.get_device() != dev:
         raise ValueError(f"{what} must be a 2-D view on cuda:{dev} with unit column stride")
     rows, cols = shape
-    # the stride of a single row is never used, and torch leaves it arbitrary
-    return t.data_ptr(), stride[0] if rows > 1 else max(stride[0], cols), rows, cols
+    return t.data_ptr(), cols if t.is_contiguous() else _fp8_ld(t, rows, cols, what), rows, cols
 
 
 def _fp8_operand(values, scales, cols: int, by_row: bool, dev: int, what: str):
     """(values pointer, ld, scales pointer, lds, rows) of an 8-bit matrix of
     ``cols`` columns: a scale per row and 128 columns (``by_row``), or per 128
     x 128 block."""
-    shape, stride, sshape, sstride = values.shape, values.stride(), scales.shape, scales.stride()
-    if (values.dtype not in _fp8_eights or scales.dtype != _fp8_scale or len(shape) != 2 or len(sshape) != 2
-            or values.get_device() != dev or scales.get_device() != dev or (stride[1] != 1 and shape[1] > 1)
-            or (sstride[1] != 1 and sshape[1] > 1)):
+    shape, sshape = values.shape, scales.shape
+    if (values.dtype not in _fp8_eights or scales.dtype is not _fp8_scale or len(shape) != 2 or len(sshape) != 2
+            or values.get_device() != dev or scales.get_device() != dev):
         raise ValueError(f"{what}: values must be a 2-D float8_e4m3fn view and scales a 2-D float32 view on cuda:{dev}, "
                          f"both with unit column stride")
     rows, held = shape
@@ -400,9 +408,8 @@ def _fp8_operand(values, scales, cols: int, by_row: bool, dev: int, what: str):
         raise ValueError(f"{what}: {held} stored columns hold fewer than {cols} rounded up to 128")
     if (lead < nb or along < rows) if by_row else (lead < (rows + 127) >> 7 or along < nb):
         raise ValueError(f"{what}: scales {(lead, along)} for {rows} x {cols}")
-    # (single rows: as above)
-    return (values.data_ptr(), stride[0] if rows > 1 else max(stride[0], held), scales.data_ptr(),
-            sstride[0] if lead > 1 else max(sstride[0], along), rows)
+    return (values.data_ptr(), held if values.is_contiguous() else _fp8_ld(values, rows, held, what),
+            scales.data_ptr(), along if scales.is_contiguous() else _fp8_ld(scales, lead, along, what), rows)
 
 
 def _fp8_made(values, scales, cols: int, along: int, dev: int):
