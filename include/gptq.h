@@ -442,7 +442,7 @@ int gptq_obq_quantize(const void* W, int w_dtype, int64_t d_out, int64_t d_in, c
  *           [ceil(d_out/128), lds].
  * Errors: GPTQ_EINVAL (negative size, ldw < d_in, ldq or lds too small,
  * unknown dtype, null pointer), GPTQ_EUNSUPPORTED (q or ldq not 16-byte
- * aligned, d_out or d_in above 2^24, 2^24 blocks or more).
+ * aligned, d_out or d_in above 2^24, 2^22 blocks or more).
  */
 int gptq_fp8_weight(const void* W, int w_dtype, int64_t d_out, int64_t d_in, int64_t ldw, uint8_t* q,
                     int64_t ldq, float* scales, int64_t lds, void* stream);

@@ -363,9 +363,10 @@ inline bool f8_short(int64_t ldq, int64_t d, int64_t lds, int64_t along) {
 }
 constexpr int64_t kF8MaxLd = (int64_t)1 << 22;  // 256 rows of a tile stay within 2^30 bytes
 constexpr int64_t kF8MaxRows = (int64_t)1 << 24;
-// a launch has fewer than 2^32 threads: 16 a (token, block) pair, 256 a block
-// of weights or 128 x 64 piece of channel-major activations, up to 512 a
-// normed row, 512 a 256 x 256 tile
+// a launch has fewer than 2^32 threads: 16 a (token, block) pair, 256 a 128 x 64
+// piece of channel-major activations, up to 512 a normed row, 512 a 256 x 256
+// tile
+constexpr int64_t kF8MaxWeightBlocks = ((int64_t)1 << 32) / kF8WeightThreads - 1;
 constexpr int64_t kF8MaxPairs = ((int64_t)1 << 28) - 1, kF8MaxPieces = ((int64_t)1 << 24) - 1;
 constexpr int64_t kF8MaxNormRows = ((int64_t)1 << 23) - 1, kF8MaxTiles = (int64_t)1 << 22;
 }  // namespace
@@ -377,7 +378,7 @@ int gptq_fp8_weight(const void* W, int w_dtype, int64_t d_out, int64_t d_in, int
     if (d_out == 0 || d_in == 0) return GPTQ_OK;
     if (!W || !q || !scales) return GPTQ_EINVAL;
     if (!f8_aligned(q, ldq) || d_out > kF8MaxRows || d_in > ((int64_t)1 << 24)) return GPTQ_EUNSUPPORTED;
-    if (f8_blocks(d_out) * f8_blocks(d_in) > kF8MaxPieces) return GPTQ_EUNSUPPORTED;
+    if (f8_blocks(d_out) * f8_blocks(d_in) > kF8MaxWeightBlocks) return GPTQ_EUNSUPPORTED;
     return hip_status(launch_f8_weight(W, w_dtype, d_out, d_in, ldw, q, ldq, scales, lds, as_stream(stream)));
 }
 

@@ -25,7 +25,7 @@ inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 1
 // 32.1 with plain stores; 512 and 256 threads 24.7 and 26.6 us, at 128 x 248
 // bfloat16 3.4 and 4.3 us against 3.2.
 // ---------------------------------------------------------------------------
-constexpr int kWThreads = 1024;
+constexpr int kWThreads = kF8WeightThreads;
 constexpr int kWRows = 128 * 16 / kWThreads;  // rows a thread
 
 template <typename T, bool kVec>
