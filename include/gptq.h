@@ -453,9 +453,9 @@ int gptq_fp8_weight(const void* W, int w_dtype, int64_t d_out, int64_t d_in, int
  *           the calibration inputs), of x_dtype, row stride ldx elements.
  *   q, scales  the outputs: values [n_tokens, ldq], scales [ceil(d/128), lds].
  * Errors: as gptq_fp8_weight, and GPTQ_EINVAL for channel_major not 0 or 1;
- * the limits are n_tokens below 2^31, d at most 2^24 and fewer than 2^28
- * (token, block of 128) pairs (channel_major: 2^24 pieces of 128 channels by
- * 64 tokens).
+ * the limits are n_tokens below 2^31, d at most 2^24 and at most 2^28 - 16
+ * (token, block of 128) pairs (channel_major: fewer than 2^24 pieces of 128
+ * channels by 64 tokens).
  */
 int gptq_fp8_activations(const void* X, int x_dtype, int64_t n_tokens, int64_t d, int64_t ldx, int channel_major,
                          uint8_t* q, int64_t ldq, float* scales, int64_t lds, void* stream);

@@ -363,12 +363,13 @@ inline bool f8_short(int64_t ldq, int64_t d, int64_t lds, int64_t along) {
 }
 constexpr int64_t kF8MaxLd = (int64_t)1 << 22;  // 256 rows of a tile stay within 2^30 bytes
 constexpr int64_t kF8MaxRows = (int64_t)1 << 24;
-// a launch has fewer than 2^32 threads: 16 a (token, block) pair, 256 a 128 x 64
-// piece of channel-major activations, up to 512 a normed row, 512 a 256 x 256
-// tile
-constexpr int64_t kF8MaxWeightBlocks = ((int64_t)1 << 32) / kF8WeightThreads - 1;
-constexpr int64_t kF8MaxPairs = ((int64_t)1 << 28) - 1, kF8MaxPieces = ((int64_t)1 << 24) - 1;
-constexpr int64_t kF8MaxNormRows = ((int64_t)1 << 23) - 1, kF8MaxTiles = (int64_t)1 << 22;
+// A launch has fewer than 2^32 threads; token-major activations come in whole
+// workgroups of sixteen pairs, products take up to 512 a 256 x 256 tile.
+constexpr int64_t f8_most_groups(int threads) { return ((int64_t)1 << 32) / threads - 1; }
+constexpr int64_t kF8MaxWeightBlocks = f8_most_groups(kF8WeightThreads);
+constexpr int64_t kF8MaxPairs = f8_most_groups(kF8RowsThreads) * (kF8RowsThreads / 16);
+constexpr int64_t kF8MaxPieces = f8_most_groups(kF8ColumnsThreads);
+constexpr int64_t kF8MaxNormRows = f8_most_groups(kF8NormThreads), kF8MaxTiles = (int64_t)1 << 22;
 }  // namespace
 
 int gptq_fp8_weight(const void* W, int w_dtype, int64_t d_out, int64_t d_in, int64_t ldw, uint8_t* q, int64_t ldq,

@@ -13,7 +13,7 @@ namespace gptq {
 
 namespace {
 
-constexpr int kQThreads = 256;
+constexpr int kQThreads = kF8RowsThreads;
 
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
@@ -95,6 +95,7 @@ __global__ __launch_bounds__(kQThreads) void f8_rows_kernel(const T* __restrict_
 constexpr int kCmTokens = 64;
 constexpr int kCmEights = kCmTokens / 8;
 constexpr int kCmThreads = 32 * kCmEights;
+static_assert(kCmThreads == kF8ColumnsThreads && kCmTokens == 64, "the entry point's limit");
 
 // word of (token, four channels): rows of 33 words, four more from token 64 on
 __device__ __forceinline__ int cm_word(int token, int quad) {
@@ -224,6 +225,7 @@ __device__ __forceinline__ void norm_chunk_out(const NormArgs<T>& a, float (&h)[
 
 template <typename T, int kThreads, int kRows, int kJ, bool kVec>
 __global__ __launch_bounds__(kThreads* kRows) void f8_rms_norm_kernel(NormArgs<T> a) {
+    static_assert(kThreads * kRows <= kF8NormThreads, "the entry point's limit");
     __shared__ float part[kThreads / kWave];
     const int tid = threadIdx.x % kThreads;
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kThreads;

@@ -121,6 +121,9 @@ hipError_t launch_propagate(const void* W, int64_t d_out, int64_t d_in, const vo
 // dtype codes as gptq_dtype: 0 f16, 1 f32, 2 bf16
 // Threads a workgroup: the entry points keep every launch below 2^32 threads.
 constexpr int kF8WeightThreads = 1024;  // per 128 x 128 block
+constexpr int kF8RowsThreads = 256;     // per 16 (token, block of 128) pairs
+constexpr int kF8ColumnsThreads = 256;  // per 128 channels x 64 tokens
+constexpr int kF8NormThreads = 512;     // per row, at most
 hipError_t launch_f8_weight(const void* W, int dtype, int64_t d_out, int64_t d_in, int64_t ldw, uint8_t* q,
                             int64_t ldq, float* scales, int64_t lds, hipStream_t s);
 hipError_t launch_f8_activations(const void* X, int dtype, int64_t n, int64_t d, int64_t ldx, int channel_major,

@@ -41,3 +41,37 @@ def test_weight_past_the_limit(clib, m, k):
 def test_weight_below_the_limit(clib, m, k):
     _no_device()
     assert weight(clib, m, k) == EHIP
+
+
+def acts(lib, n, d, cm=0):
+    return lib.gptq_fp8_activations(P, 0, n, d, n if cm else d, cm, P, (d + 127) // 128 * 128, P, n, None)
+
+
+# (token, block of 128) pairs, sixteen a workgroup of 256 threads: at most 2^28 - 16
+@pytest.mark.parametrize("n,d", [((1 << 28) - 15, 128), ((1 << 28) - 1, 1), ((1 << 27) - 7, 129), (1 << 28, 128)])
+def test_activations_past_the_limit(clib, n, d):
+    assert acts(clib, n, d) == EUNSUPPORTED
+
+
+@pytest.mark.parametrize("n,d", [((1 << 28) - 16, 128), ((1 << 27) - 8, 129)])
+def test_activations_below_the_limit(clib, n, d):
+    _no_device()
+    assert acts(clib, n, d) == EHIP
+
+
+# pieces of 128 channels by 64 tokens, 256 threads each: below 2^24
+def test_channel_major_activations_at_the_limit(clib):
+    assert acts(clib, (1 << 30) - 63, 128, 1) == EUNSUPPORTED
+    assert acts(clib, (1 << 29) - 63, 129, 1) == EUNSUPPORTED
+    _no_device()
+    assert acts(clib, (1 << 30) - 64, 128, 1) == EHIP
+
+
+# rows, up to 512 threads each: below 2^23
+def test_norm_at_the_limit(clib):
+    def norm(n):
+        return clib.gptq_fp8_rms_norm(P, 128, None, 0, None, 0, P, 0, n, 128, 1e-6, P, 128, P, n, None)
+
+    assert norm(1 << 23) == EUNSUPPORTED
+    _no_device()
+    assert norm((1 << 23) - 1) == EHIP
