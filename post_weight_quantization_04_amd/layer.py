@@ -307,8 +307,13 @@ def fp8_gated(gate: Fp8, up: Fp8, x: Fp8, ws: Optional[Workspace] = None, out: O
 
 def propagate_fp8(w: Fp8, X, relu: bool = False, out=None, stream=None):
     """``propagate`` through a layer kept in 8 bits: the activations ``X [d_in,
-    n]`` go to 8 bits, and ``act(W X)`` comes back as ``[d_out, n]`` in X's
-    type, the next layer's input."""
+    n]`` go to 8 bits, and ``act(W X)`` comes back as ``[d_out, n]``, the next
+    layer's input: in X's type, or float32 for bfloat16 X, since ``hessian``
+    takes float16 and float32.  A given ``out`` has the type that its owner
+    chose."""
     x = fp8_activations(X, channel_major=True, stream=stream)
-    return fp8_matmul(w, x, dtype=X.dtype if out is None else None, relu=relu, channel_major=True, out=out,
-                      stream=stream)
+    dtype = None
+    if out is None:
+        import torch
+        dtype = torch.float32 if X.dtype == torch.bfloat16 else X.dtype
+    return fp8_matmul(w, x, dtype=dtype, relu=relu, channel_major=True, out=out, stream=stream)

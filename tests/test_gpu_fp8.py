@@ -479,6 +479,39 @@ def test_propagate_fp8_feeds_the_next_hessian(lib):
     assert np.linalg.norm(np.tril(H) - np.tril(full)) <= 1e-5 * np.linalg.norm(np.tril(full))
 
 
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("d,n,m,relu", [(200, 5, 144, False), (130, 264, 300, True), (640, 1000, 257, False)])
+def test_propagate_fp8_of_every_type_feeds_the_next_hessian(lib, d, n, m, relu, name):
+    """float16 and float32 come back as they were, bfloat16 as float32; the
+    Hessian takes each, and a second layer of the chain the first one's."""
+    from post_weight_quantization_04_amd import layer
+    torch = _t()
+    say("propagate", d, n, m, relu, name)
+    rng = np.random.default_rng(d + n)
+    X, Xf = typed(rng.standard_normal((d, n)), name)
+    w8 = layer.fp8_weight(typed(rng.standard_normal((m, d)) * 0.1, name)[0])
+    Y = layer.propagate_fp8(w8, X, relu=relu)
+    back = "float32" if name == "bfloat16" else name
+    assert Y.shape == (m, n) and Y.dtype == getattr(torch, back)
+    xq, xs = ref.quantize_rows(np.ascontiguousarray(Xf.T))
+    want, dy = ref.product(ref.rows_values(xq, xs, d), ref.tiles_values(codes_of(w8), w8.scales.cpu().numpy(), d),
+                           ref.cuts(n, back))
+    want = np.maximum(want, 0) if relu else want
+    got = Y.float().cpu().numpy().T
+    assert np.all(np.abs(got - want) <= dy + ref.HALF[back] * (np.abs(want) + dy) + ref.TINY[back])
+    H = layer.hessian(Y).cpu().numpy()
+    full = 2 * got.astype(np.float64).T @ got
+    assert np.linalg.norm(np.tril(H) - np.tril(full)) <= 1e-5 * np.linalg.norm(np.tril(full))
+    v8 = layer.fp8_weight(typed(rng.standard_normal((64, m)) * 0.1, name)[0])
+    assert layer.propagate_fp8(v8, Y).dtype == Y.dtype
+    out = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    assert layer.propagate_fp8(w8, X, relu=relu, out=out) is out
+    _, dy = ref.product(ref.rows_values(xq, xs, d), ref.tiles_values(codes_of(w8), w8.scales.cpu().numpy(), d),
+                        ref.cuts(n, "bfloat16"))
+    off = np.abs(out.float().cpu().numpy().T - want)
+    assert np.all(off <= dy + 2.0 ** -8 * (np.abs(want) + dy) + 2.0 ** -134)
+
+
 @pytest.mark.parametrize("n", [2, 150])
 def test_graphs_and_streams(lib, n):
     """The chain captured twice on a side stream, replayed in turn with eager
