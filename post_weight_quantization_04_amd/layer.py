@@ -48,7 +48,7 @@ class Workspace:
                 self._kept.append(self.buf)
                 self._captured = False
             self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
-        if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+        if self.buf.is_cuda and torch.cuda.is_current_stream_capturing():
             self._captured = True
         return self.buf
 

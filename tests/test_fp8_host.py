@@ -162,3 +162,26 @@ def test_propagate_fp8_gives_a_type_that_hessian_takes(monkeypatch):
         _lib._dtype_code(Y)
         out = torch.empty(4, 4, dtype=torch.bfloat16)
         assert layer.propagate_fp8(None, X, out=out) is out
+
+
+def test_a_workspace_asks_only_whether_its_stream_is_captured(monkeypatch):
+    """Every call of the framework takes its scratch memory here: a host
+    buffer asks nothing, a device buffer the one question."""
+    import torch
+    from post_weight_quantization_04_amd import layer
+    asked = []
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: asked.append("available"))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: asked.append("capturing") or True)
+    ws = layer.Workspace("cpu")
+    assert ws.get(1000).numel() == 1000 and ws.get(10) is ws.buf and asked == []
+
+    class Device:
+        is_cuda = True
+
+        def numel(self):
+            return 5000
+
+    ws.buf = held = Device()
+    assert ws.get(5000) is held and asked == ["capturing"]
+    ws.get(6000)                   # handed out during a capture: kept for its graph
+    assert ws.buf is not held and ws._kept == [held]
