@@ -97,10 +97,8 @@ constexpr int kCmEights = kCmTokens / 8;
 constexpr int kCmThreads = 32 * kCmEights;
 static_assert(kCmThreads == kF8ColumnsThreads && kCmTokens == 64, "the entry point's limit");
 
-// word of (token, four channels): rows of 33 words, four more from token 64 on
-__device__ __forceinline__ int cm_word(int token, int quad) {
-    return token * (kF8Block / 4 + 1) + 4 * (token / 64) + quad;
-}
+// word of (token, four channels): rows of 33 words
+__device__ __forceinline__ int cm_word(int token, int quad) { return token * (kF8Block / 4 + 1) + quad; }
 
 template <typename T, bool kVec>
 __global__ __launch_bounds__(kCmThreads) void f8_columns_kernel(const T* __restrict__ X, int64_t n, int64_t d,
@@ -108,7 +106,7 @@ __global__ __launch_bounds__(kCmThreads) void f8_columns_kernel(const T* __restr
                                                                 float* __restrict__ scales, int64_t lds, unsigned nb) {
     constexpr int kWaves = kCmThreads / kWave;
     __shared__ uint32_t peaks[kWaves][kCmTokens];
-    __shared__ uint32_t codes[kCmTokens * (kF8Block / 4 + 1) + 4 * (kCmTokens / 64)];
+    __shared__ uint32_t codes[kCmTokens * (kF8Block / 4 + 1)];
     const int tid = threadIdx.x, lane = tid % kWave, w = tid / kWave;
     const int64_t blk = blockIdx.x % nb, t0 = (int64_t)(blockIdx.x / nb) * kCmTokens;
     const int64_t t = t0 + 8 * (tid % kCmEights), c0 = blk * kF8Block + 4 * (tid / kCmEights);
