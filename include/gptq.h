@@ -533,6 +533,15 @@ int gptq_fp8_gated(const uint8_t* gq, const float* gs, const uint8_t* uq, const 
                    int64_t ldxs, int64_t n_tokens, uint8_t* q, int64_t ldq, float* scales, int64_t lds,
                    void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Which kernel a product or gated block of these sizes runs on (a static
+ * string; measurement and test aid): by estimated time on a device of
+ * compute_units CUs, or on the current one where that is 0 or less.  NULL for
+ * sizes that the calls refuse or that are empty, and without a device.
+ */
+const char* gptq_fp8_matmul_kernel(int64_t d_out, int64_t d_in, int64_t n_tokens, int y_dtype, int compute_units);
+const char* gptq_fp8_gated_kernel(int64_t d_ff, int64_t d_in, int64_t n_tokens, int compute_units);
+
 /* Human-readable name of a gptq_status value (static string). */
 const char* gptq_status_string(int status);
 

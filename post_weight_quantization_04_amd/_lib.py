@@ -45,6 +45,8 @@ EXPORTS = (
     "gptq_fp8_matmul",
     "gptq_fp8_gated_workspace",
     "gptq_fp8_gated",
+    "gptq_fp8_matmul_kernel",
+    "gptq_fp8_gated_kernel",
     "gptq_kernel_count",
     "gptq_kernel_name",
     "gptq_timing_enable",
@@ -111,6 +113,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "gptq_fp8_gated_workspace": (_sz, [_i64, _i64]),
         "gptq_fp8_gated": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64,
                                   _vp, _i64, _vp, _sz, _vp]),
+        "gptq_fp8_matmul_kernel": (ctypes.c_char_p, [_i64, _i64, _i64, _i32, _i32]),
+        "gptq_fp8_gated_kernel": (ctypes.c_char_p, [_i64, _i64, _i64, _i32]),
         "gptq_kernel_count": (_i32, []),
         "gptq_kernel_name": (ctypes.c_char_p, [_i32]),
         "gptq_timing_enable": (_i32, [_i32]),
@@ -529,6 +533,19 @@ def fp8_gated(gq, gs, uq, us, xq, xs, d_in: int, values, scales, workspace=None,
                             _ptr(workspace), room, _fp8_stream(dev, stream))
     if rc:
         _check("gptq_fp8_gated", rc)
+
+
+def fp8_matmul_kernel(n: int, d_out: int, d_in: int, dtype, compute_units: int = 0) -> Optional[str]:
+    """Which kernel a product of these sizes and output type runs on, on a
+    device of ``compute_units`` CUs (0: the current one)."""
+    name = load().gptq_fp8_matmul_kernel(d_out, d_in, n, _fp8_codes[dtype], compute_units)
+    return name.decode() if name else None
+
+
+def fp8_gated_kernel(n: int, d_ff: int, d_in: int, compute_units: int = 0) -> Optional[str]:
+    """Which kernel a gated block of these sizes runs on."""
+    name = load().gptq_fp8_gated_kernel(d_ff, d_in, n, compute_units)
+    return name.decode() if name else None
 
 
 # ---------------------------------------------------------------------------

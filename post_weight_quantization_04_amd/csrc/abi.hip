@@ -452,4 +452,17 @@ int gptq_fp8_gated(const uint8_t* gq, const float* gs, const uint8_t* uq, const 
     return hip_status(launch_f8_gated(c, q, ldq, scales, lds, workspace, as_stream(stream)));
 }
 
+const char* gptq_fp8_matmul_kernel(int64_t d_out, int64_t d_in, int64_t n, int y_dtype, int compute_units) {
+    if (d_out <= 0 || d_in < 0 || n <= 0 || !f8_dtype(y_dtype)) return nullptr;
+    if (d_out > kF8MaxRows || n > kF8MaxRows || d_in > kF8MaxLd) return nullptr;
+    const int64_t cus = compute_units > 0 ? compute_units : device_cu_count();
+    return cus > 0 ? f8_matmul_kernel_name(d_out, d_in, n, y_dtype, cus) : nullptr;
+}
+
+const char* gptq_fp8_gated_kernel(int64_t d_ff, int64_t d_in, int64_t n, int compute_units) {
+    if (d_ff <= 0 || d_in < 0 || n <= 0 || d_ff > kF8MaxRows || n > kF8MaxRows || d_in > kF8MaxLd) return nullptr;
+    const int64_t cus = compute_units > 0 ? compute_units : device_cu_count();
+    return cus > 0 ? f8_gated_kernel_name(d_ff, d_in, n, cus) : nullptr;
+}
+
 }  // extern "C"

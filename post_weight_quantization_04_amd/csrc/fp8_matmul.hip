@@ -773,46 +773,54 @@ constexpr int64_t kFewTokens = 32;  // the few-token kernel always, up to here
 // (float32 63, 60, -, 66).  The few-token kernel against 64 x 64 tiles: 512 rows,
 // k 4096, 100 tokens 5.4 against 8.1 us (float32 13.6); 1363 rows, 200 tokens
 // 12.0 against 10.4 (15.2); 5376 rows, 64 tokens 12.0 against 9.6 (14.4).
+enum F8Kernel { kFew, k64Split, k64, k128x64Split, k128, k256x128, k256 };
+const char* const kF8KernelNames[] = {"few tokens", "64 x 64, k in two groups", "64 x 64", "128 x 64, k in two groups", "128 x 128",
+                                      "256 x 128", "256 x 256"};
+
+F8Kernel f8_matmul_choice(int64_t M, int64_t n, int nb, bool half, int64_t cus) {
+    if (n <= kFewTokens) return kFew;
+    auto rounds = [&](int64_t tm, int64_t tn, int64_t each) {
+        return (((M + tm - 1) / tm) * ((n + tn - 1) / tn) + cus * each - 1) / (cus * each);
+    };
+    const bool one = rounds(64, 64, 1) == 1, two = rounds(64, 64, 2) == 1;
+    auto cost = [&](int64_t rounds, double own, double block) { return rounds * (own + block * nb); };
+    const double groups = (double)f8_few_groups(n, M);
+    // (its grid's second dimension, 32 tokens each, holds less than 2^16)
+    const double few = n > ((int64_t)1 << 20) ? 1e30 : 1.3 + 0.002 * groups + (0.07 + 0.0003 * groups) * nb;
+    double t[] = {few, one ? cost(1, 2.5, 0.2) : 1e30, two ? cost(1, 2.2, 0.41) : cost(rounds(64, 64, 3), 1.4, 0.5),
+                  cost(rounds(128, 64, 1), 2.6, 0.33), cost(rounds(128, 128, 1), 1.7, 0.58),
+                  cost(rounds(256, 128, 1), 1.5, 1.05), cost(rounds(256, 256, 1), 1.3, 1.8)};
+    if (half) {
+        t[k64Split] = one ? cost(1, 2.5, 0.35) : 1e30;
+        t[k64] = two ? cost(1, 2.2, 0.76) : cost(rounds(64, 64, 3), 1.4, 1.3);
+        t[k128x64Split] = cost(rounds(128, 64, 1), 2.6, 0.55);
+        t[k128] = 1e30;
+        t[k256x128] = cost(rounds(256, 128, 1), 0.5, 1.8);
+        t[k256] = cost(rounds(256, 256, 1), 0.4, 3.0);
+    }
+    if (one) t[k64] = 1e30;
+    return (F8Kernel)(std::min_element(t, t + 7) - t);
+}
+
 template <typename T, bool kHalf>
 hipError_t matmul_typed(const MmArgs& m, hipStream_t s) {
     TimedLaunch t(K_F8_MATMUL, s);
-    if (m.n <= kFewTokens) return few_launch<T, 1>(m, t, s);
+    const int64_t cus = m.n <= kFewTokens ? 1 : device_cu_count();
+    if (cus <= 0) return hipErrorInvalidDevice;
     TileArgs a = {};
     a.m = m;
-    const int64_t cus = device_cu_count();
-    if (cus <= 0) return hipErrorInvalidDevice;
-    auto rounds = [&](int64_t tm, int64_t tn, int64_t each) {
-        return (((m.M + tm - 1) / tm) * ((m.n + tn - 1) / tn) + cus * each - 1) / (cus * each);
-    };
-    const bool one = rounds(64, 64, 1) == 1, two = rounds(64, 64, 2) == 1;
-    auto cost = [&](int64_t rounds, double own, double block) { return rounds * (own + block * m.nb); };
-    const double groups = (double)f8_few_groups(m.n, m.M);
-    // (its grid's second dimension, 32 tokens each, holds less than 2^16)
-    const double few = m.n > ((int64_t)1 << 20) ? 1e30 : 1.3 + 0.002 * groups + (0.07 + 0.0003 * groups) * m.nb;
-    if constexpr (kHalf) {
-        const double t64 = one ? cost(1, 2.5, 0.35) : two ? cost(1, 2.2, 0.76) : cost(rounds(64, 64, 3), 1.4, 1.3);
-        const double t96 = cost(rounds(128, 64, 1), 2.6, 0.55), t256 = cost(rounds(256, 128, 1), 0.5, 1.8);
-        const double t512 = cost(rounds(256, 256, 1), 0.4, 3.0);
-        const double least = std::min(std::min(t64, t96), std::min(t256, t512));
-        if (few <= least) return few_launch<T, 1>(m, t, s);
-        if (t64 == least && one) return tile_launch<T, 64, 64, 2, 2, 3, false, true, 2>(a, t, s);
-        if (t64 == least) return tile_launch<T, 64, 64, 2, 2, 3, false, true>(a, t, s);
-        if (t96 == least) return tile_launch<T, 128, 64, 2, 2, 3, false, true, 2>(a, t, s);
-        if (t256 == least) return tile_launch<T, 256, 128, 4, 2, 2, false, true>(a, t, s);
-        return tile_launch<T, 256, 256, 2, 4, 2, false, true, 1, false, false>(a, t, s);
-    } else {
-        const double t64 = one ? cost(1, 2.5, 0.2) : two ? cost(1, 2.2, 0.41) : cost(rounds(64, 64, 3), 1.4, 0.5);
-        const double t96 = cost(rounds(128, 64, 1), 2.6, 0.33), t128 = cost(rounds(128, 128, 1), 1.7, 0.58);
-        const double t256 = cost(rounds(256, 128, 1), 1.5, 1.05), t512 = cost(rounds(256, 256, 1), 1.3, 1.8);
-        const double least = std::min(std::min(t64, t96), std::min(t128, std::min(t256, t512)));
-        if (few <= least) return few_launch<T, 1>(m, t, s);
-        if (t64 == least && one) return tile_launch<T, 64, 64, 2, 2, 3, false, false, 2>(a, t, s);
-        if (t64 == least) return tile_launch<T, 64, 64, 2, 2, 3, false, false>(a, t, s);
-        if (t96 == least) return tile_launch<T, 128, 64, 2, 2, 3, false, false, 2>(a, t, s);
-        if (t128 == least) return tile_launch<T, 128, 128, 4, 2, 3, false, false>(a, t, s);
-        if (t256 == least) return tile_launch<T, 256, 128, 4, 2, 3, false, false>(a, t, s);
-        return tile_launch<T, 256, 256, 2, 4, 2, false, false>(a, t, s);
+    switch (f8_matmul_choice(m.M, m.n, m.nb, kHalf, cus)) {
+        case kFew: return few_launch<T, 1>(m, t, s);
+        case k64Split: return tile_launch<T, 64, 64, 2, 2, 3, false, kHalf, 2>(a, t, s);
+        case k64: return tile_launch<T, 64, 64, 2, 2, 3, false, kHalf>(a, t, s);
+        case k128x64Split: return tile_launch<T, 128, 64, 2, 2, 3, false, kHalf, 2>(a, t, s);
+        case k128:
+            if constexpr (!kHalf) return tile_launch<T, 128, 128, 4, 2, 3, false, false>(a, t, s);
+            break;
+        case k256x128: return tile_launch<T, 256, 128, 4, 2, kHalf ? 2 : 3, false, kHalf>(a, t, s);
+        case k256: return tile_launch<T, 256, 256, 2, 4, 2, false, kHalf, 1, !kHalf, !kHalf>(a, t, s);
     }
+    return hipErrorInvalidValue;
 }
 
 // Up to here the gated block may leave its products in float32 (a rule without
@@ -838,6 +846,13 @@ size_t f8_gated_workspace_bytes(int64_t n, int64_t d_ff) {
     return (size_t)(n * ((d_ff + kF8Block - 1) / kF8Block) * kF8Block) * sizeof(float);
 }
 
+namespace {
+
+enum F8GatedKernel { kGatedFew, kGated32, kGated64, kGated128x64, kGated128x128, kGated128x256 };
+const char* const kF8GatedNames[] = {"few tokens, then the quantizer", "32 channels x 64, k in two groups, then the quantizer",
+                                     "64 channels x 64, k in two groups, then the quantizer", "128 channels x 64",
+                                     "128 channels x 128", "128 channels x 256"};
+
 // In one kernel: tiles of 128 channels, which are whole blocks of the result,
 // 64, 128 or 256 tokens wide.  At 256 a wave converts fewer values for its
 // products (192 an m-tile for four token tiles of twice the rows, against 128),
@@ -854,44 +869,62 @@ size_t f8_gated_workspace_bytes(int64_t n, int64_t d_ff) {
 // 616.  1408 channels, k 4096, 100 tokens: 33.8, 22.0, 17.1 and 12.9 with the
 // few-token kernel; 200 tokens 34.1, 22.4, 18.4 and 18.1.  8320 channels, k
 // 128, 4671 tokens: 91, 65 and 50 us for 64, 128 and 256 tokens wide.
+F8GatedKernel f8_gated_choice(int64_t M, int64_t n, int nb, int64_t cus) {
+    if (n <= kFewTokens) return kGatedFew;
+    auto cost = [&](int64_t channels, int64_t tokens, double own, double block) {
+        const int64_t tiles = ((M + channels - 1) / channels) * ((n + tokens - 1) / tokens);
+        return ((tiles + cus - 1) / cus) * (own + block * nb);
+    };
+    double t[] = {1e30, 1e30, 1e30, cost(128, 64, 4.0, 0.97), cost(128, 128, 4.9, 1.73), cost(128, 256, 7.0, 3.1)};
+    if (f8_gated_in_two(n, M)) {
+        const double groups = (double)f8_few_groups(n, M);
+        const double two[] = {3.4 + 0.0032 * groups + (0.08 + 0.00037 * groups) * nb, cost(32, 64, 4.0, 0.32),
+                              cost(64, 64, 5.0, 0.47)};
+        for (int i = 0; i < 3; ++i) t[i] = two[i] + 2.0;
+        const double one = std::min(t[3], std::min(t[4], t[5]));
+        for (int i = 0; i < 3; ++i)
+            if (!(t[i] < one)) t[i] = 1e30;
+    }
+    return (F8GatedKernel)(std::min_element(t, t + 6) - t);
+}
+
+}  // namespace
+
+const char* f8_matmul_kernel_name(int64_t M, int64_t K, int64_t n, int y_dtype, int64_t cus) {
+    return kF8KernelNames[f8_matmul_choice(M, n, (int)((K + kF8Block - 1) / kF8Block), y_dtype == 1, cus)];
+}
+
+const char* f8_gated_kernel_name(int64_t M, int64_t K, int64_t n, int64_t cus) {
+    return kF8GatedNames[f8_gated_choice(M, n, (int)((K + kF8Block - 1) / kF8Block), cus)];
+}
+
 hipError_t launch_f8_gated(const F8Product& c, uint8_t* q, int64_t ldq, float* scales, int64_t lds, void* ws,
                            hipStream_t s) {
     const int64_t cus = device_cu_count();
     if (cus <= 0) return hipErrorInvalidDevice;
-    const bool two = f8_gated_in_two(c.n, c.M);
+    const int nb = (int)((c.K + kF8Block - 1) / kF8Block);
+    const F8GatedKernel kernel = f8_gated_choice(c.M, c.n, nb, cus);
+    const bool two = kernel <= kGated64;
     const int64_t ldh = (c.M + kF8Block - 1) / kF8Block * kF8Block;
     TileArgs t = {};
     t.m = {{c.wq[0], c.wq[1]}, {c.ws[0], c.ws[1]}, c.xq, c.xs, two ? ws : nullptr, c.ldw, c.ldws, c.ldx, c.ldxs,
-           two ? ldh : 0, c.M, c.n, (int)((c.K + kF8Block - 1) / kF8Block), 0, 0};
+           two ? ldh : 0, c.M, c.n, nb, 0, 0};
     t.q = q;
     t.qs = scales;
     t.ldq = ldq;
     t.ldqs = lds;
-    const int nb = t.m.nb;
-    auto cost = [&](int64_t channels, int64_t tokens, double own, double block) {
-        const int64_t tiles = ((c.M + channels - 1) / channels) * ((c.n + tokens - 1) / tokens);
-        return ((tiles + cus - 1) / cus) * (own + block * nb);
-    };
-    const double w64 = cost(128, 64, 4.0, 0.97), w128 = cost(128, 128, 4.9, 1.73), w256 = cost(128, 256, 7.0, 3.1);
-    const double one = std::min(w64, std::min(w128, w256));
     const TimedLaunch k(K_F8_GATED, s);
-    if (two) {
-        const double groups = (double)f8_few_groups(c.n, c.M);
-        const double few = 3.4 + 0.0032 * groups + (0.08 + 0.00037 * groups) * nb;
-        const double c32 = cost(32, 64, 4.0, 0.32), c64 = cost(64, 64, 5.0, 0.47);
-        const double least = std::min(few, std::min(c32, c64));
-        if (c.n <= kFewTokens || least + 2.0 < one) {
-            hipError_t e;
-            if (c.n <= kFewTokens || few == least) e = few_launch<float, 2>(t.m, k, s);
-            else if (c32 == least) e = tile_launch<float, 64, 64, 2, 2, 3, true, true, 2>(t, k, s);
-            else e = tile_launch<float, 128, 64, 2, 2, 3, true, true, 2>(t, k, s);
-            if (e != hipSuccess) return e;
-            return launch_f8_activations(ws, 1, c.n, c.M, ldh, 0, q, ldq, scales, lds, s);
-        }
+    hipError_t e = hipErrorInvalidValue;
+    switch (kernel) {
+        case kGatedFew: e = few_launch<float, 2>(t.m, k, s); break;
+        case kGated32: e = tile_launch<float, 64, 64, 2, 2, 3, true, true, 2>(t, k, s); break;
+        case kGated64: e = tile_launch<float, 128, 64, 2, 2, 3, true, true, 2>(t, k, s); break;
+        case kGated128x64: return tile_launch<float, 256, 64, 4, 2, 3, true, true>(t, k, s);
+        case kGated128x128: return tile_launch<float, 256, 128, 4, 2, 2, true, true>(t, k, s);
+        case kGated128x256: return tile_launch<float, 256, 256, 2, 4, 2, true, true, 1, false, false>(t, k, s);
     }
-    if (w64 == one) return tile_launch<float, 256, 64, 4, 2, 3, true, true>(t, k, s);
-    if (w128 == one) return tile_launch<float, 256, 128, 4, 2, 2, true, true>(t, k, s);
-    return tile_launch<float, 256, 256, 2, 4, 2, true, true, 1, false, false>(t, k, s);
+    if (e != hipSuccess) return e;
+    return launch_f8_activations(ws, 1, c.n, c.M, ldh, 0, q, ldq, scales, lds, s);
 }
 
 }  // namespace gptq

@@ -148,6 +148,9 @@ struct F8Product {
     int channel_major, relu;
 };
 hipError_t launch_f8_matmul(const F8Product& c, int y_dtype, hipStream_t s);
+// The kernel that sizes (n > 0, M > 0) are sent to on a device of `cus` compute units.
+const char* f8_matmul_kernel_name(int64_t M, int64_t K, int64_t n, int y_dtype, int64_t cus);
+const char* f8_gated_kernel_name(int64_t M, int64_t K, int64_t n, int64_t cus);
 size_t f8_gated_workspace_bytes(int64_t n, int64_t d_ff);
 hipError_t launch_f8_gated(const F8Product& c, uint8_t* q, int64_t ldq, float* scales, int64_t lds, void* ws,
                            hipStream_t s);
