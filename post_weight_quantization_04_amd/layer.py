@@ -265,7 +265,9 @@ def fp8_rms_norm(x, gain, eps: float = 1e-6, residual=None, out: Optional[Fp8] =
 def fp8_matmul(w: Fp8, x: Fp8, dtype=None, relu: bool = False, channel_major: bool = False, out=None, stream=None):
     """``act(X W^T)`` of an 8-bit weight and 8-bit activations
     (``gptq_fp8_matmul``): ``[n, d_out]``, or ``[d_out, n]`` with
-    ``channel_major``, as ``dtype`` (float16 by default)."""
+    ``channel_major``, as ``dtype`` (float16 by default).  float32 results are
+    summed in float32; 16-bit ones of more than 32 tokens may lose what lies 13
+    bits below the largest of eight neighbouring products."""
     if w.cols != x.cols:
         raise ValueError(f"weights of {w.cols} columns, activations of {x.cols}")
     if out is None:
