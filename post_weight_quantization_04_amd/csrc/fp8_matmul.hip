@@ -136,7 +136,8 @@ struct MmArgs {
 };
 
 // ---------------------------------------------------------------------------
-// Few tokens: sixteen weight rows and 16 kTn tokens a workgroup.  The waves
+// Few tokens, and small products of more: sixteen weight rows and 16 kTn tokens
+// a workgroup, so that the weights are read once for every 32 tokens.  The waves
 // share the blocks of k and work on their own, without barriers: a wave copies
 // its next two blocks to its own part of LDS (eight rows of 128 bytes
 // an instruction; loads into registers would ask for 64 separate pieces of 16
@@ -320,9 +321,9 @@ hipError_t few_launch(const MmArgs& a, TimedLaunch t, hipStream_t s) {
 // row) of both operands is a stage; stages are copied from memory to LDS without
 // passing registers, kStages - 1 ahead of the one in use, one barrier a stage.
 //
-// Bound by MFMA: 16384 x 11008 -> 4096 in 588 us, 2510 TFLOP/s (e4m3 MFMA, 61 %
-// of the cycles busy); float32 8192 x 11008 -> 4096 in 544 us, 1360 TFLOP/s, and
-// the gated block 8192 x 4096 -> 11008 in 1145 us, 1290 TFLOP/s (float16 MFMA,
+// Bound by MFMA: 16384 x 11008 -> 4096 in 589 us, 2510 TFLOP/s (e4m3 MFMA, 63 %
+// of the cycles busy); float32 8192 x 11008 -> 4096 in 538 us, 1370 TFLOP/s, and
+// the gated block 8192 x 4096 -> 11008 in 1130 us, 1310 TFLOP/s (float16 MFMA,
 // 52 % busy: the conversions and the scaling take the other cycles).  Four waves
 // of twice the size in place of eight read less of LDS, and lose: 8192 x 11008
 // -> 4096, 256 x 128 394 us against 338, 256 x 256 1130 against 297.
@@ -762,9 +763,12 @@ constexpr int64_t kFewTokens = 32;  // the few-token kernel always, up to here
 //                   256 x 256   256 x 128   128 x 128   128 x 64*  64 x 64, three a CU  two   one*
 //   e4m3 MFMA       1.3 + 1.8   1.5 + 1.05  1.7 + 0.58  2.6 + 0.33  1.4 + 0.5   2.2 + 0.41  2.5 + 0.2
 //   float16 MFMA    0.4 + 3.0   0.5 + 1.8               2.6 + 0.55  1.4 + 1.3   2.2 + 0.76  2.5 + 0.35
-// (*: two groups of waves share k).  The few-token kernel, which runs
-// workgroups of sixteen rows by 32 tokens: 1.3 us, 0.002 a workgroup and, a
-// block, 0.07 and 0.0003 a workgroup.  Measured, 4096 x 4096 weights, e4m3: 256
+// (*: two groups of waves share k).  The parts fit whole times over many sizes;
+// they do not split one launch's time (256 x 128, 2048 tokens, 4096 rows: 8.7 us
+// at one block, 14.8 at 8, 33.8 at 32, 62.4 at 64, Y included).  The few-token
+// kernel, which runs workgroups of sixteen rows by 32 tokens and reads the
+// weights again for each 32: 1.3 us, 0.002 a workgroup and, a block, 0.07 and
+// 0.0003 a workgroup.  Measured, 4096 x 4096 weights, e4m3: 256
 // tokens 10.7 us in 64 x 64 tiles (13.4 in one group), 13.4 in 128 x 64, 29 in
 // 256 x 128; 512 tokens 14.6 in 128 x 64, 16.5 in 64 x 64; 1024 tokens 22 in 128
 // x 128, 28 in 128 x 64, 31 in 256 x 128; 4096 tokens 59 in 256 x 256 (float32
@@ -823,9 +827,10 @@ hipError_t matmul_typed(const MmArgs& m, hipStream_t s) {
     return hipErrorInvalidValue;
 }
 
-// Up to here the gated block may leave its products in float32 (a rule without
-// k: the workspace's size goes by it): few tokens, or tiles of 128 channels by
-// 64 tokens that leave half of the CUs idle.
+// Up to here the gated block may leave its products in float32: few tokens, or
+// tiles of 128 channels by 64 tokens that leave half of 256 CUs idle.  The
+// workspace's size goes by this rule, so it knows neither k nor the device; the
+// choice below, which does, may still take one kernel.
 constexpr int64_t kGatedTiles = 128;
 bool f8_gated_in_two(int64_t n, int64_t M) {
     return n <= kFewTokens || ((M + kF8Block - 1) / kF8Block) * ((n + 63) / 64) <= kGatedTiles;

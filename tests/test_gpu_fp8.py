@@ -278,8 +278,8 @@ def test_matmul(lib, n, m, d, name, channel_major):
     assert (rest[shape[0]:] == 3).all() and (rest[:, shape[1]:] == 3).all()
 
 
-# every tile: 256 x 256, 256 x 128, 128 x 128, 128 x 64 and 64 x 64, the last of
-# them in ragged sizes too, over k that ends inside a round of 64 scales and past it
+# tiles from 64 x 64 to 256 x 256 and once the few-token kernel, most in ragged
+# sizes, mostly of a few blocks of k (``fp8_cases`` holds sizes of every kernel by name)
 LARGE = [(4090, 4100, 300), (2040, 4096, 200), (1020, 4096, 260), (500, 4096, 128), (700, 4000, 8400), (90, 300, 16520),
          (1030, 1025, 72), (500, 4096, 1300), (4090, 4096, 600), (4000, 4090, 250)]
 
