@@ -32,8 +32,9 @@ class Workspace:
     """Grow-only device scratch buffer shared by the calls of one stream.
 
     A buffer that a captured graph uses is kept when the workspace grows: the
-    graph goes on writing to it whenever it is replayed.  Replays and calls
-    that share a workspace have to run one after the other."""
+    graph goes on writing to it whenever it is replayed, so the workspace has
+    to live as long as the graph.  Replays and calls that share a workspace
+    have to run one after the other."""
 
     def __init__(self, device="cuda"):
         self.device = device
