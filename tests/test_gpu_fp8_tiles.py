@@ -115,6 +115,29 @@ def test_accuracy_of_sums(lib, n, m, d, name, dtype):
 
 
 @pytest.mark.parametrize("n,m,d,name,dtype", fp8_cases.matmul())
+def test_what_cancels(lib, n, m, d, name, dtype):
+    """Products of 2^16 and -2^16, seven of 3.5 beside the first: float32
+    results and the few-token kernel hold the rest, 24.5; the e4m3 MFMA may cut
+    it, within 2^-10 of the sum of magnitudes."""
+    from post_weight_quantization_04_amd import layer
+    torch = _t()
+    say("cancels", n, m, d, name, dtype)
+    x, w = torch.zeros((n, d), device="cuda"), torch.zeros((m, d), device="cuda")
+    x[:, 0] = x[:, d - 1] = w[:, 0] = 256
+    w[:, d - 1] = -256
+    x[:, 1:8], w[:, 1:8] = 3.5, 1
+    x8 = held(x, torch.ones((ref.blocks(d), n), device="cuda"))
+    w8 = held(w, torch.ones((ref.blocks(m), ref.blocks(d)), device="cuda"))
+    y = layer.fp8_matmul(w8, x8, dtype=getattr(torch, dtype)).float()
+    if dtype == "float32" or name == "few tokens":
+        assert bool((y == 24.5).all())
+    else:
+        assert float((y - 24.5).abs().max()) <= 2.0 ** -10 * (2 * 65536 + 24.5)
+    few = layer.fp8_matmul(w8, layer.Fp8(x8.data[:32], x8.scales[:, :32], d), dtype=getattr(torch, dtype))
+    assert bool((few == 24.5).all())
+
+
+@pytest.mark.parametrize("n,m,d,name,dtype", fp8_cases.matmul())
 def test_bad_values_stay_where_they_belong(lib, n, m, d, name, dtype):
     """A NaN and infinities in tokens (the last one in the last block of k) and
     a NaN in a weight: those tokens and that block of 128 channels are NaN, and
