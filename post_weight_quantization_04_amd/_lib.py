@@ -538,7 +538,7 @@ def fp8_gated(gq, gs, uq, us, xq, xs, d_in: int, values, scales, workspace=None,
 def fp8_matmul_kernel(n: int, d_out: int, d_in: int, dtype, compute_units: int = 0) -> Optional[str]:
     """Which kernel a product of these sizes and output type runs on, on a
     device of ``compute_units`` CUs (0: the current one)."""
-    name = load().gptq_fp8_matmul_kernel(d_out, d_in, n, _fp8_codes[dtype], compute_units)
+    name = load().gptq_fp8_matmul_kernel(d_out, d_in, n, _fp8_codes.get(dtype, -1), compute_units)
     return name.decode() if name else None
 
 

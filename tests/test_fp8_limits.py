@@ -123,6 +123,10 @@ def test_kernel_names_of_empty_and_refused_sizes(clib):
                     (4, 128, (1 << 24) + 1)):
         assert clib.gptq_fp8_matmul_kernel(m, d, n, 0, 256) is None and clib.gptq_fp8_gated_kernel(m, d, n, 256) is None
     assert clib.gptq_fp8_matmul_kernel(4, 128, 4, 3, 256) is None
+    import torch
+    from post_weight_quantization_04_amd import _lib
+    assert _lib.fp8_matmul_kernel(4, 4, 128, torch.float64, 256) is None
+    assert _lib.fp8_matmul_kernel(4, 4, 128, torch.bfloat16, 256) == "few tokens"
     _no_device()
     assert clib.gptq_fp8_matmul_kernel(400, 128, 400, 0, 0) is None and clib.gptq_fp8_gated_kernel(400, 128, 400, 0) is None
 
