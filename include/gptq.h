@@ -22,6 +22,12 @@
  * (gptq_fp8_matmul) and the gated feed-forward projections
  * (gptq_fp8_gated).
  *
+ * What carries activations through a block of quantized layers: the product
+ * with packed few-bit weights (gptq_packed_matmul), the attention over whole
+ * prompts (gptq_attention), the store of new keys and values into a paged
+ * cache (gptq_cache_store) and the attention of one new token over that cache
+ * (gptq_cached_attention).
+ *
  * Conventions shared by every entry point
  *   - Tensor arguments are DEVICE pointers allocated and owned by the caller;
  *     the library never allocates, frees or keeps caller memory.  Scratch
@@ -61,7 +67,8 @@ typedef enum {
 typedef enum {
     GPTQ_F16 = 0, /* IEEE binary16 */
     GPTQ_F32 = 1, /* IEEE binary32 */
-    GPTQ_BF16 = 2 /* bfloat16; taken by the gptq_fp8_* calls only */
+    GPTQ_BF16 = 2 /* bfloat16; taken by the gptq_fp8_* calls, gptq_packed_matmul
+                   * and the attention and cache calls */
 } gptq_dtype;
 
 /*
@@ -550,6 +557,131 @@ int gptq_fp8_gated(const uint8_t* gq, const float* gs, const uint8_t* uq, const 
  */
 const char* gptq_fp8_matmul_kernel(int64_t d_out, int64_t d_in, int64_t n_tokens, int y_dtype, int compute_units);
 const char* gptq_fp8_gated_kernel(int64_t d_ff, int64_t d_in, int64_t n_tokens, int compute_units);
+
+/*
+ * Product with packed few-bit weights, bias, activation and residual:
+ *     y[t, o] = act( sum_g s[o, g] sum_{k in g} (q[o, k] - z[o, g]) x[t, k] + b[o] ) + r[t, o]
+ * over the codes of gptq_pack_codes and the grids of gptq_quantize_layer: the
+ * layer is run as it is stored, without a float16 copy of its weights.  The
+ * differences q - z are whole numbers that both 16-bit types hold, so every
+ * product is exact; products are summed on MFMA in float32, a group's sum (or
+ * that of a part of it) times its scale is added in float32, and bias,
+ * activation and residual follow in float32; y is rounded once.
+ *   packed    [d_out, gptq_packed_words(d_in, bits)] uint32.
+ *   scales    [d_out, n_groups] float32, zeros [d_out, n_groups] int32 within
+ *             [0, 2^bits - 1] (others give unspecified values), n_groups = 1
+ *             if group_size == 0 else d_in / group_size.
+ *   X         [n_tokens, d_in] of x_dtype (GPTQ_F16 or GPTQ_BF16), row stride
+ *             ldx elements.
+ *   bias      [d_out] of y_dtype, or NULL.
+ *   residual  [n_tokens, d_out] of y_dtype, row stride ldr, or NULL; it may be
+ *             Y itself (same pointer and stride).
+ *   Y         [n_tokens, d_out] of y_dtype (x_dtype or GPTQ_F32), row stride
+ *             ldy elements.
+ *   activation 0: none; 1: max(0, .), a NaN kept; 2: v / (1 + exp(-v)); 3:
+ *             v (1 + erf(v / sqrt 2)) / 2.
+ * d_in = 0 gives act(b) + r.  Rows need no more than their type's alignment;
+ * rows of X that start 16-byte aligned with d_in a multiple of 8 load faster.
+ * Which kernel runs, and with it the order of the sums, goes by the sizes.
+ * Errors: GPTQ_EINVAL (negative size, bits outside [2, 8], negative
+ * group_size or one not dividing d_in, a stride below its row, unknown dtype
+ * or activation, null pointer), GPTQ_EUNSUPPORTED (x_dtype GPTQ_F32, y_dtype
+ * neither x_dtype nor GPTQ_F32, group_size not a multiple of 16, d_in or ldx
+ * above 2^21, d_out or n_tokens above 2^24, more than 2^22 tiles of 256 rows
+ * by 256 tokens).
+ */
+int gptq_packed_matmul(const uint32_t* packed, int bits, int64_t d_out, int64_t d_in, const float* scales,
+                       const int32_t* zeros, int64_t group_size, const void* X, int x_dtype, int64_t n_tokens,
+                       int64_t ldx, const void* bias, const void* residual, int64_t ldr, void* Y, int y_dtype,
+                       int64_t ldy, int activation, void* stream);
+
+/*
+ * Attention over whole prompts, several sequences packed one behind the other:
+ *     y[i, h] = sum_j p_ij v[j, h'],  p_ij = softmax over j of scale q[i, h] . k[j, h'],
+ *     h' = h / (heads / kv_heads),
+ * where j runs over the tokens of i's own sequence, up to i with causal.  What
+ * lies outside (later tokens, other sequences) has no influence, infinities and
+ * NaN included.  Scores, maxima, sums and outputs are float32; the weights
+ * exp(.) go into the second product rounded to the inputs' type, as its
+ * matrix instruction takes them, and are summed before that rounding; y is
+ * rounded once.
+ *   q, out    [n_tokens, heads, head_dim], k, v [n_tokens, kv_heads, head_dim]
+ *             of dtype (GPTQ_F16 or GPTQ_BF16); each with a stride per token
+ *             and one per head, in elements, the last dimension contiguous.
+ *             out overlaps none of the others.
+ *   starts    device [n_seqs + 1] int32, not decreasing, within [0, n_tokens]:
+ *             sequence s holds the tokens [starts[s], starts[s + 1]), and may
+ *             be empty.  Tokens of no sequence are neither read nor written.
+ *             NULL with n_seqs = 1: one sequence of all tokens.
+ *   scale     finite and above 0; scores times scale have to be finite.
+ * Errors: GPTQ_EINVAL (negative size, heads not a multiple of kv_heads, a
+ * stride below head_dim, starts NULL with n_seqs not 1, causal not 0 or 1,
+ * scale not finite or not above 0, unknown dtype, null pointer),
+ * GPTQ_EUNSUPPORTED (GPTQ_F32, head_dim above 128 or not a multiple of 8,
+ * pointers or strides not 16-byte aligned, a token stride above 2^22, n_tokens
+ * or n_seqs above 2^24, heads above 2^16, more than 2^22 pieces of 32 rows by
+ * head).
+ */
+int gptq_attention(const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token, int64_t k_head,
+                   const void* v, int64_t v_token, int64_t v_head, void* out, int64_t out_token, int64_t out_head,
+                   int dtype, int64_t n_tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                   const int32_t* starts, int64_t n_seqs, int causal, double scale, void* stream);
+
+/*
+ * Paged cache of keys and values.  keys and values are [pages, kv_heads,
+ * page_size, head_dim] of one 16-bit type, with a stride per page, per head and
+ * per row (elements, the last dimension contiguous), so that other orders of
+ * the first three dimensions will do as well.  A token's slot is page *
+ * page_size + row.
+ *
+ * gptq_cache_store copies new tokens into it, keys[page, h, row] = k[t, h] and
+ * the same for the values, for slot[t] = page * page_size + row.
+ *   k, v      [n_tokens, kv_heads, head_dim] of dtype, a stride per token and
+ *             one per head.
+ *   slots     device [n_tokens] int32.  A slot outside [0, pages * page_size)
+ *             (-1, say, for the padding of a batch) stores nothing.  The others
+ *             have to differ from one another.
+ * Errors: GPTQ_EINVAL (negative size, page_size below 1, a stride below
+ * head_dim, unknown dtype, null pointer), GPTQ_EUNSUPPORTED (GPTQ_F32, head_dim
+ * above 128 or not a multiple of 8, pointers or strides not 16-byte aligned,
+ * pages * page_size of 2^31 or more, n_tokens * kv_heads above 2^27).
+ */
+int gptq_cache_store(const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token, int64_t v_head,
+                     int dtype, int64_t n_tokens, int64_t kv_heads, int64_t head_dim, const int32_t* slots, void* keys,
+                     int64_t key_page, int64_t key_head, int64_t key_row, void* values, int64_t value_page,
+                     int64_t value_head, int64_t value_row, int64_t pages, int64_t page_size, void* stream);
+
+/*
+ * Attention of one new token of each sequence over its part of a paged cache:
+ *     y[b, h] = sum_{j < lengths[b]} p_j V[b, j, h'],  p = softmax over j of scale q[b, h] . K[b, j, h'],
+ * token j of sequence b on page table[b, j / page_size], row j % page_size
+ * (store the new token first to have it attend to itself).  Rows of pages
+ * behind the length have no influence, infinities and NaN included, and
+ * neither have tokens on a page number outside [0, pages): -1 marks a page
+ * that was freed.  A sequence without tokens gives zeros.  Numbers as for
+ * gptq_attention.  A long sequence is divided among many workgroups, which
+ * leave partial results in the workspace; a second kernel joins them in a
+ * fixed order.
+ *   q, out    [n_seqs, heads, head_dim] of dtype, a stride per sequence and one
+ *             per head.
+ *   table     device [n_seqs, ldt] int32, max_pages columns of it in use.
+ *   lengths   device [n_seqs] int32; below 0 counts as 0, above max_pages *
+ *             page_size as that.
+ *   workspace device memory of at least gptq_cached_attention_workspace() bytes,
+ *             256-byte aligned; clobbered, needs no clearing.
+ * Errors: as gptq_attention and gptq_cache_store (max_pages negative or above
+ * ldt: GPTQ_EINVAL; max_pages * page_size of 2^31 or more, n_seqs above 2^20:
+ * GPTQ_EUNSUPPORTED), and GPTQ_EWORKSPACE.
+ */
+size_t gptq_cached_attention_workspace(int64_t n_seqs, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                       int64_t max_pages, int64_t page_size);
+int gptq_cached_attention(const void* q, int64_t q_seq, int64_t q_head, const void* keys, int64_t key_page,
+                          int64_t key_head, int64_t key_row, const void* values, int64_t value_page,
+                          int64_t value_head, int64_t value_row, int64_t pages, int64_t page_size,
+                          const int32_t* table, int64_t ldt, int64_t max_pages, const int32_t* lengths,
+                          int64_t n_seqs, int64_t heads, int64_t kv_heads, int64_t head_dim, void* out,
+                          int64_t out_seq, int64_t out_head, int dtype, double scale, void* workspace,
+                          size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a gptq_status value (static string). */
 const char* gptq_status_string(int status);

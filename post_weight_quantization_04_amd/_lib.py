@@ -47,6 +47,11 @@ EXPORTS = (
     "gptq_fp8_gated",
     "gptq_fp8_matmul_kernel",
     "gptq_fp8_gated_kernel",
+    "gptq_packed_matmul",
+    "gptq_attention",
+    "gptq_cache_store",
+    "gptq_cached_attention_workspace",
+    "gptq_cached_attention",
     "gptq_kernel_count",
     "gptq_kernel_name",
     "gptq_timing_enable",
@@ -115,6 +120,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                   _vp, _i64, _vp, _sz, _vp]),
         "gptq_fp8_matmul_kernel": (ctypes.c_char_p, [_i64, _i64, _i64, _i32, _i32]),
         "gptq_fp8_gated_kernel": (ctypes.c_char_p, [_i64, _i64, _i64, _i32]),
+        "gptq_packed_matmul": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _i64, _i64, _vp, _vp, _i64,
+                                      _vp, _i32, _i64, _i32, _vp]),
+        "gptq_attention": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64, _i64,
+                                  _i64, _i64, _vp, _i64, _i32, ctypes.c_double, _vp]),
+        "gptq_cache_store": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64, _i64, _i64, _vp, _vp, _i64, _i64,
+                                    _i64, _vp, _i64, _i64, _i64, _i64, _i64, _vp]),
+        "gptq_cached_attention_workspace": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64]),
+        "gptq_cached_attention": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _vp,
+                                         _i64, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _i32,
+                                         ctypes.c_double, _vp, _sz, _vp]),
         "gptq_kernel_count": (_i32, []),
         "gptq_kernel_name": (ctypes.c_char_p, [_i32]),
         "gptq_timing_enable": (_i32, [_i32]),
@@ -337,13 +352,15 @@ def obq_quantize(W, U, dead, bits: int, codes, scales, zeros, order=None, loss=N
 _fp8_codes = {}          # torch type -> gptq_dtype
 _fp8_eights = ()         # types of the 8-bit values
 _fp8_scale = None        # type of the scales
+_int32 = None
 _fp8_current = None      # () -> index of the current device
 _fp8_current_stream = None  # (device index) -> handle of its current stream
 
 
 def _fp8_names() -> None:
-    global _fp8_codes, _fp8_eights, _fp8_scale, _fp8_current, _fp8_current_stream
+    global _fp8_codes, _fp8_eights, _fp8_scale, _int32, _fp8_current, _fp8_current_stream
     import torch
+    _int32 = torch.int32
     _fp8_codes = {torch.float16: GPTQ_F16, torch.float32: GPTQ_F32, torch.bfloat16: GPTQ_BF16}
     _fp8_eights = (torch.float8_e4m3fn, torch.uint8)
     _fp8_scale = torch.float32
@@ -546,6 +563,173 @@ def fp8_gated_kernel(n: int, d_ff: int, d_in: int, compute_units: int = 0) -> Op
     """Which kernel a gated block of these sizes runs on."""
     name = load().gptq_fp8_gated_kernel(d_ff, d_in, n, compute_units)
     return name.decode() if name else None
+
+
+# ---------------------------------------------------------------------------
+# Products with packed weights, attention and the paged cache.  As above, these
+# calls are written to cost the host little: they take as long as a small call's
+# kernel.
+# ---------------------------------------------------------------------------
+ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3}
+
+
+def _whole_numbers(t, dev: int, what: str):
+    """(pointer, row stride) of a 1-D or 2-D int32 tensor on device ``dev``,
+    its last dimension contiguous."""
+    if t.dtype is not _int32 or t.get_device() != dev:
+        raise ValueError(f"{what} must be int32 on cuda:{dev}")
+    if not t.is_contiguous() and (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{what} must be contiguous in its last dimension")
+    if len(t.shape) == 1:
+        return t.data_ptr(), 0
+    rows, cols = t.shape
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+
+
+def packed_matmul(packed, bits: int, d_in: int, scales, zeros, group_size: int, X, Y, bias=None, residual=None,
+                  activation: int = 0, stream=None) -> None:
+    """``Y = act(X W^T + bias) + residual`` over packed codes, ``X [n, d_in]``
+    and ``Y [n, d_out]`` 2-D views with unit column stride."""
+    lib = _lib or load()
+    dev = _fp8_device(Y)
+    yp, ldy, n, d_out = _fp8_matrix(Y, dev, "Y")
+    xp, ldx, n_x, d_x = _fp8_matrix(X, dev, "X")
+    if n_x != n or d_x != d_in:
+        raise ValueError(f"X is {n_x} x {d_x}, the product {n} x {d_in}")
+    groups = d_in // group_size if group_size > 0 else 1
+    shape, kind = scales.shape, Y.dtype
+    if (packed.dtype is not _int32 or packed.get_device() != dev or not packed.is_contiguous()
+            or len(packed.shape) != 2 or packed.shape[0] != d_out
+            or packed.shape[1] != max((d_in * bits + 31) >> 5, 1)):
+        raise ValueError(f"packed must be a contiguous int32 [{d_out}, {max((d_in * bits + 31) >> 5, 1)}] on cuda:{dev}")
+    if (len(shape) != 2 or shape[0] != d_out or shape[1] != groups or zeros.shape != shape or scales.dtype is not _fp8_scale
+            or zeros.dtype is not _int32 or scales.get_device() != dev or zeros.get_device() != dev
+            or not scales.is_contiguous() or not zeros.is_contiguous()):
+        raise ValueError(f"scales (float32) and zeros (int32) must be contiguous [{d_out}, {groups}] on cuda:{dev}")
+    bp, rp, ldr = None, None, 0
+    if bias is not None:
+        if bias.shape != Y.shape[1:] or bias.dtype != kind or bias.get_device() != dev or not bias.is_contiguous():
+            raise ValueError("bias must be a contiguous vector of Y's type, one value per output")
+        bp = bias.data_ptr()
+    if residual is not None:
+        if residual.shape != Y.shape or residual.dtype != kind:
+            raise ValueError("residual must have the shape and type of Y")
+        rp, ldr, _, _ = _fp8_matrix(residual, dev, "residual")
+    rc = lib.gptq_packed_matmul(packed.data_ptr(), bits, d_out, d_in, scales.data_ptr(), zeros.data_ptr(), group_size,
+                                xp, _fp8_dtype(X), n, ldx, bp, rp, ldr, yp, _fp8_dtype(Y), ldy, activation,
+                                _fp8_stream(dev, stream))
+    if rc:
+        _check("gptq_packed_matmul", rc)
+
+
+def _heads_of(t, dev: int, kind, what: str):
+    """(pointer, token stride, head stride, tokens, heads, d) of a [tokens,
+    heads, d] view on device ``dev`` with unit last stride."""
+    shape = t.shape
+    if len(shape) != 3 or t.dtype is not kind or t.get_device() != dev:
+        raise ValueError(f"{what} must be a 3-D {kind} view on cuda:{dev}")
+    n, heads, d = shape
+    if t.is_contiguous():
+        return t.data_ptr(), heads * d, d, n, heads, d
+    token, head, step = t.stride()
+    if step != 1 and d > 1:
+        raise ValueError(f"{what} must be contiguous in its last dimension")
+    # strides that are never used, and that torch leaves arbitrary
+    if heads <= 1:
+        head = d
+    if n <= 1:
+        token = max(d, 8)
+    return t.data_ptr(), token, head, n, heads, d
+
+
+def _pages_of(t, dev: int, kind, what: str):
+    """(pointer, page, head and row strides) of a [pages, heads, rows, d] view."""
+    shape = t.shape
+    if len(shape) != 4 or t.dtype is not kind or t.get_device() != dev:
+        raise ValueError(f"{what} must be a 4-D {kind} view on cuda:{dev}")
+    pages, heads, rows, d = shape
+    if t.is_contiguous():
+        return t.data_ptr(), heads * rows * d, rows * d, d
+    page, head, row, step = t.stride()
+    if step != 1 and d > 1:
+        raise ValueError(f"{what} must be contiguous in its last dimension")
+    return t.data_ptr(), page if pages > 1 else max(d, 8), head if heads > 1 else d, row if rows > 1 else d
+
+
+def attention(q, k, v, starts, out, causal: bool, scale: float, stream=None) -> None:
+    """Attention over packed prompts: ``q``, ``out`` [n, heads, d], ``k``, ``v``
+    [n, kv_heads, d], ``starts`` [n_seqs + 1] int32 or None (one sequence)."""
+    lib = _lib or load()
+    dev, kind = _fp8_device(q), q.dtype
+    qp, qt, qh, n, heads, d = _heads_of(q, dev, kind, "q")
+    kp, kt, kh, n_k, kv_heads, d_k = _heads_of(k, dev, kind, "k")
+    vp, vt, vh, n_v, heads_v, d_v = _heads_of(v, dev, kind, "v")
+    op, ot, oh, n_o, heads_o, d_o = _heads_of(out, dev, kind, "out")
+    if n_k != n or n_v != n or n_o != n or heads_v != kv_heads or heads_o != heads or d_k != d or d_v != d or d_o != d:
+        raise ValueError("q and out must have one shape, k and v too, with q's tokens and head size")
+    sp, seqs = None, 1
+    if starts is not None:
+        if len(starts.shape) != 1 or starts.shape[0] < 1:
+            raise ValueError("starts must be a vector of one value per sequence and one more")
+        sp, _ = _whole_numbers(starts, dev, "starts")
+        seqs = starts.shape[0] - 1
+    rc = lib.gptq_attention(qp, qt, qh, kp, kt, kh, vp, vt, vh, op, ot, oh, _fp8_dtype(q), n, heads, kv_heads, d, sp,
+                            seqs, 1 if causal else 0, scale, _fp8_stream(dev, stream))
+    if rc:
+        _check("gptq_attention", rc)
+
+
+def cache_store(k, v, slots, keys, values, stream=None) -> None:
+    """``keys[page, :, row] = k[t]``, ``values[page, :, row] = v[t]`` for
+    ``slots[t] = page * page_size + row``."""
+    lib = _lib or load()
+    dev, kind = _fp8_device(k), k.dtype
+    kp, kt, kh, n, kv_heads, d = _heads_of(k, dev, kind, "k")
+    vp, vt, vh, n_v, heads_v, d_v = _heads_of(v, dev, kind, "v")
+    cp, c0, c1, c2 = _pages_of(keys, dev, kind, "keys")
+    wp, w0, w1, w2 = _pages_of(values, dev, kind, "values")
+    pages, cached, page_size, d_c = keys.shape
+    if n_v != n or heads_v != kv_heads or d_v != d or values.shape != keys.shape or cached != kv_heads or d_c != d:
+        raise ValueError("k and v must have one shape, keys and values too, with the heads and head size of k")
+    if slots.shape != k.shape[:1]:
+        raise ValueError("slots must be a vector of one value per token")
+    sp, _ = _whole_numbers(slots, dev, "slots")
+    rc = lib.gptq_cache_store(kp, kt, kh, vp, vt, vh, _fp8_dtype(k), n, kv_heads, d, sp, cp, c0, c1, c2, wp, w0, w1, w2,
+                              pages, page_size, _fp8_stream(dev, stream))
+    if rc:
+        _check("gptq_cache_store", rc)
+
+
+def cached_attention_workspace(n_seqs: int, heads: int, kv_heads: int, d: int, max_pages: int, page_size: int) -> int:
+    return load().gptq_cached_attention_workspace(n_seqs, heads, kv_heads, d, max_pages, page_size)
+
+
+def cached_attention(q, keys, values, table, lengths, out, scale: float, workspace=None, stream=None) -> None:
+    """Attention of one new token a sequence: ``q``, ``out`` [n_seqs, heads, d],
+    ``table`` [n_seqs, max_pages] and ``lengths`` [n_seqs] int32."""
+    lib = _lib or load()
+    dev, kind = _fp8_device(q), q.dtype
+    qp, qt, qh, n, heads, d = _heads_of(q, dev, kind, "q")
+    op, ot, oh, n_o, heads_o, d_o = _heads_of(out, dev, kind, "out")
+    cp, c0, c1, c2 = _pages_of(keys, dev, kind, "keys")
+    wp, w0, w1, w2 = _pages_of(values, dev, kind, "values")
+    pages, kv_heads, page_size, d_c = keys.shape
+    if n_o != n or heads_o != heads or d_o != d or values.shape != keys.shape or d_c != d:
+        raise ValueError("q and out must have one shape, keys and values too, with one head size")
+    if len(table.shape) != 2 or table.shape[0] != n or lengths.shape != q.shape[:1]:
+        raise ValueError("table must have a row, and lengths a value, per sequence")
+    tp, ldt = _whole_numbers(table, dev, "table")
+    lp, _ = _whole_numbers(lengths, dev, "lengths")
+    room = 0
+    if workspace is not None:
+        if workspace.get_device() != dev:
+            raise ValueError("workspace on another device")
+        room = workspace.numel() * workspace.element_size()
+    rc = lib.gptq_cached_attention(qp, qt, qh, cp, c0, c1, c2, wp, w0, w1, w2, pages, page_size, tp, ldt,
+                                   table.shape[1], lp, n, heads, kv_heads, d, op, ot, oh, _fp8_dtype(q), scale,
+                                   _ptr(workspace), room, _fp8_stream(dev, stream))
+    if rc:
+        _check("gptq_cached_attention", rc)
 
 
 # ---------------------------------------------------------------------------

@@ -23,6 +23,7 @@ const char* const kNames[K_COUNT] = {
     "pack_codes",  "dequantize",  "output_error", "obq_hinv", "obq_rows", "propagate",
     "hinv32_load_reversed", "chol32_step", "hinv32_store_u",
     "fp8_weight", "fp8_rows", "fp8_columns", "fp8_rms_norm", "fp8_matmul", "fp8_gated",
+    "packed_matmul", "attention", "cache_store", "cached_attention", "cached_join",
 };
 // The timing state is process-wide; the mutex makes concurrent entry-point
 // calls from several host threads safe, though the events then interleave.
@@ -463,6 +464,134 @@ const char* gptq_fp8_gated_kernel(int64_t d_ff, int64_t d_in, int64_t n, int com
     if (d_ff <= 0 || d_in < 0 || n <= 0 || d_ff > kF8MaxRows || n > kF8MaxRows || d_in > kF8MaxLd) return nullptr;
     const int64_t cus = compute_units > 0 ? compute_units : device_cu_count();
     return cus > 0 ? f8_gated_kernel_name(d_ff, d_in, n, cus) : nullptr;
+}
+
+namespace {
+constexpr int64_t kPackedMaxCols = (int64_t)1 << 21;  // 256 rows of X stay within 2^30 bytes
+constexpr int64_t kPackedMaxRows = (int64_t)1 << 24;
+}  // namespace
+
+int gptq_packed_matmul(const uint32_t* packed, int bits, int64_t d_out, int64_t d_in, const float* scales,
+                       const int32_t* zeros, int64_t group_size, const void* X, int x_dtype, int64_t n, int64_t ldx,
+                       const void* bias, const void* residual, int64_t ldr, void* Y, int y_dtype, int64_t ldy,
+                       int activation, void* stream) {
+    if (d_out < 0 || d_in < 0 || n < 0 || bits < 2 || bits > 8 || group_size < 0) return GPTQ_EINVAL;
+    if (!f8_dtype(x_dtype) || !f8_dtype(y_dtype) || activation < 0 || activation > 3) return GPTQ_EINVAL;
+    if (group_size > 0 && d_in % group_size != 0) return GPTQ_EINVAL;
+    if (ldx < d_in || ldy < d_out || (residual && ldr < d_out)) return GPTQ_EINVAL;
+    if (d_out == 0 || n == 0) return GPTQ_OK;
+    if (!Y || (d_in > 0 && (!packed || !scales || !zeros || !X))) return GPTQ_EINVAL;
+    if (x_dtype == GPTQ_F32 || (y_dtype != x_dtype && y_dtype != GPTQ_F32) || group_size % 16 != 0)
+        return GPTQ_EUNSUPPORTED;
+    if (d_in > kPackedMaxCols || ldx > kPackedMaxCols || d_out > kPackedMaxRows || n > kPackedMaxRows)
+        return GPTQ_EUNSUPPORTED;
+    if (((d_out + 255) / 256) * ((n + 255) / 256) > kF8MaxTiles) return GPTQ_EUNSUPPORTED;
+    const PackedProduct c = {packed, scales, zeros, X, bias, residual, Y, d_out, d_in, group_size, n, ldx, ldr, ldy,
+                             bits, activation};
+    return hip_status(launch_packed_matmul(c, x_dtype, y_dtype, as_stream(stream)));
+}
+
+namespace {
+constexpr int64_t kMaxHeadDim = 128, kMaxHeads = (int64_t)1 << 16, kMaxTokenStride = (int64_t)1 << 22;
+// rows that the 16-byte loads of the attention and the cache can take
+inline bool rows16(const void* p, int64_t a, int64_t b, int64_t c = 0) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && a % 8 == 0 && b % 8 == 0 && c % 8 == 0;
+}
+inline bool bad_scale(double scale) { return !(scale > 0.0) || !isfinite((float)scale) || !((float)scale > 0.0f); }
+inline bool bad_heads(int64_t heads, int64_t kv_heads, int64_t d) {
+    return heads < 0 || kv_heads < 0 || d < 0 || (kv_heads == 0 ? heads != 0 : heads % kv_heads != 0);
+}
+inline bool odd_heads(int64_t heads, int64_t d) { return d > kMaxHeadDim || d % 8 != 0 || heads > kMaxHeads; }
+inline bool short_cache(int64_t d, int64_t key_page, int64_t key_head, int64_t key_row, int64_t value_page,
+                        int64_t value_head, int64_t value_row) {
+    return key_page < d || key_head < d || key_row < d || value_page < d || value_head < d || value_row < d;
+}
+inline bool odd_cache(const CacheView& c) {
+    return !rows16(c.keys, c.ldk[0], c.ldk[1], c.ldk[2]) || !rows16(c.values, c.ldv[0], c.ldv[1], c.ldv[2]) ||
+           c.ldk[2] > kMaxTokenStride || c.ldv[2] > kMaxTokenStride || c.pages > INT32_MAX ||
+           c.page_size > INT32_MAX || c.pages * c.page_size > INT32_MAX;
+}
+constexpr int64_t kMaxPieces = (int64_t)1 << 22;
+}  // namespace
+
+int gptq_attention(const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token, int64_t k_head,
+                   const void* v, int64_t v_token, int64_t v_head, void* out, int64_t out_token, int64_t out_head,
+                   int dtype, int64_t n, int64_t heads, int64_t kv_heads, int64_t d, const int32_t* starts,
+                   int64_t n_seqs, int causal, double scale, void* stream) {
+    if (n < 0 || n_seqs < 0 || bad_heads(heads, kv_heads, d) || !f8_dtype(dtype) || (causal != 0 && causal != 1))
+        return GPTQ_EINVAL;
+    if (q_token < d || q_head < d || k_token < d || k_head < d || v_token < d || v_head < d || out_token < d ||
+        out_head < d || bad_scale(scale) || (!starts && n_seqs != 1))
+        return GPTQ_EINVAL;
+    if (n == 0 || n_seqs == 0 || heads == 0 || d == 0) return GPTQ_OK;
+    if (!q || !k || !v || !out) return GPTQ_EINVAL;
+    if (dtype == GPTQ_F32 || odd_heads(heads, d) || n > kPackedMaxRows || n_seqs > kPackedMaxRows)
+        return GPTQ_EUNSUPPORTED;
+    if (!rows16(q, q_token, q_head) || !rows16(k, k_token, k_head) || !rows16(v, v_token, v_head) ||
+        !rows16(out, out_token, out_head))
+        return GPTQ_EUNSUPPORTED;
+    if (q_token > kMaxTokenStride || k_token > kMaxTokenStride || v_token > kMaxTokenStride ||
+        out_token > kMaxTokenStride)
+        return GPTQ_EUNSUPPORTED;
+    if ((n / 2 + n_seqs) * heads > kMaxPieces * 16) return GPTQ_EUNSUPPORTED;
+    const AttentionCall c = {q, k, v, out, {q_token, q_head}, {k_token, k_head}, {v_token, v_head},
+                             {out_token, out_head}, n, heads, kv_heads, d, n_seqs, starts, causal, (float)scale};
+    return hip_status(launch_attention(c, dtype, as_stream(stream)));
+}
+
+int gptq_cache_store(const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token, int64_t v_head,
+                     int dtype, int64_t n, int64_t kv_heads, int64_t d, const int32_t* slots, void* keys,
+                     int64_t key_page, int64_t key_head, int64_t key_row, void* values, int64_t value_page,
+                     int64_t value_head, int64_t value_row, int64_t pages, int64_t page_size, void* stream) {
+    if (n < 0 || kv_heads < 0 || d < 0 || pages < 0 || page_size < 1 || !f8_dtype(dtype)) return GPTQ_EINVAL;
+    if (k_token < d || k_head < d || v_token < d || v_head < d ||
+        short_cache(d, key_page, key_head, key_row, value_page, value_head, value_row))
+        return GPTQ_EINVAL;
+    if (n == 0 || kv_heads == 0 || d == 0 || pages == 0) return GPTQ_OK;
+    if (!k || !v || !slots || !keys || !values) return GPTQ_EINVAL;
+    const CacheView cache = {keys, values, {key_page, key_head, key_row}, {value_page, value_head, value_row}, pages,
+                             page_size};
+    if (dtype == GPTQ_F32 || odd_heads(kv_heads, d) || odd_cache(cache)) return GPTQ_EUNSUPPORTED;
+    if (!rows16(k, k_token, k_head) || !rows16(v, v_token, v_head)) return GPTQ_EUNSUPPORTED;
+    if (n > ((int64_t)1 << 27) || n * kv_heads > ((int64_t)1 << 27)) return GPTQ_EUNSUPPORTED;
+    const CacheStoreCall c = {k, v, {k_token, k_head}, {v_token, v_head}, n, kv_heads, d, slots, cache};
+    return hip_status(launch_cache_store(c, as_stream(stream)));
+}
+
+size_t gptq_cached_attention_workspace(int64_t n_seqs, int64_t heads, int64_t kv_heads, int64_t d, int64_t max_pages,
+                                       int64_t page_size) {
+    if (n_seqs <= 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0 || d <= 0 || odd_heads(heads, d)) return 0;
+    if (max_pages < 0 || page_size < 1) return 0;
+    return cached_attention_workspace_bytes(n_seqs, heads, kv_heads, d, max_pages, page_size);
+}
+
+int gptq_cached_attention(const void* q, int64_t q_seq, int64_t q_head, const void* keys, int64_t key_page,
+                          int64_t key_head, int64_t key_row, const void* values, int64_t value_page,
+                          int64_t value_head, int64_t value_row, int64_t pages, int64_t page_size,
+                          const int32_t* table, int64_t ldt, int64_t max_pages, const int32_t* lengths,
+                          int64_t n_seqs, int64_t heads, int64_t kv_heads, int64_t d, void* out, int64_t out_seq,
+                          int64_t out_head, int dtype, double scale, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+    if (n_seqs < 0 || bad_heads(heads, kv_heads, d) || pages < 0 || page_size < 1 || max_pages < 0 ||
+        max_pages > ldt || !f8_dtype(dtype) || bad_scale(scale))
+        return GPTQ_EINVAL;
+    if (q_seq < d || q_head < d || out_seq < d || out_head < d ||
+        short_cache(d, key_page, key_head, key_row, value_page, value_head, value_row))
+        return GPTQ_EINVAL;
+    if (n_seqs == 0 || heads == 0 || d == 0) return GPTQ_OK;
+    if (!q || !out || !lengths || (max_pages > 0 && !table) || (pages > 0 && (!keys || !values))) return GPTQ_EINVAL;
+    const CacheView cache = {const_cast<void*>(keys), const_cast<void*>(values), {key_page, key_head, key_row},
+                             {value_page, value_head, value_row}, pages, page_size};
+    if (dtype == GPTQ_F32 || odd_heads(heads, d) || odd_cache(cache) || n_seqs > ((int64_t)1 << 20) ||
+        max_pages > INT32_MAX || max_pages * page_size > INT32_MAX)
+        return GPTQ_EUNSUPPORTED;
+    if (!rows16(q, q_seq, q_head) || !rows16(out, out_seq, out_head)) return GPTQ_EUNSUPPORTED;
+    const size_t need = cached_attention_workspace_bytes(n_seqs, heads, kv_heads, d, max_pages, page_size);
+    if (need > 0 && (!workspace || workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256 != 0))
+        return GPTQ_EWORKSPACE;
+    const CachedAttentionCall c = {q, out, {q_seq, q_head}, {out_seq, out_head}, table, lengths, ldt, max_pages,
+                                   n_seqs, heads, kv_heads, d, cache, (float)scale, workspace};
+    return hip_status(launch_cached_attention(c, dtype, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -34,6 +34,11 @@ enum KernelId {
     K_F8_NORM,
     K_F8_MATMUL,
     K_F8_GATED,
+    K_PACKED_MATMUL,
+    K_ATTENTION,
+    K_CACHE_STORE,
+    K_CACHED_ATTENTION,
+    K_CACHED_JOIN,
     K_COUNT
 };
 
@@ -154,5 +159,61 @@ const char* f8_gated_kernel_name(int64_t M, int64_t K, int64_t n, int64_t cus);
 size_t f8_gated_workspace_bytes(int64_t n, int64_t d_ff);
 hipError_t launch_f8_gated(const F8Product& c, uint8_t* q, int64_t ldq, float* scales, int64_t lds, void* ws,
                            hipStream_t s);
+
+// ---- products with packed few-bit weights -------------------------------------
+struct PackedProduct {
+    const uint32_t* packed;
+    const float* scales;
+    const int32_t* zeros;
+    const void *x, *bias, *residual;  // bias, residual: or null
+    void* y;
+    int64_t M, K, group, n, ldx, ldr, ldy;  // M: rows of the weights, group: 0 = one a row
+    int bits, activation;
+};
+hipError_t launch_packed_matmul(const PackedProduct& c, int x_dtype, int y_dtype, hipStream_t s);
+
+// ---- attention ------------------------------------------------------------------
+// Query heads that share a key head are rows of one tile, up to this many.
+constexpr int64_t kHeadRows = 16;
+// strides in elements: [.][0] per token, [.][1] per head
+struct AttentionCall {
+    const void *q, *k, *v;
+    void* out;
+    int64_t ldq[2], ldk[2], ldv[2], ldo[2];
+    int64_t n, heads, kv_heads, d, n_seqs;
+    const int32_t* starts;
+    int causal;
+    float scale;
+};
+hipError_t launch_attention(const AttentionCall& c, int dtype, hipStream_t s);
+
+// ---- paged cache ----------------------------------------------------------------
+// strides in elements, per page, head and row
+struct CacheView {
+    void *keys, *values;
+    int64_t ldk[3], ldv[3];
+    int64_t pages, page_size;
+};
+struct CacheStoreCall {
+    const void *k, *v;
+    int64_t ldk[2], ldv[2];
+    int64_t n, kv_heads, d;
+    const int32_t* slots;
+    CacheView cache;
+};
+hipError_t launch_cache_store(const CacheStoreCall& c, hipStream_t s);
+struct CachedAttentionCall {
+    const void* q;
+    void* out;
+    int64_t ldq[2], ldo[2];
+    const int32_t *table, *lengths;
+    int64_t ldt, max_pages, n_seqs, heads, kv_heads, d;
+    CacheView cache;
+    float scale;
+    void* ws;
+};
+size_t cached_attention_workspace_bytes(int64_t n_seqs, int64_t heads, int64_t kv_heads, int64_t d, int64_t max_pages,
+                                        int64_t page_size);
+hipError_t launch_cached_attention(const CachedAttentionCall& c, int dtype, hipStream_t s);
 
 }  // namespace gptq

@@ -216,6 +216,19 @@ def _empty(rows: int, cols: int, dtype, device, stream):
         return torch.empty(rows, cols, dtype=dtype, device=device)
 
 
+def _scratch(need: int, ws: Optional[Workspace], device, stream):
+    """``need`` bytes of ``ws``, or of the call's own; None for 0."""
+    if not need:
+        return None
+    import torch
+    if ws is None:
+        return _empty(1, need, torch.uint8, device, stream)
+    if stream is None:
+        return ws.get(need)
+    with torch.cuda.stream(stream):
+        return ws.get(need)
+
+
 def _fp8_out(rows: int, cols: int, lead: int, along: int, device, stream) -> Fp8:
     """An 8-bit matrix with scales ``[lead, along]``."""
     import torch
@@ -292,17 +305,7 @@ def fp8_gated(gate: Fp8, up: Fp8, x: Fp8, ws: Optional[Workspace] = None, out: O
     n, d_ff = x.data.shape[0], gate.data.shape[0]
     made = out is None
     out = _fp8_out(n, d_ff, (d_ff + 127) // 128, n, x.data.device, stream) if made else _fp8_cols(out, d_ff)
-    need = _lib.fp8_gated_workspace(n, d_ff)
-    buf = None
-    if need:
-        import torch
-        if ws is None:
-            buf = _empty(1, need, torch.uint8, x.data.device, stream)
-        elif stream is None:
-            buf = ws.get(need)
-        else:
-            with torch.cuda.stream(stream):
-                buf = ws.get(need)
+    buf = _scratch(_lib.fp8_gated_workspace(n, d_ff), ws, x.data.device, stream)
     _lib.fp8_gated(gate.data, gate.scales, up.data, up.scales, x.data, x.scales, gate.cols, out.data, out.scales, buf,
                    stream, made)
     return out
@@ -320,3 +323,102 @@ def propagate_fp8(w: Fp8, X, relu: bool = False, out=None, stream=None):
         import torch
         dtype = torch.float32 if X.dtype == torch.bfloat16 else X.dtype
     return fp8_matmul(w, x, dtype=dtype, relu=relu, channel_major=True, out=out, stream=stream)
+
+
+# ---------------------------------------------------------------------------
+# A block of quantized layers: products with packed weights, attention over
+# prompts, and the paged cache with the attention over it
+# ---------------------------------------------------------------------------
+@dataclasses.dataclass
+class Packed:
+    """A few-bit weight as it is stored: ``cols`` codes a row, packed, and the
+    grids of its groups (``group_size`` 0: one a row)."""
+    codes: "torch.Tensor"    # [d_out, words] int32
+    scales: "torch.Tensor"   # [d_out, n_groups] float32
+    zeros: "torch.Tensor"    # [d_out, n_groups] int32
+    bits: int
+    cols: int
+    group_size: int
+
+
+def packed(q: Quantized, bits: int, group_size: int, stream=None) -> Packed:
+    """A quantized layer in packed form (``gptq_pack_codes``)."""
+    return Packed(pack(q.codes, bits, stream=stream), q.scales, q.zeros, bits, q.codes.shape[1], group_size)
+
+
+def packed_matmul(w: Packed, x, bias=None, activation: Optional[str] = None, residual=None, dtype=None, out=None,
+                  stream=None):
+    """``act(x W^T + bias) + residual`` of packed weights and activations ``x
+    [n, d_in]`` in float16 or bfloat16 (``gptq_packed_matmul``): ``[n, d_out]``
+    in x's type, or float32 by ``dtype`` or ``out``.  ``activation``: None,
+    "relu", "silu" or "gelu".  ``residual`` may be ``out``."""
+    if activation not in _lib.ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}")
+    if out is None:
+        out = _empty(x.shape[0], w.codes.shape[0], dtype or x.dtype, x.device, stream)
+    elif dtype is not None and dtype != out.dtype:
+        raise ValueError(f"out is {out.dtype}, not {dtype}")
+    _lib.packed_matmul(w.codes, w.bits, w.cols, w.scales, w.zeros, w.group_size, x, out, bias, residual,
+                       _lib.ACTIVATIONS[activation], stream)
+    return out
+
+
+def _like(q, stream):
+    """Memory of q's shape and type, contiguous."""
+    import torch
+    if stream is None:
+        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+
+
+def attention(q, k, v, starts=None, causal: bool = True, scale: Optional[float] = None, out=None, stream=None):
+    """Attention over whole prompts (``gptq_attention``): ``q [n, heads, d]``,
+    ``k`` and ``v [n, kv_heads, d]``, float16 or bfloat16, views of a fused
+    projection among them.  ``starts`` (int32, one value per sequence and one
+    more) packs several sequences one behind the other; None: one sequence.
+    ``scale``: 1 / sqrt(d) by default."""
+    if out is None:
+        out = _like(q, stream)
+    _lib.attention(q, k, v, starts, out, causal, q.shape[-1] ** -0.5 if scale is None else scale, stream)
+    return out
+
+
+@dataclasses.dataclass
+class KVCache:
+    """Pages of keys and values, each ``[pages, kv_heads, page_size, d]``; a
+    token's slot is ``page * page_size + row``.  Which page belongs to which
+    sequence is the caller's to keep."""
+    keys: "torch.Tensor"
+    values: "torch.Tensor"
+
+
+def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, dtype=None, device="cuda") -> KVCache:
+    """An empty cache (float16 by default)."""
+    import torch
+    shape = (pages, kv_heads, page_size, head_dim)
+    return KVCache(torch.empty(shape, dtype=dtype or torch.float16, device=device),
+                   torch.empty(shape, dtype=dtype or torch.float16, device=device))
+
+
+def cache_store(cache: KVCache, k, v, slots, stream=None) -> None:
+    """Keys and values ``[n, kv_heads, d]`` of new tokens to their ``slots``
+    (int32; below 0: not stored) of a cache (``gptq_cache_store``)."""
+    _lib.cache_store(k, v, slots, cache.keys, cache.values, stream)
+
+
+def cached_attention(q, cache: KVCache, table, lengths, scale: Optional[float] = None, ws: Optional[Workspace] = None,
+                     out=None, stream=None):
+    """Attention of one new token of each sequence, ``q [n_seqs, heads, d]``,
+    over its pages (``gptq_cached_attention``): sequence b's token j is on page
+    ``table[b, j // page_size]``, and there are ``lengths[b]`` (both int32).
+    Scratch memory is that of ``ws``, or memory of the call's own."""
+    if out is None:
+        out = _like(q, stream)
+    n, heads, d = q.shape
+    _, kv_heads, page_size, _ = cache.keys.shape
+    need = _lib.cached_attention_workspace(n, heads, kv_heads, d, table.shape[1], page_size)
+    buf = _scratch(need, ws, q.device, stream)
+    _lib.cached_attention(q, cache.keys, cache.values, table, lengths, out, d ** -0.5 if scale is None else scale, buf,
+                          stream)
+    return out
