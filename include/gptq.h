@@ -644,7 +644,8 @@ int gptq_attention(const void* q, int64_t q_token, int64_t q_head, const void* k
  * Errors: GPTQ_EINVAL (negative size, page_size below 1, a stride below
  * head_dim, unknown dtype, null pointer), GPTQ_EUNSUPPORTED (GPTQ_F32, head_dim
  * above 128 or not a multiple of 8, pointers or strides not 16-byte aligned,
- * pages * page_size of 2^31 or more, n_tokens * kv_heads above 2^27).
+ * pages * page_size or a page stride of 2^31 or more, a row stride above 2^22,
+ * n_tokens * kv_heads above 2^27).
  */
 int gptq_cache_store(const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token, int64_t v_head,
                      int dtype, int64_t n_tokens, int64_t kv_heads, int64_t head_dim, const int32_t* slots, void* keys,
@@ -670,8 +671,8 @@ int gptq_cache_store(const void* k, int64_t k_token, int64_t k_head, const void*
  *   workspace device memory of at least gptq_cached_attention_workspace() bytes,
  *             256-byte aligned; clobbered, needs no clearing.
  * Errors: as gptq_attention and gptq_cache_store (max_pages negative or above
- * ldt: GPTQ_EINVAL; max_pages * page_size of 2^31 or more, n_seqs above 2^20:
- * GPTQ_EUNSUPPORTED), and GPTQ_EWORKSPACE.
+ * ldt: GPTQ_EINVAL; max_pages * page_size of 2^31 or more, n_seqs above 2^20,
+ * n_seqs * heads of 2^24 or more: GPTQ_EUNSUPPORTED), and GPTQ_EWORKSPACE.
  */
 size_t gptq_cached_attention_workspace(int64_t n_seqs, int64_t heads, int64_t kv_heads, int64_t head_dim,
                                        int64_t max_pages, int64_t page_size);

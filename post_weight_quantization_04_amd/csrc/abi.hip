@@ -508,10 +508,11 @@ inline bool short_cache(int64_t d, int64_t key_page, int64_t key_head, int64_t k
 }
 inline bool odd_cache(const CacheView& c) {
     return !rows16(c.keys, c.ldk[0], c.ldk[1], c.ldk[2]) || !rows16(c.values, c.ldv[0], c.ldv[1], c.ldv[2]) ||
-           c.ldk[2] > kMaxTokenStride || c.ldv[2] > kMaxTokenStride || c.pages > INT32_MAX ||
+           c.ldk[0] > INT32_MAX || c.ldv[0] > INT32_MAX || c.ldk[2] > kMaxTokenStride || c.ldv[2] > kMaxTokenStride || c.pages > INT32_MAX ||
            c.page_size > INT32_MAX || c.pages * c.page_size > INT32_MAX;
 }
 constexpr int64_t kMaxPieces = (int64_t)1 << 22;
+constexpr int64_t kMaxUnits = (int64_t)1 << 24;  // workgroups of 256 threads: below 2^32 threads
 }  // namespace
 
 int gptq_attention(const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token, int64_t k_head,
@@ -583,7 +584,7 @@ int gptq_cached_attention(const void* q, int64_t q_seq, int64_t q_head, const vo
     const CacheView cache = {const_cast<void*>(keys), const_cast<void*>(values), {key_page, key_head, key_row},
                              {value_page, value_head, value_row}, pages, page_size};
     if (dtype == GPTQ_F32 || odd_heads(heads, d) || odd_cache(cache) || n_seqs > ((int64_t)1 << 20) ||
-        max_pages > INT32_MAX || max_pages * page_size > INT32_MAX)
+        n_seqs * heads >= kMaxUnits || max_pages > INT32_MAX || max_pages * page_size > INT32_MAX)
         return GPTQ_EUNSUPPORTED;
     if (!rows16(q, q_seq, q_head) || !rows16(out, out_seq, out_head)) return GPTQ_EUNSUPPORTED;
     const size_t need = cached_attention_workspace_bytes(n_seqs, heads, kv_heads, d, max_pages, page_size);

@@ -1,0 +1,67 @@
+// Shared device helpers of the attention kernels: MFMA on the two 16-bit types,
+// transposed reads from LDS, the online softmax.
+#pragma once
+
+#include "fp8_common.hpp"
+
+namespace gptq {
+
+typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short short4v __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896f;
+constexpr float kLowest = -__FLT_MAX__;  // a row's maximum before its first key
+
+// Vector types and MFMA of the two input types.  Operands as in common.hpp;
+// 16x16x16: A[i][k] from lane i + 16 kg with k = 4 kg .. 4 kg + 3.
+template <typename T>
+struct Mat;
+template <>
+struct Mat<half_t> {
+    typedef half8 v8;
+    typedef half4 v4;
+    static __device__ __forceinline__ float4v mfma16(v8 a, v8 b, float4v c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float4v mfma16h(v4 a, v4 b, float4v c) {
+        return __builtin_amdgcn_mfma_f32_16x16x16f16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float16v mfma32(v8 a, v8 b, float16v c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Mat<bf16_t> {
+    typedef bf16x8 v8;
+    typedef bf16x4 v4;
+    static __device__ __forceinline__ float4v mfma16(v8 a, v8 b, float4v c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float4v mfma16h(v4 a, v4 b, float4v c) {
+        return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(short4v, a), __builtin_bit_cast(short4v, b),
+                                                         c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float16v mfma32(v8 a, v8 b, float16v c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+
+// Four rows by sixteen columns of 16-bit values, turned: lane i of sixteen points
+// at columns 4 (i % 4) .. of row i / 4 and receives column i of the four rows.
+typedef __attribute__((address_space(3))) short4v lds_short4;
+template <typename T>
+__device__ __forceinline__ typename Mat<T>::v4 read_turned(const uint8_t* p) {
+    return __builtin_bit_cast(typename Mat<T>::v4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)p));
+}
+
+// exp2 of the hardware (one unit in the last place, results below 2^-126 are
+// zero: such weights are below half a unit of any sum they join).
+__device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// -m * c for the exponent fma(s, c, .), kept finite so that a masked score of
+// -infinity stays one.
+__device__ __forceinline__ float exponent_offset(float m, float c) { return fminf(-m * c, __FLT_MAX__); }
+
+}  // namespace gptq

@@ -1,6 +1,9 @@
 // Paged cache of keys and values: the store of new tokens, and the attention of
-// one new token of each sequence over its pages.
-#include "fp8_common.hpp"
+// one new token of each sequence over its pages,
+//   y[b, h] = sum_{j < length[b]} p_j V[b, j, h'],  p = softmax over j of scale q[b, h] . K[b, j, h'].
+#include <algorithm>
+
+#include "attention_common.hpp"
 #include "kernels.hpp"
 
 namespace gptq {
@@ -23,40 +26,466 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheStoreCall c, int 
         *reinterpret_cast<const uint4v*>(static_cast<const uint16_t*>(c.v) + t * c.ldv[0] + h * c.ldv[1] + e);
 }
 
-__device__ __forceinline__ float wave_sum32(float v) {
+// ---------------------------------------------------------------------------
+// Attention over the cache.  A unit is a sequence's key head with up to sixteen
+// of the query heads that share it: they are the columns of S^T = K Q^T and of
+// O^T = V^T P^T, so a lane's scores, maximum and sum belong to one query row, and
+// P^T leaves the first product in the layout that the second takes.  A unit's
+// keys are cut into steps; a workgroup's waves take a tile of kKeys keys each of
+// a step, copy it to LDS of their own two tiles ahead (buffers of memory lie in
+// flight, which is what HBM wants) and work without barriers.  At the end of a
+// unit the waves' results are joined in LDS.
+//
+// Long sequences (kSplit): all steps of all units, in order, are shared equally
+// among the workgroups, whatever the lengths, so that a batch of unequal
+// sequences ends at one time.  A workgroup that computes a part of a unit leaves
+// (maximum, sum, O) in the workspace: slot 2 w for a part that begins inside the
+// unit, 2 w + 1 for one that begins with it.  cached_join_kernel adds the parts
+// in order.
+// ---------------------------------------------------------------------------
+struct CachedArgs {
+    CachedAttentionCall c;
+    int rows;          // query heads of a unit
+    int head_groups;   // units per key head
+    uint32_t page_mul, page_shift;  // division by the page size
+    float c2;          // scale log2 e
+    float* parts;
+};
+
+__device__ const uint32_t kZeroRow[64] = {};  // 256 bytes: what keys that are none are read from
+
+__device__ __forceinline__ uint32_t page_of(const CachedArgs& a, uint32_t pos) {
+    const uint32_t t = __umulhi(a.page_mul, pos);
+    return a.page_shift ? (t + ((pos - t) >> 1)) >> (a.page_shift - 1) : pos;
+}
+
+__device__ __forceinline__ uint32_t cached_length(const CachedArgs& a, int64_t b) {
+    const int64_t n = a.c.lengths[b];
+    return (uint32_t)min(max(n, (int64_t)0), a.c.max_pages * a.c.cache.page_size);
+}
+
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+    const int lane = threadIdx.x % kWave;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+    for (int o = 1; o < kWave; o *= 2) {
+        const int64_t u = __shfl_up(v, o, kWave);
+        v += lane >= o ? u : 0;
+    }
     return v;
 }
 
-// The plainest form: one wave a sequence and head, two values of the head a lane.
-template <typename T>
-__global__ __launch_bounds__(64) void cached_plain_kernel(CachedAttentionCall c) {
-    const int lane = threadIdx.x;
-    const int64_t b = blockIdx.x, h = blockIdx.y, hk = h / (c.heads / c.kv_heads);
-    const CacheView& cache = c.cache;
-    const int64_t count = min((int64_t)c.lengths[b], c.max_pages * cache.page_size);
-    const T* q = static_cast<const T*>(c.q) + b * c.ldq[0] + h * c.ldq[1];
-    float qv[2], acc[2] = {0.0f, 0.0f}, m = -__FLT_MAX__, l = 0.0f;
-    for (int e = 0; e < 2; ++e) qv[e] = lane + 64 * e < c.d ? to_f32(q[lane + 64 * e]) : 0.0f;
-    for (int64_t j = 0; j < count; ++j) {
-        const int64_t page = c.table[b * c.ldt + j / cache.page_size], r = j % cache.page_size;
-        if (page < 0 || page >= cache.pages) continue;
-        const T* k = static_cast<const T*>(cache.keys) + page * cache.ldk[0] + hk * cache.ldk[1] + r * cache.ldk[2];
-        const T* v = static_cast<const T*>(cache.values) + page * cache.ldv[0] + hk * cache.ldv[1] + r * cache.ldv[2];
-        float s = 0.0f;
-        for (int e = 0; e < 2; ++e)
-            if (lane + 64 * e < c.d) s = fmaf(qv[e], to_f32(k[lane + 64 * e]), s);
-        s = wave_sum32(s) * c.scale;
-        const float top = fmaxf(m, s), keep = __expf(m - top), p = __expf(s - top);
-        m = top;
-        l = l * keep + p;
-        for (int e = 0; e < 2; ++e)
-            acc[e] = acc[e] * keep + (lane + 64 * e < c.d ? p * to_f32(v[lane + 64 * e]) : 0.0f);
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// Steps of all sequences (of one unit each), and those before sequence `upto`.
+__device__ __forceinline__ void count_steps(const CachedArgs& a, uint32_t per, int64_t upto, int64_t& all, int64_t& before) {
+    const int lane = threadIdx.x % kWave;
+    int64_t sum = 0, part = 0;
+    for (int64_t b = lane; b < a.c.n_seqs; b += kWave) {
+        const int64_t steps = (cached_length(a, b) + (uint64_t)per - 1) / per;
+        sum += steps;
+        part += b < upto ? steps : 0;
     }
-    T* o = static_cast<T*>(c.out) + b * c.ldo[0] + h * c.ldo[1];
-    for (int e = 0; e < 2; ++e)
-        if (lane + 64 * e < c.d) o[lane + 64 * e] = (T)(l == 0.0f ? 0.0f : acc[e] / l);
+    all = uniform64(__shfl(wave_scan(sum), kWave - 1, kWave));
+    before = uniform64(__shfl(wave_scan(part), kWave - 1, kWave));
+}
+
+// Where chunk c (sixteen bytes) of row r lies in its row of LDS.  Keys are read
+// by rows: sixteen lanes, sixteen rows, one chunk.  Values are read turned: eight
+// rows of two chunks at a time.  Either way the sixteen chunks cover all banks.
+template <int kDp>
+__device__ __forceinline__ int key_place(int r, int c) {
+    return c ^ (kDp == 128 ? r % 16 : r / 2 % 8);
+}
+template <int kDp>
+__device__ __forceinline__ int value_place(int r, int c) {
+    return c ^ (kDp == 128 ? r % 8 * 2 : r / 2 % 4 * 2);
+}
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// Memory to LDS without registers in between, a wave's lanes one behind the
+// other from `lds` on.  The pages of a cache lie further apart than a buffer
+// load's 32-bit offsets reach, and the compiler takes the global form for one
+// that may read LDS: it would wait for all copies in flight at every LDS read.
+// As assembly (without outputs, so no register is pending) it leaves the waits
+// to the code that copies.  M0, which the compiler reserves, is used by nothing
+// else in these kernels.
+__device__ __forceinline__ void copy_row_piece(const void* p, const void* lds) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(p) : "memory");
+}
+__device__ __forceinline__ void copy_word(const void* p, const void* lds) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(p) : "memory");
+}
+
+template <typename T, int kDp, int kWaves, bool kSplit>
+__global__ __launch_bounds__(kWaves* kWave, 2) void cached_kernel(CachedArgs a) {
+    constexpr int kChunks = kDp / 8;                 // of a row
+    constexpr int kCopies = 4;                       // instructions for a tile of keys
+    constexpr int kRowsEach = kWave / kChunks;       // rows an instruction copies
+    constexpr int kKeys = kCopies * kRowsEach;       // of a tile
+    constexpr int kStep = kWaves * kKeys;
+    constexpr int kTile = 1024 * kCopies;            // bytes of a tile of keys or of values
+    __shared__ __align__(16) uint8_t lds0[kWaves * 2 * kTile];
+    __shared__ __align__(16) uint8_t lds1[kWaves * 2 * kTile];
+    __shared__ __align__(16) int32_t pages[2][kWaves][kWave];
+    __shared__ float tops[kWaves][16], sums[kWaves][16];
+    typedef typename Mat<T>::v8 v8;
+    typedef typename Mat<T>::v4 v4;
+
+    const CachedAttentionCall& c = a.c;
+    const int tid = threadIdx.x, lane = tid % kWave, w = wave_id(), l16 = lane % 16, kg = lane / 16;
+    const int64_t units = c.kv_heads * a.head_groups;  // of a sequence
+    const int group = (int)(c.heads / c.kv_heads);
+
+    int64_t b, unit, step, left;  // the first unit, the step in it, and how many steps are this workgroup's
+    if (kSplit) {
+        int64_t all, none;
+        count_steps(a, kStep, 0, all, none);
+        all *= units;
+        const int64_t workers = min((int64_t)gridDim.x, all);  // none without a step
+        if (blockIdx.x >= workers) return;
+        const int64_t from = (int64_t)blockIdx.x * all / workers, to = ((int64_t)blockIdx.x + 1) * all / workers;
+        left = to - from;
+        // the sequence that holds step `from`
+        int64_t before = 0;
+        b = 0;
+        for (;; b += kWave) {
+            const int64_t mine = b + lane < c.n_seqs ? (cached_length(a, b + lane) + (uint64_t)kStep - 1) / kStep : 0;
+            const int64_t sum = wave_scan(mine);
+            const uint64_t past = __ballot((before + sum) * units > from);
+            if (past) {
+                const int at = __builtin_ctzll(past);
+                before += uniform64(__shfl(sum - mine, at, kWave));
+                b += at;
+                break;
+            }
+            before += uniform64(__shfl(sum, kWave - 1, kWave));
+        }
+        const int64_t steps = (cached_length(a, b) + (uint64_t)kStep - 1) / kStep;
+        unit = (from - before * units) / steps;
+        step = (from - before * units) % steps;
+    } else {
+        b = blockIdx.x / units;
+        unit = blockIdx.x % units;
+        step = 0;
+        left = 1;
+    }
+
+    const int chunk = lane % kChunks;
+    const uint8_t* zero = reinterpret_cast<const uint8_t*>(kZeroRow) + 16 * chunk;
+    for (; left > 0; ++unit) {
+        if (kSplit && unit == units) {
+            unit = 0;
+            do ++b;
+            while (cached_length(a, b) == 0);
+        }
+        const uint32_t length = __builtin_amdgcn_readfirstlane(cached_length(a, b));
+        const int64_t steps = ((uint64_t)length + kStep - 1) / kStep;
+        const int64_t last = kSplit ? min(steps, step + left) : steps;
+        const int64_t hk = unit / a.head_groups;
+        const int h0 = (int)(hk * group + unit % a.head_groups * 16);
+        const int rows = min(a.rows, (int)((hk + 1) * group) - h0);
+        const bool whole = step == 0 && last == steps;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (step == 0);
+
+        v8 qf[kDp / 32];
+#pragma unroll
+        for (int s = 0; s < kDp / 32; ++s) {
+            qf[s] = (v8){};
+            const int e = 32 * s + 8 * kg;
+            if (l16 < rows && e < c.d)
+                qf[s] = *reinterpret_cast<const v8*>(static_cast<const T*>(c.q) + b * c.ldq[0] + (h0 + l16) * c.ldq[1] + e);
+        }
+        const T* keys = static_cast<const T*>(c.cache.keys) + hk * c.cache.ldk[1];
+        const T* values = static_cast<const T*>(c.cache.values) + hk * c.cache.ldv[1];
+        const int32_t* table = c.table + b * c.ldt;
+
+        // The pages of the tile at k0, a word a key (lanes past the tile repeat it).
+        auto copy_pages = [&](int32_t* to, uint32_t k0) {
+            const uint32_t pos = k0 + (uint32_t)(lane % kKeys);
+            copy_word(table + (pos < length ? page_of(a, pos) : 0u), to);
+        };
+        // The tile itself; true if a key of it is on a page outside the cache.
+        auto copy = [&](uint8_t* st, const int32_t* pages, uint32_t k0) {
+            bool odd = false;
+            uint32_t pg[kCopies];
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) pg[i] = (uint32_t)pages[kRowsEach * i + lane / kChunks];
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int r = kRowsEach * i + lane / kChunks;
+                const uint32_t pos = k0 + (uint32_t)r, page = pg[i];
+                const bool in = page < (uint32_t)c.cache.pages, ok = (pos < length) & in;
+                odd |= (pos < length) & !in;
+                const uint32_t row = pos - page_of(a, pos) * (uint32_t)c.cache.page_size;
+                const int ck = 8 * key_place<kDp>(r, chunk), cv = 8 * value_place<kDp>(r, chunk);
+                const uint8_t* kp = reinterpret_cast<const uint8_t*>(keys + ck) +
+                                    2 * ((uint64_t)page * (uint32_t)c.cache.ldk[0] + (uint64_t)row * (uint32_t)c.cache.ldk[2]);
+                const uint8_t* vp = reinterpret_cast<const uint8_t*>(values + cv) +
+                                    2 * ((uint64_t)page * (uint32_t)c.cache.ldv[0] + (uint64_t)row * (uint32_t)c.cache.ldv[2]);
+                asm("" : "+v"(kp), "+v"(vp));  // selected from, not branched around
+                kp = (ok & (ck < c.d)) ? kp : zero;
+                vp = (ok & (cv < c.d)) ? vp : zero;
+                copy_row_piece(kp, st + (w * 2 * kTile + 1024 * i));
+                copy_row_piece(vp, st + (w * 2 * kTile + kTile + 1024 * i));
+            }
+            return __any(odd);
+        };
+
+        float4v acc[kDp / 16];
+#pragma unroll
+        for (int i = 0; i < kDp / 16; ++i) acc[i] = (float4v){};
+        float m = kLowest, l = 0.0f;
+
+        auto compute = [&](const uint8_t* st, uint32_t k0, bool odd) {
+            constexpr int kTiles = kKeys / 16;
+            float4v s[kTiles];
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                s[t] = (float4v){};
+#pragma unroll
+                for (int e = 0; e < kDp / 32; ++e) {
+                    const int r = 16 * t + l16;
+                    const v8 kf = *reinterpret_cast<const v8*>(st + (w * 2 * kTile + r * 2 * kDp + 16 * key_place<kDp>(r, 4 * e + kg)));
+                    s[t] = Mat<T>::mfma16(kf, qf[e], s[t]);
+                }
+            }
+            if (k0 + kKeys > length || odd) {
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const uint32_t pos = k0 + (uint32_t)(16 * t + 4 * kg + v);
+                        bool ok = pos < length;
+                        if (ok && odd) ok = (uint32_t)table[page_of(a, pos)] < (uint32_t)c.cache.pages;
+                        s[t][v] = ok ? s[t][v] : -__builtin_inff();
+                    }
+            }
+            float top = m;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) top = fmaxf(top, s[t][v]);
+            top = fmaxf(top, __shfl_xor(top, 16, kWave));
+            top = fmaxf(top, __shfl_xor(top, 32, kWave));
+            const float off = exponent_offset(top, a.c2);
+            const float keep = exp2_fast((m - top) * a.c2);
+            m = top;
+            l *= keep;
+#pragma unroll
+            for (int i = 0; i < kDp / 16; ++i) acc[i] *= keep;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                v4 p;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const float e = exp2_fast(fmaf(s[t][v], a.c2, off));
+                    l += e;
+                    p[v] = (T)e;
+                }
+                const int r = 16 * t + 4 * kg + l16 / 4;
+#pragma unroll
+                for (int i = 0; i < kDp / 16; ++i) {
+                    const v4 vf = read_turned<T>(st + (w * 2 * kTile + kTile + r * 2 * kDp +
+                                                       16 * value_place<kDp>(r, 2 * i + l16 % 4 / 2) + 8 * (l16 % 2)));
+                    acc[i] = Mat<T>::mfma16h(vf, p, acc[i]);
+                }
+            }
+        };
+
+        if (step < last) {
+            constexpr int kLoads = 2 * kCopies;
+            const int count = (int)(last - step);
+            uint32_t at = (uint32_t)step * kStep + (uint32_t)(w * kKeys);  // this wave's tile of the step in work
+            copy_pages(pages[0][w], at);
+            copy_pages(pages[1][w], at + kStep);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            bool odd0 = copy(lds0, pages[0][w], at);
+            copy_pages(pages[0][w], at + 2 * kStep);
+            bool odd1 = copy(lds1, pages[1][w], at + kStep);
+            // One tile from `st`, whose memory then takes the tile two steps on
+            // (past the last step: positions past the length, or steps of
+            // another workgroup, copied and never used).  In flight at its
+            // start, in order: this tile, the next but one's pages, the next tile.
+            auto go = [&](uint8_t* st, bool& odd, int32_t* mine, int32_t* next) {
+                copy_pages(next, at + 3 * kStep);
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads + 1) : "memory");
+                compute(st, at, odd);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                odd = copy(st, mine, at + 2 * kStep);
+                at += kStep;
+            };
+            int i = 0;
+            for (; i + 2 <= count; i += 2) {
+                go(lds0, odd0, pages[0][w], pages[1][w]);
+                go(lds1, odd1, pages[1][w], pages[0][w]);
+            }
+            if (i < count) go(lds0, odd0, pages[0][w], pages[1][w]);
+        }
+
+        // the waves' results
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __syncthreads();
+        l += __shfl_xor(l, 16, kWave);
+        l += __shfl_xor(l, 32, kWave);
+        float* o = reinterpret_cast<float*>(lds0);  // [kWaves][16][kDp], sixteen bytes at c ^ row
+        if (kg == 0) {
+            tops[w][l16] = m;
+            sums[w][l16] = l;
+        }
+#pragma unroll
+        for (int i = 0; i < kDp / 16; ++i)
+            *reinterpret_cast<float4v*>(o + ((w * 16 + l16) * kDp + 4 * ((4 * i + kg) ^ l16))) = acc[i];
+        __syncthreads();
+        for (int id = tid; id < rows * kChunks; id += kWaves * kWave) {
+            const int r = id / kChunks, e = id % kChunks * 8;
+            float top = tops[0][r];
+#pragma unroll
+            for (int i = 1; i < kWaves; ++i) top = fmaxf(top, tops[i][r]);
+            float sum = 0.0f, y[8] = {};
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) {
+                const float f = exp2_fast((tops[i][r] - top) * a.c2);
+                sum = fmaf(sums[i][r], f, sum);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float4v v = *reinterpret_cast<const float4v*>(o + ((i * 16 + r) * kDp + 4 * ((e / 4 + j) ^ r)));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[4 * j + k] = fmaf(v[k], f, y[4 * j + k]);
+                }
+            }
+            if (!kSplit || whole) {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                if (e < c.d) {
+                    v8 out;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) out[k] = (T)(y[k] * inv);
+                    *reinterpret_cast<v8*>(static_cast<T*>(c.out) + b * c.ldo[0] + (h0 + r) * c.ldo[1] + e) = out;
+                }
+            } else {
+                float* part = a.parts + slot * (a.rows * (kDp + 2));
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    *reinterpret_cast<float4v*>(part + (r * kDp + e + 4 * j)) = (float4v){y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]};
+                if (e == 0) {
+                    part[a.rows * kDp + r] = top;
+                    part[a.rows * (kDp + 1) + r] = sum;
+                }
+            }
+        }
+        __syncthreads();
+        left -= kSplit ? last - step : 1;
+        step = 0;
+    }
+}
+
+// Adds the parts of a unit that several workgroups computed; zeros for a sequence
+// without tokens.  One workgroup a unit; the parts' factors go through LDS, 64
+// parts at a time.
+template <typename T, int kDp>
+__global__ __launch_bounds__(256) void cached_join_kernel(CachedArgs a, uint32_t per_step, int64_t workers) {
+    typedef typename Mat<T>::v8 v8;
+    constexpr int kChunks = kDp / 8, kMany = 64;
+    __shared__ float tops[kMany][16], sums[kMany][16];
+    const CachedAttentionCall& c = a.c;
+    const int64_t units = c.kv_heads * a.head_groups, b = blockIdx.x / units, unit = blockIdx.x % units;
+    const int group = (int)(c.heads / c.kv_heads);
+    const int64_t hk = unit / a.head_groups;
+    const int h0 = (int)(hk * group + unit % a.head_groups * 16);
+    const int rows = min(a.rows, (int)((hk + 1) * group) - h0);
+    int64_t all, before;
+    count_steps(a, per_step, b, all, before);
+    all *= units;
+    workers = min(workers, all);
+    const int64_t steps = (cached_length(a, b) + (uint64_t)per_step - 1) / per_step;
+    int64_t first = 0, last = -1;
+    if (steps > 0) {
+        const int64_t from = before * units + unit * steps;
+        auto worker = [&](int64_t at) { return ((at + 1) * workers - 1) / all; };
+        first = worker(from);
+        last = worker(from + steps - 1);
+        if (first == last) return;  // written already
+        // the first worker's part begins with the unit, the others' inside it
+    }
+    const int r = threadIdx.x / kChunks, e = threadIdx.x % kChunks * 8;  // kDp = 64: rows to 32, the upper half idle
+    float top = kLowest, sum = 0.0f, y[8] = {};
+    for (int64_t w0 = first; w0 <= last; w0 += kMany) {
+        const int many = (int)min((int64_t)kMany, last - w0 + 1);
+        auto part_of = [&](int i) { return a.parts + (2 * (w0 + i) + (w0 + i == first)) * (a.rows * (kDp + 2)); };
+        __syncthreads();
+        for (int id = threadIdx.x; id < many * 16; id += 256) {
+            const int i = id / 16, q = id % 16;
+            if (q < rows) {
+                tops[i][q] = part_of(i)[a.rows * kDp + q];
+                sums[i][q] = part_of(i)[a.rows * (kDp + 1) + q];
+            }
+        }
+        __syncthreads();
+        if (r < rows) {
+            float now = top;
+            for (int i = 0; i < many; ++i) now = fmaxf(now, tops[i][r]);
+            const float keep = exp2_fast((top - now) * a.c2);
+            sum *= keep;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] *= keep;
+            top = now;
+#pragma unroll 4
+            for (int i = 0; i < many; ++i) {
+                const float f = exp2_fast((tops[i][r] - now) * a.c2);
+                sum = fmaf(sums[i][r], f, sum);
+                const float* p = part_of(i) + (r * kDp + e);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float4v v = *reinterpret_cast<const float4v*>(p + 4 * j);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[4 * j + k] = fmaf(v[k], f, y[4 * j + k]);
+                }
+            }
+        }
+    }
+    if (r < rows && e < c.d) {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        v8 out;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) out[k] = (T)(y[k] * inv);
+        *reinterpret_cast<v8*>(static_cast<T*>(c.out) + b * c.ldo[0] + (h0 + r) * c.ldo[1] + e) = out;
+    }
+}
+
+constexpr int64_t kCachedWorkers = 1024;  // at most
+constexpr int kCachedWaves = 4;
+constexpr int64_t kCachedWhole = 1024;    // tokens up to which a unit is one workgroup's
+
+inline int padded_head(int64_t d) { return d <= 64 ? 64 : 128; }
+inline int64_t unit_rows(int64_t heads, int64_t kv_heads) { return std::min(heads / kv_heads, kHeadRows); }
+
+template <typename T, int kDp>
+hipError_t cached_go(CachedArgs a, hipStream_t s) {
+    const CachedAttentionCall& c = a.c;
+    const int64_t units = c.n_seqs * c.kv_heads * a.head_groups, most = c.max_pages * c.cache.page_size;
+    const dim3 block(kCachedWaves * kWave);
+    const TimedLaunch t(K_CACHED_ATTENTION, s);
+    if (most <= kCachedWhole) {
+        GPTQ_LAUNCH(t, (cached_kernel<T, kDp, kCachedWaves, false>), dim3((unsigned)units), block, 0, s, a);
+        return hipGetLastError();
+    }
+    const int cus = device_cu_count();
+    if (cus <= 0) return hipErrorInvalidDevice;
+    constexpr int kStep = kCachedWaves * 4 * kWave / (kDp / 8);
+    const int64_t workers = std::min({kCachedWorkers, (int64_t)2 * cus, units * ((most + kStep - 1) / kStep)});
+    GPTQ_LAUNCH(t, (cached_kernel<T, kDp, kCachedWaves, true>), dim3((unsigned)workers), block, 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const TimedLaunch j(K_CACHED_JOIN, s);
+    GPTQ_LAUNCH(j, (cached_join_kernel<T, kDp>), dim3((unsigned)units), dim3(256), 0, s, a, (uint32_t)kStep, workers);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -71,15 +500,23 @@ hipError_t launch_cache_store(const CacheStoreCall& c, hipStream_t s) {
 
 size_t cached_attention_workspace_bytes(int64_t n_seqs, int64_t heads, int64_t kv_heads, int64_t d, int64_t max_pages,
                                         int64_t page_size) {
-    return 0;
+    if (max_pages <= kCachedWhole && max_pages * std::min(page_size, kCachedWhole + 1) <= kCachedWhole) return 0;
+    return (size_t)(2 * kCachedWorkers * unit_rows(heads, kv_heads) * (padded_head(d) + 2)) * sizeof(float);
 }
 
 hipError_t launch_cached_attention(const CachedAttentionCall& c, int dtype, hipStream_t s) {
-    const TimedLaunch t(K_CACHED_ATTENTION, s);
-    const dim3 grid((unsigned)c.n_seqs, (unsigned)c.heads);
-    if (dtype == 0) GPTQ_LAUNCH(t, cached_plain_kernel<half_t>, grid, dim3(64), 0, s, c);
-    else GPTQ_LAUNCH(t, cached_plain_kernel<bf16_t>, grid, dim3(64), 0, s, c);
-    return hipGetLastError();
+    CachedArgs a = {};
+    a.c = c;
+    a.rows = (int)unit_rows(c.heads, c.kv_heads);
+    a.head_groups = (int)((c.heads / c.kv_heads + kHeadRows - 1) / kHeadRows);
+    // pos / p = (t + (pos - t) / 2) >> (shift - 1), t = mulhi(mul, pos), shift = ceil(log2 p)
+    while (((uint64_t)1 << a.page_shift) < (uint64_t)c.cache.page_size) ++a.page_shift;
+    a.page_mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << a.page_shift) - (uint64_t)c.cache.page_size)) /
+                                (uint64_t)c.cache.page_size + 1);
+    a.c2 = c.scale * kLog2e;
+    a.parts = static_cast<float*>(c.ws);
+    if (c.d <= 64) return dtype == 0 ? cached_go<half_t, 64>(a, s) : cached_go<bf16_t, 64>(a, s);
+    return dtype == 0 ? cached_go<half_t, 128>(a, s) : cached_go<bf16_t, 128>(a, s);
 }
 
 }  // namespace gptq

@@ -94,7 +94,7 @@ def test_store_refusals(clib):
         assert store(clib, **bad) == EINVAL, bad
     for bad in (dict(dt=F32), dict(d=60), dict(k=ODD), dict(v=ODD), dict(ck=ODD), dict(cv=ODD), dict(kt=132), dict(kh=68), dict(vt=132),
                 dict(vh=68), dict(c0=2052), dict(c1=1028), dict(c2=68), dict(w0=2052), dict(w1=1028), dict(w2=68),
-                dict(c2=1 << 23), dict(pages=1 << 27), dict(pages=1 << 40), dict(page=1 << 40), dict(n=1 << 27), dict(n=1 << 40),
+                dict(c2=1 << 23), dict(c0=1 << 31), dict(w0=1 << 31), dict(pages=1 << 27), dict(pages=1 << 40), dict(page=1 << 40), dict(n=1 << 27), dict(n=1 << 40),
                 dict(d=136, kt=272, kh=136, vt=272, vh=136, c2=136, w2=136)):
         assert store(clib, **bad) == EUNSUPPORTED, bad
     assert store(clib, n=0, k=None, v=None, slots=None) == OK
@@ -116,10 +116,16 @@ def test_cached_refusals(clib):
         assert cached(clib, **bad) == EINVAL, bad
     for bad in (dict(dt=F32), dict(d=60), dict(q=ODD), dict(o=ODD), dict(ck=ODD), dict(cv=ODD), dict(qs=516), dict(qh=68), dict(c0=2052),
                 dict(c1=1028), dict(c2=68), dict(w2=68), dict(os_=516), dict(oh=68), dict(n=(1 << 20) + 1), dict(pages=1 << 27),
-                dict(ldt=1 << 40, most=1 << 40), dict(ldt=1 << 28, most=1 << 28), dict(c2=1 << 23), dict(w2=1 << 23)):
+                dict(ldt=1 << 40, most=1 << 40), dict(ldt=1 << 28, most=1 << 28), dict(c2=1 << 23), dict(w2=1 << 23), dict(n=1 << 20, h=16)):
         assert cached(clib, **bad) == EUNSUPPORTED, bad
     assert cached(clib, n=0, q=None, o=None) == OK
     assert cached(clib, h=0, kv=0) == OK
+    need = clib.gptq_cached_attention_workspace(3, 8, 2, 64, 400, 16)
+    for bad in (dict(ws=None), dict(ws=ODD), dict(room=need - 1)):
+        assert need > 0 and cached(clib, ldt=400, most=400, **bad) == EWORKSPACE, bad
+    for none in ((0, 8, 2, 64, 400, 16), (3, 8, 3, 64, 400, 16), (3, 8, 0, 64, 400, 16), (3, 8, 2, 60, 400, 16), (3, 8, 2, 64, -1, 16),
+                 (3, 8, 2, 64, 400, 0)):
+        assert clib.gptq_cached_attention_workspace(*none) == 0, none
 
 
 def test_binding_refusals(clib):
