@@ -619,8 +619,8 @@ int gptq_packed_matmul(const uint32_t* packed, int bits, int64_t d_out, int64_t 
  * scale not finite or not above 0, unknown dtype, null pointer),
  * GPTQ_EUNSUPPORTED (GPTQ_F32, head_dim above 128 or not a multiple of 8,
  * pointers or strides not 16-byte aligned, a token stride above 2^22, n_tokens
- * or n_seqs above 2^24, heads above 2^16, more than 2^22 pieces of 32 rows by
- * head).
+ * or n_seqs above 2^24, heads above 2^16, 2^23 or more pieces of 32 rows, a row
+ * being a token and one of up to sixteen query heads of a key head).
  */
 int gptq_attention(const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token, int64_t k_head,
                    const void* v, int64_t v_token, int64_t v_head, void* out, int64_t out_token, int64_t out_head,

@@ -511,7 +511,7 @@ inline bool odd_cache(const CacheView& c) {
            c.ldk[0] > INT32_MAX || c.ldv[0] > INT32_MAX || c.ldk[2] > kMaxTokenStride || c.ldv[2] > kMaxTokenStride || c.pages > INT32_MAX ||
            c.page_size > INT32_MAX || c.pages * c.page_size > INT32_MAX;
 }
-constexpr int64_t kMaxPieces = (int64_t)1 << 22;
+constexpr int64_t kMaxPieces = (int64_t)1 << 23;  // workgroups of at most 512 threads: below 2^32 threads
 constexpr int64_t kMaxUnits = (int64_t)1 << 24;  // workgroups of 256 threads: below 2^32 threads
 }  // namespace
 
@@ -534,7 +534,7 @@ int gptq_attention(const void* q, int64_t q_token, int64_t q_head, const void* k
     if (q_token > kMaxTokenStride || k_token > kMaxTokenStride || v_token > kMaxTokenStride ||
         out_token > kMaxTokenStride)
         return GPTQ_EUNSUPPORTED;
-    if ((n / 2 + n_seqs) * heads > kMaxPieces * 16) return GPTQ_EUNSUPPORTED;
+    if (attention_pieces(n, n_seqs, heads, kv_heads) >= kMaxPieces) return GPTQ_EUNSUPPORTED;
     const AttentionCall c = {q, k, v, out, {q_token, q_head}, {k_token, k_head}, {v_token, v_head},
                              {out_token, out_head}, n, heads, kv_heads, d, n_seqs, starts, causal, (float)scale};
     return hip_status(launch_attention(c, dtype, as_stream(stream)));

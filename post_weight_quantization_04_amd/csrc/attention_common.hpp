@@ -56,6 +56,31 @@ __device__ __forceinline__ typename Mat<T>::v4 read_turned(const uint8_t* p) {
     return __builtin_bit_cast(typename Mat<T>::v4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)p));
 }
 
+// Where chunk c (sixteen bytes) of row r lies in its row of LDS, kDp values long.
+// Keys are read by rows: sixteen lanes, sixteen rows, one chunk.  Values are read
+// turned: eight rows of two chunks at a time.  Either way the sixteen chunks
+// cover all banks.
+template <int kDp>
+__device__ __forceinline__ int key_place(int r, int c) {
+    return c ^ (kDp == 128 ? r % 16 : r / 2 % 8);
+}
+template <int kDp>
+__device__ __forceinline__ int value_place(int r, int c) {
+    return c ^ (kDp == 128 ? r % 8 * 2 : r / 2 % 4 * 2);
+}
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// Values of the other half of the wave (lane ^ 32) beside one's own.
+__device__ __forceinline__ float max_halves(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+__device__ __forceinline__ float add_halves(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
 // exp2 of the hardware (one unit in the last place, results below 2^-126 are
 // zero: such weights are below half a unit of any sum they join).
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }

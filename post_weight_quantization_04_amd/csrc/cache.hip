@@ -94,20 +94,6 @@ __device__ __forceinline__ void count_steps(const CachedArgs& a, uint32_t per, i
     before = uniform64(__shfl(wave_scan(part), kWave - 1, kWave));
 }
 
-// Where chunk c (sixteen bytes) of row r lies in its row of LDS.  Keys are read
-// by rows: sixteen lanes, sixteen rows, one chunk.  Values are read turned: eight
-// rows of two chunks at a time.  Either way the sixteen chunks cover all banks.
-template <int kDp>
-__device__ __forceinline__ int key_place(int r, int c) {
-    return c ^ (kDp == 128 ? r % 16 : r / 2 % 8);
-}
-template <int kDp>
-__device__ __forceinline__ int value_place(int r, int c) {
-    return c ^ (kDp == 128 ? r % 8 * 2 : r / 2 % 4 * 2);
-}
-
-typedef __attribute__((address_space(3))) void lds_void;
-
 // Memory to LDS without registers in between, a wave's lanes one behind the
 // other from `lds` on.  The pages of a cache lie further apart than a buffer
 // load's 32-bit offsets reach, and the compiler takes the global form for one

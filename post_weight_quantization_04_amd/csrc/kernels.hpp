@@ -185,6 +185,11 @@ struct AttentionCall {
     int causal;
     float scale;
 };
+// Pieces of 32 rows: no kernel has more workgroups.
+inline int64_t attention_pieces(int64_t n, int64_t n_seqs, int64_t heads, int64_t kv_heads) {
+    const int64_t group = heads / kv_heads, rows = group < kHeadRows ? group : kHeadRows;
+    return (n / (32 / rows) + n_seqs) * kv_heads * ((group + kHeadRows - 1) / kHeadRows);
+}
 hipError_t launch_attention(const AttentionCall& c, int dtype, hipStream_t s);
 
 // ---- paged cache ----------------------------------------------------------------
