@@ -587,7 +587,7 @@ const char* gptq_fp8_gated_kernel(int64_t d_ff, int64_t d_in, int64_t n_tokens, 
  * group_size or one not dividing d_in, a stride below its row, unknown dtype
  * or activation, null pointer), GPTQ_EUNSUPPORTED (x_dtype GPTQ_F32, y_dtype
  * neither x_dtype nor GPTQ_F32, group_size not a multiple of 16, d_in or ldx
- * above 2^21, d_out or n_tokens above 2^24, more than 2^22 tiles of 256 rows
+ * above 2^21, d_out or n_tokens above 2^24, more than 2^21 tiles of 256 rows
  * by 256 tokens).
  */
 int gptq_packed_matmul(const uint32_t* packed, int bits, int64_t d_out, int64_t d_in, const float* scales,

@@ -469,6 +469,7 @@ const char* gptq_fp8_gated_kernel(int64_t d_ff, int64_t d_in, int64_t n, int com
 namespace {
 constexpr int64_t kPackedMaxCols = (int64_t)1 << 21;  // 256 rows of X stay within 2^30 bytes
 constexpr int64_t kPackedMaxRows = (int64_t)1 << 24;
+constexpr int64_t kPackedMaxTiles = (int64_t)1 << 21;  // four workgroups of 256 threads each: below 2^32 threads
 }  // namespace
 
 int gptq_packed_matmul(const uint32_t* packed, int bits, int64_t d_out, int64_t d_in, const float* scales,
@@ -485,7 +486,7 @@ int gptq_packed_matmul(const uint32_t* packed, int bits, int64_t d_out, int64_t 
         return GPTQ_EUNSUPPORTED;
     if (d_in > kPackedMaxCols || ldx > kPackedMaxCols || d_out > kPackedMaxRows || n > kPackedMaxRows)
         return GPTQ_EUNSUPPORTED;
-    if (((d_out + 255) / 256) * ((n + 255) / 256) > kF8MaxTiles) return GPTQ_EUNSUPPORTED;
+    if (((d_out + 255) / 256) * ((n + 255) / 256) > kPackedMaxTiles) return GPTQ_EUNSUPPORTED;
     const PackedProduct c = {packed, scales, zeros, X, bias, residual, Y, d_out, d_in, group_size, n, ldx, ldr, ldy,
                              bits, activation};
     return hip_status(launch_packed_matmul(c, x_dtype, y_dtype, as_stream(stream)));

@@ -71,6 +71,25 @@ __device__ __forceinline__ int wave_id() {
 }
 
 // ---------------------------------------------------------------------------
+// Tiles of products over the XCDs
+// ---------------------------------------------------------------------------
+constexpr int kXcd = 8;
+constexpr unsigned kBand = 8;  // tiles of weight rows that share their tokens before the next tokens
+
+// Workgroup id -> tile.  Workgroups go to the eight XCDs in turn; each XCD gets
+// a run of tiles, in bands of kBand tile rows, tokens outermost in a band, so
+// that the tiles it works on at a time share rows in its own L2.
+__device__ __forceinline__ void xcd_tile_of(unsigned id, unsigned mt, unsigned nt, unsigned& mi, unsigned& ni) {
+    const unsigned tiles = mt * nt, per = tiles / kXcd, rest = tiles % kXcd;
+    const unsigned x = id % kXcd, i = id / kXcd;
+    const unsigned t = x * per + min(x, rest) + i;
+    const unsigned band = t / (kBand * nt), in = t % (kBand * nt);
+    const unsigned rows = min(kBand, mt - band * kBand);
+    mi = band * kBand + in % rows;
+    ni = in / rows;
+}
+
+// ---------------------------------------------------------------------------
 // Asymmetric min-max grid, IEEE float32 op sequence (only subtraction,
 // division and rint: nothing a compiler could contract).
 //   mn = min(0, lo), mx = max(0, hi); an all-zero range becomes [-1, 1];

@@ -344,22 +344,6 @@ struct TileArgs {
     unsigned mt, nt;  // tiles along the weight rows and the tokens
 };
 
-constexpr int kXcd = 8;
-constexpr unsigned kBand = 8;  // tiles of weight rows that share their tokens before the next tokens
-
-// Workgroup id -> tile.  Workgroups go to the eight XCDs in turn; each XCD gets
-// a run of tiles, in bands of kBand tile rows, tokens outermost in a band, so
-// that the tiles it works on at a time share rows in its own L2.
-__device__ __forceinline__ void f8_tile_of(unsigned id, unsigned mt, unsigned nt, unsigned& mi, unsigned& ni) {
-    const unsigned tiles = mt * nt, per = tiles / kXcd, rest = tiles % kXcd;
-    const unsigned x = id % kXcd, i = id / kXcd;
-    const unsigned t = x * per + min(x, rest) + i;
-    const unsigned band = t / (kBand * nt), in = t % (kBand * nt);
-    const unsigned rows = min(kBand, mt - band * kBand);
-    mi = band * kBand + in % rows;
-    ni = in / rows;
-}
-
 template <typename T, int kTM, int kTN, int kWM, int kWN, int kStages, int kSplit, bool kGated, bool kHalf, bool kChannels, bool kEarly, bool kCarry>
 __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileArgs a) {
     constexpr int kWaves = kWM * kWN, kThreads = kWaves * kWave;  // of one group
@@ -385,7 +369,7 @@ __global__ __launch_bounds__(kSplit* kWM* kWN* kWave) void f8_tile_kernel(TileAr
     const int base = kSplit > 1 ? group * kBytes : 0;  // of the group's part of a stage
     const int wm = w / kWN, wn = w % kWN, l16 = lane % 16, kg = lane / 16;
     unsigned mi, ni;
-    f8_tile_of(blockIdx.x, a.mt, a.nt, mi, ni);
+    xcd_tile_of(blockIdx.x, a.mt, a.nt, mi, ni);
     constexpr int kRows = kGated ? kTM / 2 : kTM;  // rows of one matrix
     const int64_t m0 = (int64_t)mi * kRows, t0 = (int64_t)ni * kTN;
     const int rows = (int)min(m.M - m0, (int64_t)kRows), toks = (int)min(m.n - t0, (int64_t)kTN);
