@@ -15,6 +15,7 @@ struct PmArgs {
     PackedProduct c;
     int nw, ng, nb;                          // words and groups of a row, blocks of 128
     uint32_t group, group_mul, group_shift;  // the group's size (a whole row for 0), and division by it
+    int vec;                                 // rows of x start 16-byte aligned and hold whole chunks of eight
     int y32;                                 // results, bias and residual in float32, else in x's type
     unsigned mt, nt;                         // tiles along the weight rows and the tokens
 };
@@ -30,15 +31,11 @@ __device__ __forceinline__ uint32_t group_of(const PmArgs& a, uint32_t k) {
     return a.group_shift ? (t + ((k - t) >> 1)) >> (a.group_shift - 1) : k;
 }
 
-// The words of 32 codes at byte offset off + base of a buffer.  tail: the run may
-// pass the matrix's end, so each word is loaded, and checked, by itself.
+// The words of 32 codes at byte offset off + base of a buffer.  (The range check is
+// each word's own, so a run that passes the matrix's end brings what is left of
+// it and zeros.)
 template <int kBits>
-__device__ __forceinline__ void load_run(uint32_t (&w)[kBits], __amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t base, bool tail) {
-    if (tail) {
-#pragma unroll
-        for (int i = 0; i < kBits; ++i) w[i] = __builtin_amdgcn_raw_buffer_load_b32(r, off + 4 * i, base, 0);
-        return;
-    }
+__device__ __forceinline__ void load_run(uint32_t (&w)[kBits], __amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t base) {
     if constexpr (kBits >= 4) {
         const uint4v v = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(r, off, base, 0));
         w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
@@ -66,7 +63,7 @@ __device__ __forceinline__ void load_run(uint32_t (&w)[kBits], __amdgpu_buffer_r
 // pair's bytes go to both halves of a word (one byte permutation, from any byte
 // of the run), a mask leaves the first code in the lower half and the second in
 // the upper one, each where it stands in its bytes, and one packed fma takes 1024,
-// the position and z out again: 3 instructions a pair.  Codes of six or seven
+// the position and z out again: three instructions a pair.  Codes of six or seven
 // bits do not fit beside each other and are shifted first.
 // bfloat16, which has no packed arithmetic: by way of float32.
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
@@ -78,11 +75,16 @@ struct Zero;
 template <int kBits>
 struct Zero<half_t, kBits> {
     half_t z;
-    __device__ __forceinline__ explicit Zero(int zero) { z = (half_t)(float)zero; }
+    uint32_t exponent;  // in a vector register: two literals do not fit one instruction
+    __device__ __forceinline__ explicit Zero(int zero) {
+        z = (half_t)(float)zero;
+        exponent = 0x64006400u;
+        asm("" : "+v"(exponent));
+    }
     // 1024 + c 2^kLow, 1024 + d 2^kHigh -> c - z, d - z
     template <int kLow, int kHigh>
     __device__ __forceinline__ uint32_t out(uint32_t pair) const {
-        const half2v v = __builtin_bit_cast(half2v, pair | 0x64006400u);
+        const half2v v = __builtin_bit_cast(half2v, pair | exponent);
         if constexpr (kLow == 0 && kHigh == 0) return __builtin_bit_cast(uint32_t, v + ((half2v)(half_t)-1024.0f - (half2v)z));
         constexpr float kL = 1.0f / (1 << kLow), kH = 1.0f / (1 << kHigh);
         const half2v mul = {(half_t)kL, (half_t)kH}, one = {(half_t)(-1024.0f * kL), (half_t)(-1024.0f * kH)};
@@ -154,6 +156,16 @@ __device__ __forceinline__ void codes32(frag_t (&f)[4], const uint32_t (&w)[kBit
     f[3] = codes8<T, kBits, 3>(w, b);
 }
 
+// Loads of what belongs to sixteen weight rows give four neighbouring lanes to a
+// row: the address unit takes sixteen lanes at a time, and asks once for what
+// neighbours read of one line (16 requests an instruction; 64 with the lanes in
+// the order of the MFMA's operands, which held the products' tiles up longer
+// than anything else).  from_row hands a value to the operand's lane: row l16, k
+// group kg or, for what is the row's, any.
+__device__ __forceinline__ uint32_t from_row(uint32_t v, int place) {
+    return (uint32_t)__builtin_amdgcn_ds_bpermute(4 * place, (int)v);
+}
+
 // A lane of k group kg holds columns 32 kg + 8 e .. of a block of 128 as f[e].
 // Turned, f[e] holds columns 32 e + 8 kg: the four lanes of a row exchange
 // fragments as a 4 x 4 transpose, halves of the wave first, then halves of those.
@@ -174,6 +186,37 @@ __device__ __forceinline__ void turn_blocks(frag_t (&f)[4]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[e][i] = v[e];
     }
+}
+
+// Where chunk c (sixteen bytes) of token row r lies in its row of 256 bytes of
+// LDS: c ^ pm_swizzle(r).  LDS serves sixteen lanes at a time: eight rows of one k
+// group (0-3, 12-15) with the other eight (4-11) of the next, whose chunk differs
+// by 4 (codes by runs) or by 1 (turned).  The swizzle is a permutation that
+// takes the bits 0 and 1 of r, which leave rows 4-11 among themselves, to the
+// bits 2 and 0, so that the sixteen chunks differ either way.
+__host__ __device__ constexpr int pm_swizzle(int r) {
+    return (r & 1) << 2 | (r >> 1 & 1) | (r >> 2 & 1) << 1 | (r & 8);
+}
+
+__device__ __forceinline__ void pm_copy16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off, uint32_t base) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, base, 0, 0);
+}
+
+// Columns k .. k + 7 of a row of x from p + at on, whose `left` columns need no more
+// than their type's alignment; zeros behind the last.
+template <typename T>
+__device__ __forceinline__ frag_t pm_chunk(const T* p, int64_t at, int k, int left) {
+    T v[8] = {};
+    if (left >= kPmBlock) {  // (the same for all lanes: no branch around the load)
+        __builtin_memcpy(v, p + at + k, 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (k + e < left) v[e] = p[at + k + e];
+    }
+    frag_t f;
+    __builtin_memcpy(&f, v, 16);
+    return f;
 }
 
 __device__ __forceinline__ float activated(float v, int activation) {

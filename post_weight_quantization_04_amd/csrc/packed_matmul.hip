@@ -8,7 +8,7 @@
 // Tokens are the rows of the MFMA's result and weight rows its columns: a lane's
 // values belong to one weight row, so that scale and zero are one value a lane.
 //
-// This file: few tokens, and which kernel a product is sent to.
+// This file: which kernel a product is sent to.
 #include <algorithm>
 
 #include "packed_common.hpp"
@@ -18,161 +18,32 @@ namespace gptq {
 
 namespace {
 
-// ---------------------------------------------------------------------------
-// Few tokens: sixteen weight rows and 16 kTn tokens a workgroup, whose waves
-// share the blocks of 128 columns and work on their own, without barriers.  A
-// lane loads a run of 32 codes of its row (64 neighbouring bytes for the four
-// lanes of a row at four bits), and of x what stands beside one MFMA step, 64
-// neighbouring bytes of a token, which is why the codes are turned: read by runs,
-// x would come in 64 pieces of 16 bytes.  Two blocks are in flight a wave.  The
-// waves' sums meet in LDS, added in wave order.
-// ---------------------------------------------------------------------------
-template <typename T, int kBits, bool kFine, int kWaves, int kTn>
-__global__ __launch_bounds__(kWaves* kWave) void packed_few_kernel(PmArgs a) {
-    constexpr int kScales = kFine ? 8 : 1;  // of a block
-    __shared__ float sums[kWaves][kTn][4][kWave];
-    typedef typename Mat<T>::v8 v8;
-    const PackedProduct& c = a.c;
-    const int tid = threadIdx.x, lane = tid % kWave, w = wave_id(), l16 = lane % 16, kg = lane / 16;
-    const int64_t r0 = (int64_t)blockIdx.x * 16, t0 = (int64_t)blockIdx.y * (16 * kTn);
-    const int rows = (int)min(c.M - r0, (int64_t)16);
-    const int row = min(l16, rows - 1);
-    const __amdgpu_buffer_rsrc_t rw = pm_rsrc(c.packed + r0 * a.nw, (uint32_t)rows * (uint32_t)a.nw * 4u);
-    const uint32_t wo = 4u * ((uint32_t)row * (uint32_t)a.nw + (uint32_t)(kg * kBits));
-    const float* scales = c.scales + (r0 + row) * a.ng;
-    const int32_t* zeros = c.zeros + (r0 + row) * a.ng;
-    const T* x[kTn];
-#pragma unroll
-    for (int j = 0; j < kTn; ++j)
-        x[j] = static_cast<const T*>(c.x) + min(t0 + 16 * j + l16, c.n - 1) * c.ldx + 8 * kg;
-    const int nb = a.nb;
-    const bool ragged = c.K % kPmBlock != 0;
-
-    struct Block {
-        uint32_t w[kBits];
-        v8 x[kTn][4];
-        float s[kScales];
-        int z[2];
+// Which kernel, by estimated time: rounds of workgroups over the CUs, each with a
+// part of its own and one for a block of 128 columns, in us:
+//                 few tokens (16 rows, a round)      32 x 64        64 x 128, one a CU   two   128 x 384
+//   4-bit f16     1.7 + 0.1 (to 4), 0.12 (to 16), 0.2   2.0 + 0.4      2.0 + 0.9   2.0 + 1.4   3.5 + 2.65
+PmKernel choose(const PmArgs& a, bool fine, int64_t cus) {
+    const int64_t M = a.c.M, n = a.c.n, nb = a.nb;
+    if (n <= 4) return kPmFew;
+    auto rounds = [&](int64_t tokens, int64_t rows, int64_t each) {
+        return (double)((((n + tokens - 1) / tokens) * ((M + rows - 1) / rows) + cus * each - 1) / (cus * each));
     };
-    auto load = [&](Block& g, int b) {
-        b = min(b, nb - 1);  // past the last block, that one again, never used
-        const bool tail = ragged && b == nb - 1;
-        const uint32_t k0 = (uint32_t)b * kPmBlock;
-        load_run<kBits>(g.w, rw, wo, (uint32_t)b * (16u * kBits), tail);
-        if (kFine) {
-            g.z[0] = zeros[group_of(a, k0 + 32 * kg)];
-            g.z[1] = zeros[group_of(a, k0 + 32 * kg + 16)];
-#pragma unroll
-            for (int i = 0; i < kScales; ++i) g.s[i] = scales[group_of(a, k0 + 16 * i)];
-        } else {
-            const uint32_t at = group_of(a, k0);
-            g.z[0] = g.z[1] = zeros[at];
-            g.s[0] = scales[at];
-        }
-#pragma unroll
-        for (int j = 0; j < kTn; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const T* p = x[j] + (k0 + 32 * e);
-                if (!tail) {
-                    __builtin_memcpy(&g.x[j][e], p, 16);
-                } else {
-                    const int left = (int)c.K - (int)(k0 + 32 * e + 8 * kg);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) g.x[j][e][i] = i < left ? p[i] : (T)0.0f;
-                }
-            }
-    };
-    float4v acc[kTn];
-#pragma unroll
-    for (int j = 0; j < kTn; ++j) acc[j] = (float4v){};
-    auto use = [&](const Block& g) {
-        frag_t f[4];
-        codes32<T, kBits>(f, g.w, g.z[0], g.z[1]);
-        turn_blocks(f);
-#pragma unroll
-        for (int j = 0; j < kTn; ++j) {
-            if (!kFine) {
-                float4v p = {};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) p = Mat<T>::mfma16(g.x[j][e], __builtin_bit_cast(v8, f[e]), p);
-#pragma unroll
-                for (int v = 0; v < 4; ++v) acc[j][v] = fmaf(p[v], g.s[0], acc[j][v]);
-            } else {
-                // sixteen columns at a time: the others' codes as zeros
-#pragma unroll
-                for (int h = 0; h < 8; ++h) {
-                    const frag_t half = kg / 2 == h % 2 ? f[h / 2] : (frag_t){};
-                    const v8 xh = kg / 2 == h % 2 ? g.x[j][h / 2] : (v8){};  // an infinity times zero would be NaN
-                    const float4v p = Mat<T>::mfma16(xh, __builtin_bit_cast(v8, half), (float4v){});
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[j][v] = fmaf(p[v], g.s[h], acc[j][v]);
-                }
-            }
-        }
-    };
-    const int mine = w < nb ? (nb - w + kWaves - 1) / kWaves : 0;
-    if (mine > 0) {
-        Block g0, g1;
-        load(g0, w);
-        load(g1, w + kWaves);
-        int i = 0;
-        for (; i + 2 <= mine; i += 2) {
-            use(g0);
-            load(g0, w + (i + 2) * kWaves);
-            use(g1);
-            load(g1, w + (i + 3) * kWaves);
-        }
-        if (i < mine) use(g0);
-    }
-#pragma unroll
-    for (int j = 0; j < kTn; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) sums[w][j][v][lane] = acc[j][v];
-    __syncthreads();
-    // value i of the 256 kTn: token tile, register, lane
-    for (int i = tid; i < 256 * kTn; i += kWaves * kWave) {
-        const int j = i / 256, v = i / kWave % 4, l = i % kWave;
-        float y = 0.0f;
-#pragma unroll
-        for (int ww = 0; ww < kWaves; ++ww) y += sums[ww][j][v][l];
-        const int64_t t = t0 + 16 * j + 4 * (l / 16) + v, o = r0 + l % 16;
-        if (t >= c.n || o >= c.M) continue;
-        if (a.y32) {
-            if (c.bias) y += static_cast<const float*>(c.bias)[o];
-            y = activated(y, c.activation);
-            if (c.residual) y += static_cast<const float*>(c.residual)[t * c.ldr + o];
-            static_cast<float*>(c.y)[t * c.ldy + o] = y;
-        } else {
-            if (c.bias) y += to_f32(static_cast<const T*>(c.bias)[o]);
-            y = activated(y, c.activation);
-            if (c.residual) y += to_f32(static_cast<const T*>(c.residual)[t * c.ldr + o]);
-            static_cast<T*>(c.y)[t * c.ldy + o] = (T)y;
-        }
-    }
+    const double few = rounds(32, 16, 1) * (1.7 + (n <= 16 ? 0.12 : 0.2) * nb), small = rounds(32, 64, 1) * (2.0 + 0.4 * nb);
+    const bool one = rounds(64, 128, 1) == 1.0;
+    const double mid = one ? 2.0 + 0.9 * nb : rounds(64, 128, 2) * (2.0 + 1.4 * nb);
+    const double big = a.vec && !fine ? rounds(128, 384, 1) * (3.5 + 2.65 * nb) : 1e30;
+    const double least = std::min(std::min(few, small), std::min(mid, big));
+    return least == few ? kPmFew : least == small ? kPm32x64 : least == mid ? kPm64x128 : kPm128x384;
 }
-
-template <typename T, int kBits, bool kFine, int kWaves, int kTn>
-hipError_t few_go(const PmArgs& a, hipStream_t s) {
-    const TimedLaunch t(K_PACKED_MATMUL, s);
-    const dim3 grid((unsigned)((a.c.M + 15) / 16), (unsigned)((a.c.n + 16 * kTn - 1) / (16 * kTn)));
-    GPTQ_LAUNCH(t, (packed_few_kernel<T, kBits, kFine, kWaves, kTn>), grid, dim3(kWaves * kWave), 0, s, a);
-    return hipGetLastError();
-}
-
-template <typename T, int kBits, bool kFine>
-hipError_t few_launch(const PmArgs& a, hipStream_t s) {
-    if (a.c.n <= 16) return few_go<T, kBits, kFine, 8, 1>(a, s);
-    return few_go<T, kBits, kFine, 8, 2>(a, s);
-}
-
-constexpr int64_t kPmFewTokens = 32;  // the few-token kernel up to here
 
 template <typename T, int kBits>
 hipError_t bits_go(const PmArgs& a, hipStream_t s) {
     const bool fine = a.group % kPmBlock != 0 && a.ng > 1;
-    if (a.c.n <= kPmFewTokens) return fine ? few_launch<T, kBits, true>(a, s) : few_launch<T, kBits, false>(a, s);
-    return launch_packed_tile<T, kBits>(a, fine, s);
+    const int64_t cus = device_cu_count();
+    if (cus <= 0) return hipErrorInvalidDevice;
+    const PmKernel kernel = choose(a, fine, cus);
+    if (kernel == kPmFew) return launch_packed_few<T, kBits>(a, fine, s);
+    return launch_packed_tile<T, kBits>(a, kernel, fine, s);
 }
 
 template <typename T>
@@ -200,6 +71,7 @@ hipError_t launch_packed_matmul(const PackedProduct& c, int x_dtype, int y_dtype
     while (((uint64_t)1 << a.group_shift) < a.group) ++a.group_shift;
     a.group_mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << a.group_shift) - a.group)) / a.group + 1);
     a.y32 = y_dtype == 1;
+    a.vec = c.K % 8 == 0 && c.ldx % 8 == 0 && reinterpret_cast<uintptr_t>(c.x) % 16 == 0;
     return x_dtype == 0 ? typed_go<half_t>(a, s) : typed_go<bf16_t>(a, s);
 }
 

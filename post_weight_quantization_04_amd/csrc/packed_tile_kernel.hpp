@@ -7,46 +7,70 @@ namespace gptq {
 
 namespace {
 
-// Where chunk c (sixteen bytes) of token row r lies in its row of 256 bytes of
-// LDS: c ^ pm_swizzle(r).  LDS serves sixteen lanes at a time: eight rows of one k
-// group (0-3, 12-15) with the other eight (4-11) of the next, whose chunk differs
-// by 4 (codes by runs) or by 1 (turned).  The swizzle is a permutation that
-// takes the bits 0 and 1 of r, which leave rows 4-11 among themselves, to the
-// bits 2 and 0, so that the sixteen chunks differ either way.
-__host__ __device__ constexpr int pm_swizzle(int r) {
-    return (r & 1) << 2 | (r >> 1 & 1) | (r >> 2 & 1) << 1 | (r & 8);
+// Bias, activation and residual of eight neighbouring rows of token t, and their store.
+template <typename T>
+__device__ __forceinline__ void pm_finish(const PmArgs& a, const float* sums, int64_t t, int64_t o) {
+    const PackedProduct& c = a.c;
+    const int64_t left = c.M - o;
+    if (t >= c.n || left <= 0) return;
+    float y[8], e[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = sums[k];
+    if (c.bias) {
+        if (a.y32) load8<float, false>(e, static_cast<const float*>(c.bias) + o, left);
+        else load8<T, false>(e, static_cast<const T*>(c.bias) + o, left);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] += e[k];
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = activated(y[k], c.activation);
+    if (c.residual) {
+        if (a.y32) load8<float, false>(e, static_cast<const float*>(c.residual) + t * c.ldr + o, left);
+        else load8<T, false>(e, static_cast<const T*>(c.residual) + t * c.ldr + o, left);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] += e[k];
+    }
+    if (a.y32) store8<float, false>(static_cast<float*>(c.y) + t * c.ldy + o, y, left);
+    else store8<T, false>(static_cast<T*>(c.y) + t * c.ldy + o, y, left);
 }
 
-__device__ __forceinline__ void pm_copy16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off, uint32_t base) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, base, 0, 0);
-}
-
-// kTT tokens by kTR weight rows a workgroup, kWT x kWR waves.  A block of 128
-// columns of x is a stage of LDS, copied from memory without passing registers
-// one block ahead, one barrier a block (kVec; else, where rows of x are not
-// aligned or end inside a chunk, by way of registers).  A wave loads the codes of
-// its own rows into registers, a block ahead, and converts them there once a
-// block: they then meet all of its tokens.
-template <typename T, int kBits, bool kFine, bool kVec, int kTT, int kTR, int kWT, int kWR, int kPerCu>
-__global__ __launch_bounds__(kWT* kWR* kWave, kWT* kWR / 4 * kPerCu) void packed_tile_kernel(PmArgs a) {
-    constexpr int kWaves = kWT * kWR, kMt = kTT / kWT / 16, kNt = kTR / kWR / 16;
+// kTT tokens by kTR weight rows a workgroup, whose waves share the rows: each
+// wave loads the codes of its own into registers, converts them there once a
+// block and has them meet all of the tokens.  A block of 128 columns of x is a
+// stage of LDS, four of which are a ring: copied from memory without passing
+// registers three blocks ahead, one barrier a block (kVec; else, where rows of x
+// are not aligned or end inside a chunk, by way of registers).
+//
+// Tokens and rows lie this way round because copies are what the tile waits for:
+// with waves two by four over 256 x 192, which copies twice the x for the same
+// products, 8192 x 4096 -> 11008 took 881 us, 616 of them without the copies.
+//
+// A tile that has a CU to itself takes 0.9 us a block whatever its size: each step
+// is a chain of reads, conversions and products.  So small products have kGroups
+// such groups of waves in a workgroup, which take turns with the blocks and add
+// their sums at the end.
+template <typename T, int kBits, bool kFine, bool kVec, int kTT, int kTR, int kWaves, int kPerCu, int kRing, int kGroups>
+__global__ __launch_bounds__(kGroups* kWaves* kWave, kGroups* kWaves / 4 * kPerCu) void packed_tile_kernel(PmArgs a) {
+    constexpr int kMt = kTT / 16, kNt = kTR / kWaves / 16;
     constexpr int kCopies = kTT / 4 / kWaves;  // of four token rows, a wave and stage
-    static_assert(kTT % (4 * kWaves) == 0, "whole copies");
+    static_assert(kRing == 1 || kRing == 4, "steps come in fours");
+    static_assert(kTT % (4 * kWaves) == 0 && kTR % (16 * kWaves) == 0, "whole copies and rows");
     constexpr int kBytes = kTT * 2 * kPmBlock;
     // separate arrays: the compiler then knows that a read of one does not wait for copies into another
-    __shared__ __align__(16) uint8_t lds0[kBytes];
-    __shared__ __align__(16) uint8_t lds1[kBytes];
+    __shared__ __align__(16) uint8_t lds0[kGroups * kBytes];
+    __shared__ __align__(16) uint8_t lds1[kGroups * kBytes];
+    __shared__ __align__(16) uint8_t lds2[kGroups * kBytes];
+    __shared__ __align__(16) uint8_t lds3[kGroups * kBytes];
     typedef typename Mat<T>::v8 v8;
 
     const PackedProduct& c = a.c;
-    const int tid = threadIdx.x, lane = tid % kWave, w = wave_id(), l16 = lane % 16, kg = lane / 16;
-    const int wt = w / kWR, wr = w % kWR;
+    const int tid = threadIdx.x, lane = tid % kWave, l16 = lane % 16, kg = lane / 16;
+    const int set = kGroups > 1 ? wave_id() / kWaves : 0, w = wave_id() - set * kWaves, base = set * kBytes;
     unsigned mi, ni;
     xcd_tile_of(blockIdx.x, a.mt, a.nt, mi, ni);
     const int64_t r0 = (int64_t)mi * kTR, t0 = (int64_t)ni * kTT;
     const int rows = (int)min(c.M - r0, (int64_t)kTR), toks = (int)min(c.n - t0, (int64_t)kTT);
     const int nb = a.nb;
-    const bool ragged = c.K % kPmBlock != 0;
     const T* x = static_cast<const T*>(c.x) + t0 * c.ldx;
 
     const __amdgpu_buffer_rsrc_t rw = pm_rsrc(c.packed + r0 * a.nw, (uint32_t)rows * (uint32_t)a.nw * 4u);
@@ -56,69 +80,59 @@ __global__ __launch_bounds__(kWT* kWR* kWave, kWT* kWR / 4 * kPerCu) void packed
 
     // Sources of this lane's copies: four rows an instruction; every fourth
     // instruction has the same swizzle.  Rows past the last lie past the end of the
-    // buffer (a row's stride covers what is read of it), and load zero.
+    // buffer (a row's stride covers what is read of it), and load zero; so do
+    // chunks past the last column, since what follows it is not the row's.
     const int copy_row = 4 * kCopies * w + lane / 16;
-    uint32_t xo[4];
-    int xc[4];
+    uint32_t xo[kCopies];
+    int xk[kCopies];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kCopies; ++i) {
         const int r = copy_row + 4 * i;
-        xc[i] = 8 * ((lane % 16) ^ pm_swizzle(r % 16));
-        xo[i] = 2 * ((uint32_t)r * (uint32_t)c.ldx + (uint32_t)xc[i]);
+        xk[i] = 8 * ((lane % 16) ^ pm_swizzle(r % 16));
+        xo[i] = 2 * ((uint32_t)r * (uint32_t)c.ldx + (uint32_t)xk[i]);
     }
-    auto copy = [&](uint8_t* st, int b) {
-        const int k0 = min(b, nb - 1) * kPmBlock;  // past the last block, that one again, never used
-        const bool tail = ragged && b >= nb - 1;
+    // (steps count the group's blocks: every kGroups-th)
+    frag_t held[kVec ? 1 : kCopies];  // by way of registers: what goes to LDS a step after it was asked for
+    auto copy = [&](uint8_t* st, int step) {
+        const int b = step * kGroups + set, left = (int)c.K - b * kPmBlock;
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
-            uint8_t* to = st + 1024 * (kCopies * w + i);
-            if (kVec) {
-                const uint32_t off = tail && k0 + xc[i % 4] >= c.K ? kPmOut : xo[i % 4];
-                pm_copy16(rx, to, off, (uint32_t)(2 * k0) + (uint32_t)(i / 4) * 32u * (uint32_t)c.ldx);
-            } else {
-                const int r = copy_row + 4 * i, k = k0 + xc[i % 4];
-                const T* p = x + r * c.ldx + k;
-                T v[8] = {};
-                if (r < toks) {
-                    if (k + 8 <= c.K) __builtin_memcpy(v, p, 16);
-                    else
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (k + e < c.K) v[e] = p[e];
-                }
-                __builtin_memcpy(to + 16 * lane, v, 16);
-            }
+            if (kVec) pm_copy16(rx, st + (base + 1024 * (kCopies * w + i)), xk[i] < left ? xo[i] : kPmOut, (uint32_t)(2 * b * kPmBlock));
+            else held[i] = pm_chunk(x, min(copy_row + 4 * i, toks - 1) * c.ldx + b * kPmBlock, xk[i], left);
         }
     };
+    auto put = [&](uint8_t* st) {
+#pragma unroll
+        for (int i = 0; i < kCopies && !kVec; ++i) *reinterpret_cast<frag_t*>(st + (base + 1024 * (kCopies * w + i) + 16 * lane)) = held[i];
+    };
 
-    // This lane's rows: 16 j + l16 of the wave's.
-    uint32_t wo[kNt], so[kNt];
+    // The wave's rows, 16 j + l16 for this lane; scales and zeros come by way of row 16 j + lane / 4.
+    const uint32_t r = (uint32_t)(w * kNt * 16 + lane / 4);
+    const uint32_t wo = 4u * ((uint32_t)(w * kNt * 16 + l16) * (uint32_t)a.nw + (uint32_t)(kg * kBits)), so = 4u * r * (uint32_t)a.ng;
+    const uint32_t w16 = 64u * (uint32_t)a.nw, s16 = 64u * (uint32_t)a.ng;  // sixteen rows on
+    // The codes of the next kRing blocks (one where registers are short).
+    uint32_t words[kRing][kNt][kBits];
+    auto load = [&](int step, int slot) {
+        const int b = step * kGroups + set;
 #pragma unroll
-    for (int j = 0; j < kNt; ++j) {
-        const uint32_t r = (uint32_t)((wr * kNt + j) * 16 + l16);
-        wo[j] = 4u * (r * (uint32_t)a.nw + (uint32_t)(kg * kBits));
-        so[j] = 4u * r * (uint32_t)a.ng;
-    }
+        for (int j = 0; j < kNt; ++j) load_run<kBits>(words[slot][j], rw, wo, (uint32_t)b * (16u * kBits) + (uint32_t)j * w16);
+    };
+    // Scales and zeros of four blocks, one a lane of the row's four (groups of
+    // whole blocks; of finer ones, the zeros of this lane's run of codes of one block).
     constexpr int kZeros = kFine ? 2 : 1;
-    uint32_t words[kNt][kBits];
-    int zs[kNt][kZeros];
-    float ss[kNt];  // of groups of whole blocks
-    auto load = [&](int b) {
-        b = min(b, nb - 1);
-        const bool tail = ragged && b == nb - 1;
-        const uint32_t k0 = (uint32_t)b * kPmBlock, base = (uint32_t)b * (16u * kBits);
-#pragma unroll
-        for (int j = 0; j < kNt; ++j) load_run<kBits>(words[j], rw, wo[j], base, tail);
+    uint32_t ss[kNt], zs[kNt][kZeros];
+    auto load_grids = [&](int step) {
+        const int b = step * kGroups + set;
 #pragma unroll
         for (int j = 0; j < kNt; ++j) {
             if (kFine) {
 #pragma unroll
                 for (int h = 0; h < kZeros; ++h)
-                    zs[j][h] = (int)__builtin_amdgcn_raw_buffer_load_b32(rz, so[j] + 4 * group_of(a, k0 + 32 * kg + 16 * h), 0, 0);
+                    zs[j][h] = __builtin_amdgcn_raw_buffer_load_b32(rz, so + 4 * group_of(a, (uint32_t)(b * kPmBlock + 32 * (lane % 4) + 16 * h)), (uint32_t)j * s16, 0);
             } else {
-                const uint32_t at = 4 * group_of(a, k0);
-                zs[j][0] = (int)__builtin_amdgcn_raw_buffer_load_b32(rz, so[j], at, 0);
-                ss[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, so[j], at, 0));
+                const uint32_t at = so + 4 * group_of(a, (uint32_t)((b + lane % 4 * kGroups) * kPmBlock));
+                zs[j][0] = __builtin_amdgcn_raw_buffer_load_b32(rz, at, (uint32_t)j * s16, 0);
+                ss[j] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, (uint32_t)j * s16, 0);
             }
         }
     };
@@ -129,53 +143,94 @@ __global__ __launch_bounds__(kWT* kWR* kWave, kWT* kWR / 4 * kPerCu) void packed
 #pragma unroll
         for (int j = 0; j < kNt; ++j) acc[i][j] = (float4v){};
 
-    const int place = l16 * 2 * kPmBlock;
+    const int place = base + l16 * 2 * kPmBlock;
     auto tokens = [&](const uint8_t* st, int i, int e) {
         const int chunk = kFine ? 4 * e + kg : 4 * kg + e;
-        return *reinterpret_cast<const v8*>(st + ((wt * kMt + i) * 16 * 2 * kPmBlock + place + 16 * (chunk ^ pm_swizzle(l16))));
+        return *reinterpret_cast<const v8*>(st + (i * 16 * 2 * kPmBlock + place + 16 * (chunk ^ pm_swizzle(l16))));
     };
-    auto step = [&](uint8_t* st, uint8_t* nx, int b) {
-        frag_t f[kNt][4];
-        float s[kNt];
-#pragma unroll
-        for (int j = 0; j < kNt; ++j) {
-            codes32<T, kBits>(f[j], words[j], zs[j][0], zs[j][kZeros - 1]);
-            if (kFine) turn_blocks(f[j]);
-            s[j] = ss[j];
-        }
-        // this block has landed for all waves, and all are done with the one before
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    // Block b, the i4-th of four, from stage st; the block three on goes to `to`,
+    // which all waves were done with at this step's barrier (kVec; otherwise the one
+    // two on goes to the stage `before` that, and the one three on to registers).
+    auto step = [&](uint8_t* st, uint8_t* before, uint8_t* to, int b, int i4) {
+        // (this block's copies; behind them are the next two blocks' and, with a ring
+        // of codes, two blocks of those, an instruction or two a run)
+        if (kVec) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * kCopies + (kRing > 1 ? 2 * kNt : 0)) : "memory");
+        else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        load(b + 1);
-        copy(nx, b + 1);
+        frag_t f[kNt][4];
         if (!kFine) {
+            // A token tile's fragments are read while the one before is multiplied,
+            // and its products scaled while the next one is.
+            float s[kNt];
+            v8 xf[2][4];
+            float4v late[kNt];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) xf[0][e] = tokens(st, 0, e);
 #pragma unroll
             for (int i = 0; i < kMt; ++i) {
-                v8 xf[4];
+                if (i + 1 < kMt) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) xf[e] = tokens(st, i, e);
-#pragma unroll
-                for (int j = 0; j < kNt; ++j) {
-                    float4v p = {};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) p = Mat<T>::mfma16(xf[e], __builtin_bit_cast(v8, f[j][e]), p);
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(p[v], s[j], acc[i][j][v]);
+                    for (int e = 0; e < 4; ++e) xf[(i + 1) % 2][e] = tokens(st, i + 1, e);
                 }
+                float4v p[kNt];
+                if (i == 0) {
+                    // the codes become fragments beside the first products
+#pragma unroll
+                    for (int j = 0; j < kNt; ++j) {
+                        const int z = (int)from_row(zs[j][0], 4 * l16 + i4);
+                        s[j] = __builtin_bit_cast(float, from_row(ss[j], 4 * l16 + i4));
+                        codes32<T, kBits>(f[j], words[i4 % kRing][j], z, z);
+                        p[j] = (float4v){};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[j] = Mat<T>::mfma16(xf[0][e], __builtin_bit_cast(v8, f[j][e]), p[j]);
+                    }
+                } else {
+                    if (i == 1) {
+                        // (the codes first: they are waited for with the copies before these)
+                        load(b + kRing, i4 % kRing);
+                        if (i4 == 3) load_grids(b + 1);
+                        put(before);
+                        copy(to, b + 3);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int j = 0; j < kNt; ++j)
+                            p[j] = Mat<T>::mfma16(xf[i % 2][e], __builtin_bit_cast(v8, f[j][e]), e == 0 ? (float4v){} : p[j]);
+#pragma unroll
+                    for (int j = 0; j < kNt; ++j)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) acc[i - 1][j][v] = fmaf(late[j][v], s[j], acc[i - 1][j][v]);
+                }
+#pragma unroll
+                for (int j = 0; j < kNt; ++j) late[j] = p[j];
                 __builtin_amdgcn_sched_barrier(0);  // left alone, the scheduler reads every fragment first and spills
             }
+#pragma unroll
+            for (int j = 0; j < kNt; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[kMt - 1][j][v] = fmaf(late[j][v], s[j], acc[kMt - 1][j][v]);
         } else {
+#pragma unroll
+            for (int j = 0; j < kNt; ++j) {
+                codes32<T, kBits>(f[j], words[i4 % kRing][j], (int)from_row(zs[j][0], 4 * l16 + kg), (int)from_row(zs[j][kZeros - 1], 4 * l16 + kg));
+                turn_blocks(f[j]);
+            }
+            load(b + kRing, i4 % kRing);
+            load_grids(b + 1);
+            put(before);
+            copy(to, b + 3);
             // 32 columns at a time, or twice sixteen (the others as zeros)
             const bool halves = a.group % 32 != 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float sa[kNt], sb[kNt];
-                const uint32_t ga = 4 * group_of(a, (uint32_t)(b * kPmBlock + 32 * e)), gb = 4 * group_of(a, (uint32_t)(b * kPmBlock + 32 * e + 16));
+                const uint32_t k = (uint32_t)((b * kGroups + set) * kPmBlock + 32 * e), ga = 4 * group_of(a, k), gb = 4 * group_of(a, k + 16);
 #pragma unroll
                 for (int j = 0; j < kNt; ++j) {
-                    sa[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, so[j], ga, 0));
-                    sb[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, so[j], gb, 0));
+                    sa[j] = __builtin_bit_cast(float, from_row(__builtin_amdgcn_raw_buffer_load_b32(rs, so, ga + (uint32_t)j * s16, 0), 4 * l16));
+                    sb[j] = __builtin_bit_cast(float, from_row(__builtin_amdgcn_raw_buffer_load_b32(rs, so, gb + (uint32_t)j * s16, 0), 4 * l16));
                 }
 #pragma unroll
                 for (int i = 0; i < kMt; ++i) {
@@ -198,12 +253,30 @@ __global__ __launch_bounds__(kWT* kWR* kWave, kWT* kWR / 4 * kPerCu) void packed
         }
     };
     if (nb > 0) {
-        load(0);
+        // (in the order that the waits count on: the compiler may not move them past one another)
+        auto in_order = [] { asm volatile("" ::: "memory"); };
+        constexpr int kFirst = kRing > 1 ? kRing - 2 : 1;
+#pragma unroll
+        for (int b = 0; b < kFirst; ++b) load(b, b);
+        load_grids(0);
+        in_order();
         copy(lds0, 0);
-        for (int b = 0; b < nb; b += 2) {
-            step(lds0, lds1, b);
-            if (b + 1 == nb) break;
-            step(lds1, lds0, b + 1);
+        put(lds0);
+        in_order();
+        if (kRing > 1) load(kFirst, kFirst);
+        copy(lds1, 1);
+        put(lds1);
+        in_order();
+        if (kRing > 1) load(kFirst + 1, kFirst + 1);
+        copy(lds2, 2);
+        // Four steps without a branch between them (the compiler would move the
+        // scaling of products past it and keep them all in registers).  Blocks past
+        // the last have x of zeros.
+        for (int b = 0; b * kGroups < nb; b += 4) {
+            step(lds0, lds2, lds3, b, 0);
+            step(lds1, lds3, lds0, b + 1, 1);
+            step(lds2, lds0, lds1, b + 2, 2);
+            step(lds3, lds1, lds2, b + 3, 3);
         }
     }
     // copies still in flight would land in memory that the epilogue uses
@@ -211,12 +284,38 @@ __global__ __launch_bounds__(kWT* kWR* kWave, kWT* kWR / 4 * kPerCu) void packed
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 
+    if (kGroups > 1) {
+        // the groups' sums, added in group order
+        constexpr int kOne = kWaves * kMt * kNt * 4 * kWave;
+        static_assert(4 * (kGroups - 1) * kOne <= kGroups * kBytes, "the sums in a stage");
+        float* sums = reinterpret_cast<float*>(lds2);
+        auto at = [&](int g, int i, int j, int v) -> float& { return sums[(g - 1) * kOne + (((w * kMt + i) * kNt + j) * 4 + v) * kWave + lane]; };
+        if (set > 0) {
+#pragma unroll
+            for (int i = 0; i < kMt; ++i)
+#pragma unroll
+                for (int j = 0; j < kNt; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) at(set, i, j, v) = acc[i][j][v];
+        }
+        __syncthreads();
+        if (set > 0) return;
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g)
+#pragma unroll
+            for (int i = 0; i < kMt; ++i)
+#pragma unroll
+                for (int j = 0; j < kNt; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[i][j][v] += at(g, i, j, v);
+    }
     // A lane holds four tokens of one weight row.  A wave turns sixteen tokens at
     // a time in LDS of its own; then a lane has eight neighbouring rows of a token.
     constexpr int kRun = 16 * kNt, kPitch = kRun + 4;
-    static_assert(kWaves * 16 * kPitch * 4 <= kBytes, "the lines of every wave");
-    float* lines = reinterpret_cast<float*>(lds0) + w * 16 * kPitch;
-    const int64_t o0 = r0 + wr * kRun;
+    constexpr int kHalf = kWaves / 2;
+    static_assert(kHalf * 16 * kPitch * 4 <= kGroups * kBytes, "the lines of every wave");
+    float* lines = reinterpret_cast<float*>(w < kHalf ? lds0 : lds1) + w % kHalf * 16 * kPitch;
+    const int64_t o0 = r0 + w * kRun;
 #pragma unroll
     for (int i = 0; i < kMt; ++i) {
 #pragma unroll
@@ -225,55 +324,32 @@ __global__ __launch_bounds__(kWT* kWR* kWave, kWT* kWR / 4 * kPerCu) void packed
             for (int v = 0; v < 4; ++v) lines[(4 * kg + v) * kPitch + 16 * j + l16] = acc[i][j][v];
         __builtin_amdgcn_wave_barrier();
         for (int q = lane; q < 2 * kRun; q += kWave) {
-            const int line = q / (kRun / 8), at = q % (kRun / 8) * 8;
-            const int64_t t = t0 + (wt * kMt + i) * 16 + line, o = o0 + at, left = c.M - o;
-            if (t >= c.n || left <= 0) continue;
-            float y[8], e[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = lines[line * kPitch + at + k];
-            if (c.bias) {
-                if (a.y32) load8<float, false>(e, static_cast<const float*>(c.bias) + o, left);
-                else load8<T, false>(e, static_cast<const T*>(c.bias) + o, left);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] += e[k];
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = activated(y[k], c.activation);
-            if (c.residual) {
-                if (a.y32) load8<float, false>(e, static_cast<const float*>(c.residual) + t * c.ldr + o, left);
-                else load8<T, false>(e, static_cast<const T*>(c.residual) + t * c.ldr + o, left);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] += e[k];
-            }
-            if (a.y32) store8<float, false>(static_cast<float*>(c.y) + t * c.ldy + o, y, left);
-            else store8<T, false>(static_cast<T*>(c.y) + t * c.ldy + o, y, left);
+            pm_finish<T>(a, lines + q / (kRun / 8) * kPitch + q % (kRun / 8) * 8, t0 + 16 * i + q / (kRun / 8), o0 + q % (kRun / 8) * 8);
         }
         __builtin_amdgcn_wave_barrier();
     }
 }
 
-template <typename T, int kBits, bool kFine, bool kVec, int kTT, int kTR, int kWT, int kWR, int kPerCu>
+template <typename T, int kBits, bool kFine, bool kVec, int kTT, int kTR, int kWaves, int kPerCu, int kRing, int kGroups>
 hipError_t tile_go(PmArgs a, hipStream_t s) {
     const TimedLaunch t(K_PACKED_MATMUL, s);
     a.mt = (unsigned)((a.c.M + kTR - 1) / kTR);
     a.nt = (unsigned)((a.c.n + kTT - 1) / kTT);
-    GPTQ_LAUNCH(t, (packed_tile_kernel<T, kBits, kFine, kVec, kTT, kTR, kWT, kWR, kPerCu>), dim3(a.mt * a.nt), dim3(kWT * kWR * kWave), 0, s, a);
+    GPTQ_LAUNCH(t, (packed_tile_kernel<T, kBits, kFine, kVec, kTT, kTR, kWaves, kPerCu, kRing, kGroups>), dim3(a.mt * a.nt), dim3(kGroups * kWaves * kWave), 0, s, a);
     return hipGetLastError();
 }
 
 }  // namespace
 
 template <typename T, int kBits>
-hipError_t launch_packed_tile(const PmArgs& a, bool fine, hipStream_t s) {
-    const bool vec = a.c.K % 8 == 0 && a.c.ldx % 8 == 0 && reinterpret_cast<uintptr_t>(a.c.x) % 16 == 0;
-    if (fine) return vec ? tile_go<T, kBits, true, true, 128, 128, 2, 2, 2>(a, s) : tile_go<T, kBits, true, false, 128, 128, 2, 2, 2>(a, s);
-    if (!vec) return tile_go<T, kBits, false, false, 128, 128, 2, 2, 2>(a, s);
-    const int64_t big = ((a.c.M + 255) / 256) * ((a.c.n + 255) / 256), mid = ((a.c.M + 127) / 128) * ((a.c.n + 127) / 128);
-    const int64_t cus = device_cu_count();
-    if (cus <= 0) return hipErrorInvalidDevice;
-    if (big >= cus) return tile_go<T, kBits, false, true, 256, 256, 2, 4, 1>(a, s);
-    if (mid >= cus) return tile_go<T, kBits, false, true, 128, 128, 2, 2, 2>(a, s);
-    return tile_go<T, kBits, false, true, 64, 64, 2, 2, 2>(a, s);
+hipError_t launch_packed_tile(const PmArgs& a, int kernel, bool fine, hipStream_t s) {
+    if (kernel == kPm32x64)
+        return a.vec ? (fine ? tile_go<T, kBits, true, true, 32, 64, 4, 1, 1, 4>(a, s) : tile_go<T, kBits, false, true, 32, 64, 4, 1, 4, 4>(a, s))
+                     : (fine ? tile_go<T, kBits, true, false, 64, 128, 4, 2, 1, 1>(a, s) : tile_go<T, kBits, false, false, 32, 64, 4, 1, 1, 4>(a, s));
+    if (!a.vec) return fine ? tile_go<T, kBits, true, false, 64, 128, 4, 2, 1, 1>(a, s) : tile_go<T, kBits, false, false, 64, 128, 4, 2, 1, 1>(a, s);
+    if (fine) return tile_go<T, kBits, true, true, 64, 128, 4, 2, 4, 1>(a, s);
+    if (kernel == kPm64x128) return tile_go<T, kBits, false, true, 64, 128, 4, 2, 4, 1>(a, s);
+    return tile_go<T, kBits, false, true, 128, 384, 8, 1, 1, 1>(a, s);
 }
 
 }  // namespace gptq
