@@ -194,6 +194,28 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
 #pragma unroll
             for (int i = 0; i < kDp / 32; ++i) acc[i] *= keep;
         }
+        if (kMasked) {
+            // The infinities and NaN of values, times their weights, where the row sees
+            // the key.  Below they count as zeros: a weight of zero would make NaN of them.
+            for (uint64_t left = odd; left; left &= left - 1) {
+                const int key = __builtin_ctzll(left), at = key / 32 * 16 + key % 32 / 8 * 4 + key % 4;
+                float mine = 0.0f;
+#pragma unroll
+                for (int v = 0; v < 32; ++v) mine = v == at ? s[v / 16][v % 16] : mine;
+                const float weight = exp2_fast(fmaf(__shfl(mine, l32 + key / 4 % 2 * 32, kWave), a.c2, off));
+                const bool seen = k0 + key < limit;
+                const uint8_t* row = st + (kTile + key * 2 * kDp + 8 * kg);
+#pragma unroll
+                for (int i = 0; i < kDp / 32; ++i)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const v4 x = *reinterpret_cast<const v4*>(row + 16 * value_place<kDp>(key, 4 * i + g));
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            if (seen && !__builtin_isfinite(to_f32(x[v]))) acc[i][4 * g + v] = fmaf(weight, to_f32(x[v]), acc[i][4 * g + v]);
+                    }
+            }
+        }
 #pragma unroll
         for (int j = 0; j < kTileKeys / 16; ++j) {
             v8 p;
@@ -215,7 +237,6 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
                 for (int g = 0; g < 2; ++g)
                     vf.h[g] = read_turned<T>(st + (kTile + (row + 8 * g) * 2 * kDp + 16 * value_place<kDp>(row + 8 * g, chunk) + 8 * (l16 % 2)));
                 if (kMasked && odd) {
-                    // a weight of zero would make NaN of them; they are added below
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const uint32_t lo = (vf.u[g] & kExponent) == kExponent ? 0u : vf.u[g] & 0xFFFFu;
@@ -226,40 +247,30 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
                 acc[i] = Mat<T>::mfma32(vf.v, p, acc[i]);
             }
         }
-        if (kMasked && odd) {
-            // the infinities and NaN of keys that the row sees, times their weights
-            for (; odd; odd &= odd - 1) {
-                const int key = __builtin_ctzll(odd), at = key / 32 * 16 + key % 32 / 8 * 4 + key % 4;
-                float mine = 0.0f;
-#pragma unroll
-                for (int v = 0; v < 32; ++v) mine = v == at ? s[v / 16][v % 16] : mine;
-                const float weight = exp2_fast(fmaf(__shfl(mine, l32 + key / 4 % 2 * 32, kWave), a.c2, off));
-                const bool seen = k0 + key < limit;
-#pragma unroll
-                for (int i = 0; i < kDp / 32; ++i)
-#pragma unroll
-                    for (int v = 0; v < 16; ++v) {
-                        const int d = 32 * i + acc32_row(v, lane);
-                        const float x = to_f32(*reinterpret_cast<const T*>(st + (kTile + key * 2 * kDp + 16 * value_place<kDp>(key, d / 8) + d % 8 * 2)));
-                        if (seen && !__builtin_isfinite(x)) acc[i][v] = fmaf(weight, x, acc[i][v]);
-                    }
-            }
-        }
     };
-    auto step = [&](uint8_t* st, uint8_t* nx, int i) {
+    auto step = [&](uint8_t* st, uint8_t* nx, int i, auto masked) {
         // this tile has landed for all waves, and all are done with the one before
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if (i + 1 < tiles) copy(nx, i + 1);
-        if (i < full) compute(st, i * kTileKeys, Plain{});
-        else if (i * kTileKeys < wave_last) compute(st, i * kTileKeys, Masked{});
+        if (!decltype(masked)::value || i * kTileKeys < wave_last) compute(st, i * kTileKeys, masked);
     };
     copy(lds0, 0);
-    for (int i = 0; i < tiles; i += 2) {
-        step(lds0, lds1, i);
+    // (a loop for each kind of tile: in one loop they would hold their addresses at the same time, and spill)
+    int i = 0;
+    for (; i + 2 <= full; i += 2) {
+        step(lds0, lds1, i, Plain{});
+        step(lds1, lds0, i + 1, Plain{});
+    }
+    if (i < full) {
+        step(lds0, lds1, i, Plain{});
+        if (++i < tiles) step(lds1, lds0, i++, Masked{});
+    }
+    for (; i < tiles; i += 2) {
+        step(lds0, lds1, i, Masked{});
         if (i + 1 == tiles) break;
-        step(lds1, lds0, i + 1);
+        step(lds1, lds0, i + 1, Masked{});
     }
 
     l = add_halves(l);
