@@ -52,7 +52,7 @@ __device__ __forceinline__ int64_t sequence_of(const AttArgs& a, int64_t tile) {
     int64_t lo = 0, range = a.c.n_seqs;
     for (;;) {
         const int64_t stride = (range + kWave - 1) / kWave, s = lo + lane * stride;
-        const bool below = s < lo + range && start_of(a, s) / a.tokens + s <= tile;
+        const bool below = s < lo + range && (uint32_t)start_of(a, s) / (uint32_t)a.tokens + s <= tile;
         const int count = __builtin_popcountll(__ballot(below));
         lo += max(count - 1, 0) * stride;
         if (stride == 1) return lo;
@@ -60,8 +60,12 @@ __device__ __forceinline__ int64_t sequence_of(const AttArgs& a, int64_t tile) {
     }
 }
 
-__device__ __forceinline__ bool finite_pair(uint32_t two, uint32_t exponent) {
-    return (two & exponent) != exponent && (two >> 16 & exponent) != exponent;
+// Bits 15 and 31: whether the two 16-bit values of a word are infinite or NaN, that is,
+// have an exponent of ones, which the addition carries out of.
+template <typename T>
+__device__ __forceinline__ uint32_t odd_pair(uint32_t two) {
+    constexpr uint32_t kExponent = __is_same(T, half_t) ? 0x7C007C00u : 0x7F807F80u, kOne = __is_same(T, half_t) ? 0x04000400u : 0x00800080u;
+    return (two & kExponent) + kOne;
 }
 
 struct Plain {
@@ -77,7 +81,6 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
     constexpr int kCopies = kTileKeys / kRowsEach / kWaves;        // instructions a wave, keys or values
     constexpr int kTile = kTileKeys * kDp * 2;                     // bytes
     static_assert(kTileKeys % (kRowsEach * kWaves) == 0, "whole copies");
-    constexpr uint32_t kExponent = sizeof(T) == 2 && __is_same(T, half_t) ? 0x7C00u : 0x7F80u;
     // separate arrays: the compiler then knows that a read of one does not wait for copies into another
     __shared__ __align__(16) uint8_t lds0[2 * kTile];
     __shared__ __align__(16) uint8_t lds1[2 * kTile];
@@ -93,7 +96,7 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
     const int64_t seq = sequence_of(a, tile);
     const int64_t first = start_of(a, seq);
     const int64_t len = start_of(a, seq + 1) - first;
-    const int64_t t0 = (tile - (first / a.tokens + seq)) * a.tokens;  // within the sequence
+    const int64_t t0 = (tile - ((uint32_t)first / (uint32_t)a.tokens + seq)) * a.tokens;  // within the sequence
     if (t0 < 0 || t0 >= len) return;
     const int64_t hk = unit / a.head_groups;
     const int group = (int)(c.heads / c.kv_heads);
@@ -110,14 +113,6 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
     const int full = (int)((kCausal ? min(t0 + 1, len) : len) / kTileKeys);  // tiles that every row sees whole
     const int tiles = (keys_end + kTileKeys - 1) / kTileKeys;
 
-    v8 qf[kDp / 16];
-#pragma unroll
-    for (int e = 0; e < kDp / 16; ++e) {
-        qf[e] = (v8){};
-        const int at = 16 * e + 8 * kg;
-        if (live && at < c.d)
-            qf[e] = *reinterpret_cast<const v8*>(static_cast<const T*>(c.q) + (first + token) * c.ldq[0] + (h0 + head) * c.ldq[1] + at);
-    }
     const T* keys = static_cast<const T*>(c.k) + first * c.ldk[0] + hk * c.ldk[1];
     const T* values = static_cast<const T*>(c.v) + first * c.ldv[0] + hk * c.ldv[1];
 
@@ -138,10 +133,20 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
         const __amdgpu_buffer_rsrc_t rv = att_rsrc(values + k0 * c.ldv[0], (uint32_t)(left * c.ldv[0] * 2));
 #pragma unroll
         for (int e = 0; e < kCopies; ++e) {
-            copy16(rk, st + 1024 * (kCopies * w + e), ko[e]);
+            copy16(rk, st + (1024 * (kCopies * w + e)), ko[e]);
             copy16(rv, st + (kTile + 1024 * (kCopies * w + e)), vo[e]);
         }
     };
+
+    copy(lds0, 0);
+    // (every lane loads, from a row that is there: under a condition each load would
+    // be waited for before the next)
+    const T* qrow = static_cast<const T*>(c.q) + (first + min(token, len - 1)) * c.ldq[0] + (h0 + min(head, rows - 1)) * c.ldq[1];
+    v8 qf[kDp / 16];
+#pragma unroll
+    for (int e = 0; e < kDp / 16; ++e) qf[e] = *reinterpret_cast<const v8*>(qrow + (16 * e + 8 * kg < c.d ? 16 * e + 8 * kg : 0));
+#pragma unroll
+    for (int e = 0; e < kDp / 16; ++e) qf[e] = (live & (16 * e + 8 * kg < c.d)) ? qf[e] : (v8){};
 
     float16v acc[kDp / 32];
 #pragma unroll
@@ -167,13 +172,13 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) s[t][v] = k0 + 32 * t + acc32_row(v, lane) < limit ? s[t][v] : -__builtin_inff();
-            bool fine = true;
+            uint32_t bad = 0;
 #pragma unroll
             for (int e = 0; e < kChunks; ++e) {
                 const uint4v x = *reinterpret_cast<const uint4v*>(st + (kTile + lane * 2 * kDp + 16 * e));
-                fine = fine && finite_pair(x.x, kExponent) && finite_pair(x.y, kExponent) && finite_pair(x.z, kExponent) && finite_pair(x.w, kExponent);
+                bad |= odd_pair<T>(x.x) | odd_pair<T>(x.y) | odd_pair<T>(x.z) | odd_pair<T>(x.w);
             }
-            odd = __ballot(!fine);
+            odd = __ballot((bad & 0x80008000u) != 0);
         }
         float top = s[0][0];
 #pragma unroll
@@ -211,8 +216,10 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
                     for (int g = 0; g < 4; ++g) {
                         const v4 x = *reinterpret_cast<const v4*>(row + 16 * value_place<kDp>(key, 4 * i + g));
 #pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            if (seen && !__builtin_isfinite(to_f32(x[v]))) acc[i][4 * g + v] = fmaf(weight, to_f32(x[v]), acc[i][4 * g + v]);
+                        for (int v = 0; v < 4; ++v) {
+                            const float y = fmaf(weight, to_f32(x[v]), acc[i][4 * g + v]);
+                            acc[i][4 * g + v] = (seen & !__builtin_isfinite(to_f32(x[v]))) ? y : acc[i][4 * g + v];
+                        }
                     }
             }
         }
@@ -238,11 +245,7 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
                     vf.h[g] = read_turned<T>(st + (kTile + (row + 8 * g) * 2 * kDp + 16 * value_place<kDp>(row + 8 * g, chunk) + 8 * (l16 % 2)));
                 if (kMasked && odd) {
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const uint32_t lo = (vf.u[g] & kExponent) == kExponent ? 0u : vf.u[g] & 0xFFFFu;
-                        const uint32_t hi = (vf.u[g] >> 16 & kExponent) == kExponent ? 0u : vf.u[g] & 0xFFFF0000u;
-                        vf.u[g] = lo | hi;
-                    }
+                    for (int g = 0; g < 4; ++g) vf.u[g] &= ~((odd_pair<T>(vf.u[g]) >> 15 & 0x10001u) * 0xFFFFu);
                 }
                 acc[i] = Mat<T>::mfma32(vf.v, p, acc[i]);
             }
@@ -256,7 +259,6 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
         if (i + 1 < tiles) copy(nx, i + 1);
         if (!decltype(masked)::value || i * kTileKeys < wave_last) compute(st, i * kTileKeys, masked);
     };
-    copy(lds0, 0);
     // (a loop for each kind of tile: in one loop they would hold their addresses at the same time, and spill)
     int i = 0;
     for (; i + 2 <= full; i += 2) {
@@ -309,12 +311,11 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
 template <typename T, int kDp>
 hipError_t attention_go(AttArgs a, hipStream_t s) {
     constexpr int kWaves = 4;
-    const AttentionCall& c = a.c;
     a.tokens = 32 * kWaves / a.rows;
-    a.tiles = (unsigned)(c.n / a.tokens + c.n_seqs);
+    a.tiles = (unsigned)(a.c.n / a.tokens + a.c.n_seqs);
     const dim3 grid(a.tiles * a.units), block(kWaves * kWave);
     const TimedLaunch t(K_ATTENTION, s);
-    if (c.causal) GPTQ_LAUNCH(t, (attention_kernel<T, kDp, kWaves, true>), grid, block, 0, s, a);
+    if (a.c.causal) GPTQ_LAUNCH(t, (attention_kernel<T, kDp, kWaves, true>), grid, block, 0, s, a);
     else GPTQ_LAUNCH(t, (attention_kernel<T, kDp, kWaves, false>), grid, block, 0, s, a);
     return hipGetLastError();
 }

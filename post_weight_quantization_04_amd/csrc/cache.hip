@@ -181,14 +181,14 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void cached_kernel(CachedArgs a) 
         const bool whole = step == 0 && last == steps;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (step == 0);
 
+        // (every lane loads, from a row that is there: under a condition each load would
+        // be waited for before the next)
+        const T* qrow = static_cast<const T*>(c.q) + b * c.ldq[0] + (h0 + min(l16, rows - 1)) * c.ldq[1];
         v8 qf[kDp / 32];
 #pragma unroll
-        for (int s = 0; s < kDp / 32; ++s) {
-            qf[s] = (v8){};
-            const int e = 32 * s + 8 * kg;
-            if (l16 < rows && e < c.d)
-                qf[s] = *reinterpret_cast<const v8*>(static_cast<const T*>(c.q) + b * c.ldq[0] + (h0 + l16) * c.ldq[1] + e);
-        }
+        for (int s = 0; s < kDp / 32; ++s) qf[s] = *reinterpret_cast<const v8*>(qrow + (32 * s + 8 * kg < c.d ? 32 * s + 8 * kg : 0));
+#pragma unroll
+        for (int s = 0; s < kDp / 32; ++s) qf[s] = ((l16 < rows) & (32 * s + 8 * kg < c.d)) ? qf[s] : (v8){};
         const T* keys = static_cast<const T*>(c.cache.keys) + hk * c.cache.ldk[1];
         const T* values = static_cast<const T*>(c.cache.values) + hk * c.cache.ldv[1];
         const int32_t* table = c.table + b * c.ldt;
