@@ -50,6 +50,7 @@ struct CachedArgs {
     uint32_t page_mul, page_shift;  // division by the page size
     float c2;          // scale log2 e
     float* parts;
+    int64_t workers;   // at most
 };
 
 __device__ const uint32_t kZeroRow[64] = {};  // 256 bytes: what keys that are none are read from
@@ -63,6 +64,10 @@ __device__ __forceinline__ uint32_t cached_length(const CachedArgs& a, int64_t b
     const int64_t n = a.c.lengths[b];
     return (uint32_t)min(max(n, (int64_t)0), a.c.max_pages * a.c.cache.page_size);
 }
+
+// Workgroups among which `all` steps are shared: two steps each at least, since a part
+// costs the join about as much.
+__device__ __forceinline__ int64_t cached_workers(int64_t most, int64_t all) { return min(most, (all + 1) / 2); }
 
 // Inclusive sum over the lanes of a wave.
 __device__ __forceinline__ int64_t wave_scan(int64_t v) {
@@ -81,17 +86,29 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
     return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
-// Steps of all sequences (of one unit each), and those before sequence `upto`.
-__device__ __forceinline__ void count_steps(const CachedArgs& a, uint32_t per, int64_t upto, int64_t& all, int64_t& before) {
+// Steps of all sequences, of one unit each.
+__device__ __forceinline__ int64_t count_steps(const CachedArgs& a, uint32_t per) {
+    int64_t sum = 0;
+    for (int64_t b = threadIdx.x % kWave; b < a.c.n_seqs; b += kWave) sum += (cached_length(a, b) + (uint64_t)per - 1) / per;
+    return uniform64(__shfl(wave_scan(sum), kWave - 1, kWave));
+}
+
+// The sequence b that holds step `at` < all, and the steps `before` it (a unit's).
+__device__ __forceinline__ void find_step(const CachedArgs& a, uint32_t per, int64_t units, int64_t at, int64_t& b, int64_t& before) {
     const int lane = threadIdx.x % kWave;
-    int64_t sum = 0, part = 0;
-    for (int64_t b = lane; b < a.c.n_seqs; b += kWave) {
-        const int64_t steps = (cached_length(a, b) + (uint64_t)per - 1) / per;
-        sum += steps;
-        part += b < upto ? steps : 0;
+    before = 0;
+    for (b = 0;; b += kWave) {
+        const int64_t mine = b + lane < a.c.n_seqs ? (cached_length(a, b + lane) + (uint64_t)per - 1) / per : 0;
+        const int64_t sum = wave_scan(mine);
+        const uint64_t past = __ballot((before + sum) * units > at);
+        if (past) {
+            const int in = __builtin_ctzll(past);
+            before += uniform64(__shfl(sum - mine, in, kWave));
+            b += in;
+            return;
+        }
+        before += uniform64(__shfl(sum, kWave - 1, kWave));
     }
-    all = uniform64(__shfl(wave_scan(sum), kWave - 1, kWave));
-    before = uniform64(__shfl(wave_scan(part), kWave - 1, kWave));
 }
 
 // Memory to LDS without registers in between, a wave's lanes one behind the
@@ -132,28 +149,13 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void cached_kernel(CachedArgs a) 
 
     int64_t b, unit, step, left;  // the first unit, the step in it, and how many steps are this workgroup's
     if (kSplit) {
-        int64_t all, none;
-        count_steps(a, kStep, 0, all, none);
-        all *= units;
-        const int64_t workers = min((int64_t)gridDim.x, all);  // none without a step
+        const int64_t all = count_steps(a, kStep) * units;
+        const int64_t workers = cached_workers(a.workers, all);
         if (blockIdx.x >= workers) return;
         const int64_t from = (int64_t)blockIdx.x * all / workers, to = ((int64_t)blockIdx.x + 1) * all / workers;
         left = to - from;
-        // the sequence that holds step `from`
-        int64_t before = 0;
-        b = 0;
-        for (;; b += kWave) {
-            const int64_t mine = b + lane < c.n_seqs ? (cached_length(a, b + lane) + (uint64_t)kStep - 1) / kStep : 0;
-            const int64_t sum = wave_scan(mine);
-            const uint64_t past = __ballot((before + sum) * units > from);
-            if (past) {
-                const int at = __builtin_ctzll(past);
-                before += uniform64(__shfl(sum - mine, at, kWave));
-                b += at;
-                break;
-            }
-            before += uniform64(__shfl(sum, kWave - 1, kWave));
-        }
+        int64_t before;
+        find_step(a, kStep, units, from, b, before);
         const int64_t steps = (cached_length(a, b) + (uint64_t)kStep - 1) / kStep;
         unit = (from - before * units) / steps;
         step = (from - before * units) % steps;
@@ -372,105 +374,120 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void cached_kernel(CachedArgs a) 
     }
 }
 
-// Adds the parts of a unit that several workgroups computed; zeros for a sequence
-// without tokens.  One workgroup a unit; the parts' factors go through LDS, 64
-// parts at a time.
+// Adds the parts of the units that several workgroups computed, each unit in the
+// workgroup that has the number of the second of them: no more workgroups than there
+// were, however many units.  Threads of eight outputs each, in groups that take turns
+// with the parts, and the groups' results added in their order.  (One thread for all
+// parts of its outputs, one workgroup a unit: 313 parts in 45 us; these 9.)  Zeros for
+// sequences without tokens besides.
+constexpr int kJoinThreads = 1024;
 template <typename T, int kDp>
-__global__ __launch_bounds__(256) void cached_join_kernel(CachedArgs a, uint32_t per_step, int64_t workers) {
+__global__ __launch_bounds__(kJoinThreads) void cached_join_kernel(CachedArgs a, uint32_t per_step) {
     typedef typename Mat<T>::v8 v8;
-    constexpr int kChunks = kDp / 8, kMany = 64;
-    __shared__ float tops[kMany][16], sums[kMany][16];
+    constexpr int kChunks = kDp / 8;
+    __shared__ __align__(16) float held[kJoinThreads][8];
+    __shared__ float tops[kJoinThreads], sums[kJoinThreads];
     const CachedAttentionCall& c = a.c;
-    const int64_t units = c.kv_heads * a.head_groups, b = blockIdx.x / units, unit = blockIdx.x % units;
+    for (int64_t b = blockIdx.x; b < c.n_seqs; b += gridDim.x) {
+        if (cached_length(a, b)) continue;
+        const int chunks = (int)c.d / 8;
+        for (int64_t i = threadIdx.x; i < c.heads * chunks; i += kJoinThreads)
+            *reinterpret_cast<v8*>(static_cast<T*>(c.out) + b * c.ldo[0] + i / chunks * c.ldo[1] + i % chunks * 8) = (v8){};
+    }
+    const int64_t units = c.kv_heads * a.head_groups;
     const int group = (int)(c.heads / c.kv_heads);
+    const int64_t all = count_steps(a, per_step) * units;
+    const int64_t workers = cached_workers(a.workers, all), here = blockIdx.x;
+    if (here == 0 || here >= workers) return;
+    const int64_t at = here * all / workers;
+    int64_t b, before;
+    find_step(a, per_step, units, at, b, before);
+    const int64_t steps = (cached_length(a, b) + (uint64_t)per_step - 1) / per_step;
+    const int64_t unit = (at - before * units) / steps, from = before * units + unit * steps;
+    auto worker = [&](int64_t step) { return ((step + 1) * workers - 1) / all; };
+    // the first worker's part begins with the unit, the others' inside it
+    const int64_t first = worker(from), last = worker(from + steps - 1);
+    if (first + 1 != here) return;
     const int64_t hk = unit / a.head_groups;
     const int h0 = (int)(hk * group + unit % a.head_groups * 16);
     const int rows = min(a.rows, (int)((hk + 1) * group) - h0);
-    int64_t all, before;
-    count_steps(a, per_step, b, all, before);
-    all *= units;
-    workers = min(workers, all);
-    const int64_t steps = (cached_length(a, b) + (uint64_t)per_step - 1) / per_step;
-    int64_t first = 0, last = -1;
-    if (steps > 0) {
-        const int64_t from = before * units + unit * steps;
-        auto worker = [&](int64_t at) { return ((at + 1) * workers - 1) / all; };
-        first = worker(from);
-        last = worker(from + steps - 1);
-        if (first == last) return;  // written already
-        // the first worker's part begins with the unit, the others' inside it
-    }
-    const int r = threadIdx.x / kChunks, e = threadIdx.x % kChunks * 8;  // kDp = 64: rows to 32, the upper half idle
+    const int tid = threadIdx.x, per = rows * kChunks, groups = kJoinThreads / per, g = tid / per;
+    const int r = tid % per / kChunks, e = tid % per % kChunks * 8;
     float top = kLowest, sum = 0.0f, y[8] = {};
-    for (int64_t w0 = first; w0 <= last; w0 += kMany) {
-        const int many = (int)min((int64_t)kMany, last - w0 + 1);
-        auto part_of = [&](int i) { return a.parts + (2 * (w0 + i) + (w0 + i == first)) * (a.rows * (kDp + 2)); };
-        __syncthreads();
-        for (int id = threadIdx.x; id < many * 16; id += 256) {
-            const int i = id / 16, q = id % 16;
-            if (q < rows) {
-                tops[i][q] = part_of(i)[a.rows * kDp + q];
-                sums[i][q] = part_of(i)[a.rows * (kDp + 1) + q];
-            }
-        }
-        __syncthreads();
-        if (r < rows) {
-            float now = top;
-            for (int i = 0; i < many; ++i) now = fmaxf(now, tops[i][r]);
-            const float keep = exp2_fast((top - now) * a.c2);
-            sum *= keep;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] *= keep;
+    if (g < groups) {
+#pragma unroll 2
+        for (int64_t w = first + g; w <= last; w += groups) {
+            const float* p = a.parts + (2 * w + (w == first)) * (a.rows * (kDp + 2));
+            const float4v lo = *reinterpret_cast<const float4v*>(p + r * kDp + e), hi = *reinterpret_cast<const float4v*>(p + r * kDp + e + 4);
+            const float pt = p[a.rows * kDp + r], ps = p[a.rows * (kDp + 1) + r];
+            const float now = fmaxf(top, pt), fa = exp2_fast((top - now) * a.c2), fb = exp2_fast((pt - now) * a.c2);
             top = now;
-#pragma unroll 4
-            for (int i = 0; i < many; ++i) {
-                const float f = exp2_fast((tops[i][r] - now) * a.c2);
-                sum = fmaf(sums[i][r], f, sum);
-                const float* p = part_of(i) + (r * kDp + e);
+            sum = sum * fa + ps * fb;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float4v v = *reinterpret_cast<const float4v*>(p + 4 * j);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) y[4 * j + k] = fmaf(v[k], f, y[4 * j + k]);
-                }
+            for (int k = 0; k < 4; ++k) {
+                y[k] = y[k] * fa + lo[k] * fb;
+                y[4 + k] = y[4 + k] * fa + hi[k] * fb;
             }
         }
     }
-    if (r < rows && e < c.d) {
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        v8 out;
+    tops[tid] = top;
+    sums[tid] = sum;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) out[k] = (T)(y[k] * inv);
-        *reinterpret_cast<v8*>(static_cast<T*>(c.out) + b * c.ldo[0] + (h0 + r) * c.ldo[1] + e) = out;
+    for (int k = 0; k < 8; ++k) held[tid][k] = y[k];
+    __syncthreads();
+    if (g > 0 || e >= c.d) return;
+    float now = top;
+    for (int i = 1; i < groups; ++i) now = fmaxf(now, tops[i * per + tid]);
+    float f = exp2_fast((top - now) * a.c2);
+    sum *= f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] *= f;
+    for (int i = 1; i < groups; ++i) {
+        f = exp2_fast((tops[i * per + tid] - now) * a.c2);
+        sum = fmaf(sums[i * per + tid], f, sum);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = fmaf(held[i * per + tid][k], f, y[k]);
     }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    v8 out;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) out[k] = (T)(y[k] * inv);
+    *reinterpret_cast<v8*>(static_cast<T*>(c.out) + b * c.ldo[0] + (h0 + r) * c.ldo[1] + e) = out;
 }
 
-constexpr int64_t kCachedWorkers = 1024;  // at most
-constexpr int kCachedWaves = 4;
+constexpr int64_t kCachedWorkers = 256;   // at most; one a CU
 constexpr int64_t kCachedWhole = 1024;    // tokens up to which a unit is one workgroup's
 
 inline int padded_head(int64_t d) { return d <= 64 ? 64 : 128; }
 inline int64_t unit_rows(int64_t heads, int64_t kv_heads) { return std::min(heads / kv_heads, kHeadRows); }
 
+template <typename T, int kDp, int kWaves>
+hipError_t cached_whole(const CachedArgs& a, int64_t units, hipStream_t s) {
+    const TimedLaunch t(K_CACHED_ATTENTION, s);
+    GPTQ_LAUNCH(t, (cached_kernel<T, kDp, kWaves, false>), dim3((unsigned)units), dim3(kWaves * kWave), 0, s, a);
+    return hipGetLastError();
+}
+
+// Short tables: a unit is one workgroup's, of eight waves where each has a CU to itself
+// (333 tokens of 8 key heads 8.4 us, 9.3 with four; 900 tokens 13.4 and 16.4), of four
+// otherwise (64 sequences of 500 tokens 24.6 us, 28.8 with eight).  Longer ones: one
+// workgroup of eight waves a CU, whose copies in flight keep memory busy (131072 tokens
+// 105 us, 5.1 TB/s, two of four waves 108; 16 x 3000 tokens of 16 heads of 64 40 us, 50).
 template <typename T, int kDp>
 hipError_t cached_go(CachedArgs a, hipStream_t s) {
     const CachedAttentionCall& c = a.c;
     const int64_t units = c.n_seqs * c.kv_heads * a.head_groups, most = c.max_pages * c.cache.page_size;
-    const dim3 block(kCachedWaves * kWave);
-    const TimedLaunch t(K_CACHED_ATTENTION, s);
-    if (most <= kCachedWhole) {
-        GPTQ_LAUNCH(t, (cached_kernel<T, kDp, kCachedWaves, false>), dim3((unsigned)units), block, 0, s, a);
-        return hipGetLastError();
-    }
     const int cus = device_cu_count();
     if (cus <= 0) return hipErrorInvalidDevice;
-    constexpr int kStep = kCachedWaves * 4 * kWave / (kDp / 8);
-    const int64_t workers = std::min({kCachedWorkers, (int64_t)2 * cus, units * ((most + kStep - 1) / kStep)});
-    GPTQ_LAUNCH(t, (cached_kernel<T, kDp, kCachedWaves, true>), dim3((unsigned)workers), block, 0, s, a);
+    if (most <= kCachedWhole) return units <= cus ? cached_whole<T, kDp, 8>(a, units, s) : cached_whole<T, kDp, 4>(a, units, s);
+    constexpr int kWaves = 8, kStep = kWaves * 4 * kWave / (kDp / 8);
+    a.workers = std::min({kCachedWorkers, (int64_t)cus, units * ((most + kStep - 1) / kStep)});
+    const TimedLaunch t(K_CACHED_ATTENTION, s);
+    GPTQ_LAUNCH(t, (cached_kernel<T, kDp, kWaves, true>), dim3((unsigned)a.workers), dim3(kWaves * kWave), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const TimedLaunch j(K_CACHED_JOIN, s);
-    GPTQ_LAUNCH(j, (cached_join_kernel<T, kDp>), dim3((unsigned)units), dim3(256), 0, s, a, (uint32_t)kStep, workers);
+    GPTQ_LAUNCH(j, (cached_join_kernel<T, kDp>), dim3((unsigned)a.workers), dim3(kJoinThreads), 0, s, a, (uint32_t)kStep);
     return hipGetLastError();
 }
 
