@@ -582,18 +582,27 @@ const char* gptq_fp8_gated_kernel(int64_t d_ff, int64_t d_in, int64_t n_tokens, 
  *             v (1 + erf(v / sqrt 2)) / 2.
  * d_in = 0 gives act(b) + r.  Rows need no more than their type's alignment;
  * rows of X that start 16-byte aligned with d_in a multiple of 8 load faster.
- * Which kernel runs, and with it the order of the sums, goes by the sizes.
+ * Which kernel runs, and with it the order of the sums, goes by the sizes
+ * (gptq_packed_matmul_kernel): a token's last bits may differ between batches
+ * that run on different kernels, and are the same on one.
  * Errors: GPTQ_EINVAL (negative size, bits outside [2, 8], negative
  * group_size or one not dividing d_in, a stride below its row, unknown dtype
  * or activation, null pointer), GPTQ_EUNSUPPORTED (x_dtype GPTQ_F32, y_dtype
  * neither x_dtype nor GPTQ_F32, group_size not a multiple of 16, d_in or ldx
- * above 2^21, d_out or n_tokens above 2^24, more than 2^21 tiles of 256 rows
+ * above 2^21, d_out or n_tokens above 2^24, more than 2^20 tiles of 256 rows
  * by 256 tokens).
  */
 int gptq_packed_matmul(const uint32_t* packed, int bits, int64_t d_out, int64_t d_in, const float* scales,
                        const int32_t* zeros, int64_t group_size, const void* X, int x_dtype, int64_t n_tokens,
                        int64_t ldx, const void* bias, const void* residual, int64_t ldr, void* Y, int y_dtype,
                        int64_t ldy, int activation, void* stream);
+
+/*
+ * Which kernel a product of these sizes runs on, as gptq_fp8_matmul_kernel;
+ * aligned: rows of X start 16-byte aligned.
+ */
+const char* gptq_packed_matmul_kernel(int64_t d_out, int64_t d_in, int64_t group_size, int64_t n_tokens, int aligned,
+                                      int compute_units);
 
 /*
  * Attention over whole prompts, several sequences packed one behind the other:

@@ -48,6 +48,7 @@ EXPORTS = (
     "gptq_fp8_matmul_kernel",
     "gptq_fp8_gated_kernel",
     "gptq_packed_matmul",
+    "gptq_packed_matmul_kernel",
     "gptq_attention",
     "gptq_cache_store",
     "gptq_cached_attention_workspace",
@@ -120,6 +121,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                   _vp, _i64, _vp, _sz, _vp]),
         "gptq_fp8_matmul_kernel": (ctypes.c_char_p, [_i64, _i64, _i64, _i32, _i32]),
         "gptq_fp8_gated_kernel": (ctypes.c_char_p, [_i64, _i64, _i64, _i32]),
+        "gptq_packed_matmul_kernel": (ctypes.c_char_p, [_i64, _i64, _i64, _i64, _i32, _i32]),
         "gptq_packed_matmul": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _i64, _i64, _vp, _vp, _i64,
                                       _vp, _i32, _i64, _i32, _vp]),
         "gptq_attention": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64, _i64,
@@ -620,6 +622,14 @@ def packed_matmul(packed, bits: int, d_in: int, scales, zeros, group_size: int, 
                                 _fp8_stream(dev, stream))
     if rc:
         _check("gptq_packed_matmul", rc)
+
+
+def packed_matmul_kernel(n: int, d_out: int, d_in: int, group_size: int = 0, aligned: bool = True,
+                         compute_units: int = 0) -> Optional[str]:
+    """Which kernel a product with packed weights of these sizes runs on, where
+    rows of X start 16-byte aligned or not."""
+    name = load().gptq_packed_matmul_kernel(d_out, d_in, group_size, n, aligned, compute_units)
+    return name.decode() if name else None
 
 
 def _heads_of(t, dev: int, kind, what: str):

@@ -469,7 +469,7 @@ const char* gptq_fp8_gated_kernel(int64_t d_ff, int64_t d_in, int64_t n, int com
 namespace {
 constexpr int64_t kPackedMaxCols = (int64_t)1 << 21;  // 256 rows of X stay within 2^30 bytes
 constexpr int64_t kPackedMaxRows = (int64_t)1 << 24;
-constexpr int64_t kPackedMaxTiles = (int64_t)1 << 21;  // four workgroups of 256 threads each: below 2^32 threads
+constexpr int64_t kPackedMaxTiles = (int64_t)1 << 20;  // eight workgroups of 256 threads each: below 2^32 threads
 }  // namespace
 
 int gptq_packed_matmul(const uint32_t* packed, int bits, int64_t d_out, int64_t d_in, const float* scales,
@@ -490,6 +490,16 @@ int gptq_packed_matmul(const uint32_t* packed, int bits, int64_t d_out, int64_t 
     const PackedProduct c = {packed, scales, zeros, X, bias, residual, Y, d_out, d_in, group_size, n, ldx, ldr, ldy,
                              bits, activation};
     return hip_status(launch_packed_matmul(c, x_dtype, y_dtype, as_stream(stream)));
+}
+
+const char* gptq_packed_matmul_kernel(int64_t d_out, int64_t d_in, int64_t group_size, int64_t n, int aligned,
+                                      int compute_units) {
+    if (d_out <= 0 || d_in < 0 || n <= 0 || group_size < 0 || group_size % 16 != 0) return nullptr;
+    if (group_size > 0 && d_in % group_size != 0) return nullptr;
+    if (d_in > kPackedMaxCols || d_out > kPackedMaxRows || n > kPackedMaxRows) return nullptr;
+    if (((d_out + 255) / 256) * ((n + 255) / 256) > kPackedMaxTiles) return nullptr;
+    const int64_t cus = compute_units > 0 ? compute_units : device_cu_count();
+    return cus > 0 ? packed_matmul_kernel_name(d_out, d_in, group_size, n, aligned != 0, cus) : nullptr;
 }
 
 namespace {

@@ -455,33 +455,21 @@ __global__ __launch_bounds__(kJoinThreads) void cached_join_kernel(CachedArgs a,
     *reinterpret_cast<v8*>(static_cast<T*>(c.out) + b * c.ldo[0] + (h0 + r) * c.ldo[1] + e) = out;
 }
 
-constexpr int64_t kCachedWorkers = 256;   // at most; one a CU
+constexpr int64_t kCachedWorkers = 512;   // at most
 constexpr int64_t kCachedWhole = 1024;    // tokens up to which a unit is one workgroup's
 
 inline int padded_head(int64_t d) { return d <= 64 ? 64 : 128; }
 inline int64_t unit_rows(int64_t heads, int64_t kv_heads) { return std::min(heads / kv_heads, kHeadRows); }
 
 template <typename T, int kDp, int kWaves>
-hipError_t cached_whole(const CachedArgs& a, int64_t units, hipStream_t s) {
-    const TimedLaunch t(K_CACHED_ATTENTION, s);
-    GPTQ_LAUNCH(t, (cached_kernel<T, kDp, kWaves, false>), dim3((unsigned)units), dim3(kWaves * kWave), 0, s, a);
-    return hipGetLastError();
-}
-
-// Short tables: a unit is one workgroup's, of eight waves where each has a CU to itself
-// (333 tokens of 8 key heads 8.4 us, 9.3 with four; 900 tokens 13.4 and 16.4), of four
-// otherwise (64 sequences of 500 tokens 24.6 us, 28.8 with eight).  Longer ones: one
-// workgroup of eight waves a CU, whose copies in flight keep memory busy (131072 tokens
-// 105 us, 5.1 TB/s, two of four waves 108; 16 x 3000 tokens of 16 heads of 64 40 us, 50).
-template <typename T, int kDp>
-hipError_t cached_go(CachedArgs a, hipStream_t s) {
-    const CachedAttentionCall& c = a.c;
-    const int64_t units = c.n_seqs * c.kv_heads * a.head_groups, most = c.max_pages * c.cache.page_size;
-    const int cus = device_cu_count();
-    if (cus <= 0) return hipErrorInvalidDevice;
-    if (most <= kCachedWhole) return units <= cus ? cached_whole<T, kDp, 8>(a, units, s) : cached_whole<T, kDp, 4>(a, units, s);
-    constexpr int kWaves = 8, kStep = kWaves * 4 * kWave / (kDp / 8);
-    a.workers = std::min({kCachedWorkers, (int64_t)cus, units * ((most + kStep - 1) / kStep)});
+hipError_t cached_waves(CachedArgs a, int64_t units, int64_t most, int cus, hipStream_t s) {
+    if (most <= kCachedWhole) {
+        const TimedLaunch t(K_CACHED_ATTENTION, s);
+        GPTQ_LAUNCH(t, (cached_kernel<T, kDp, kWaves, false>), dim3((unsigned)units), dim3(kWaves * kWave), 0, s, a);
+        return hipGetLastError();
+    }
+    constexpr int kStep = kWaves * 4 * kWave / (kDp / 8);
+    a.workers = std::min({kCachedWorkers, (int64_t)(8 / kWaves) * cus, units * ((most + kStep - 1) / kStep)});
     const TimedLaunch t(K_CACHED_ATTENTION, s);
     GPTQ_LAUNCH(t, (cached_kernel<T, kDp, kWaves, true>), dim3((unsigned)a.workers), dim3(kWaves * kWave), 0, s, a);
     const hipError_t e = hipGetLastError();
@@ -489,6 +477,21 @@ hipError_t cached_go(CachedArgs a, hipStream_t s) {
     const TimedLaunch j(K_CACHED_JOIN, s);
     GPTQ_LAUNCH(j, (cached_join_kernel<T, kDp>), dim3((unsigned)a.workers), dim3(kJoinThreads), 0, s, a, (uint32_t)kStep);
     return hipGetLastError();
+}
+
+// Eight waves a workgroup, one a CU, while there is a CU for each unit (333 tokens of 8
+// key heads 8.4 us, 9.3 with four waves; 900 tokens 13.4 and 16.4; 131072 tokens 107 us,
+// 5.0 TB/s, and 108; 16 x 3000 tokens of 16 heads of 64 41 and 50).  Four waves, two
+// workgroups a CU, for more units, since what a unit's begin and end take then lies beside
+// another's copies (64 x 500 tokens 24.6 us, 28.8 with eight; in longer tables 999 x 50 and
+// one of 7000 137 us and 216, 200 x 500 and one of 7000 104 and 111).
+template <typename T, int kDp>
+hipError_t cached_go(const CachedArgs& a, hipStream_t s) {
+    const CachedAttentionCall& c = a.c;
+    const int64_t units = c.n_seqs * c.kv_heads * a.head_groups, most = c.max_pages * c.cache.page_size;
+    const int cus = device_cu_count();
+    if (cus <= 0) return hipErrorInvalidDevice;
+    return units <= cus ? cached_waves<T, kDp, 8>(a, units, most, cus, s) : cached_waves<T, kDp, 4>(a, units, most, cus, s);
 }
 
 }  // namespace

@@ -171,6 +171,7 @@ struct PackedProduct {
     int bits, activation;
 };
 hipError_t launch_packed_matmul(const PackedProduct& c, int x_dtype, int y_dtype, hipStream_t s);
+const char* packed_matmul_kernel_name(int64_t M, int64_t K, int64_t group, int64_t n, bool wide, int64_t cus);
 
 // ---- attention ------------------------------------------------------------------
 // Query heads that share a key head are rows of one tile, up to this many.

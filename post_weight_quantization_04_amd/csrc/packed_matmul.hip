@@ -22,26 +22,35 @@ namespace {
 // part of its own and one for a block of 128 columns, in us:
 //                 few tokens (16 rows, a round)      32 x 64        64 x 128, one a CU   two   128 x 384
 //   4-bit f16     1.7 + 0.1 (to 4), 0.12 (to 16), 0.2   2.0 + 0.4      2.0 + 0.9   2.0 + 1.4   3.5 + 2.65
-PmKernel choose(const PmArgs& a, bool fine, int64_t cus) {
-    const int64_t M = a.c.M, n = a.c.n, nb = a.nb;
+// (of 4-bit codes, the other widths being near).  A kernel whose grid would be too large
+// is left out.
+PmKernel choose(int64_t M, int64_t nb, int64_t n, bool vec, bool fine, int64_t cus) {
     if (n <= 4) return kPmFew;
     auto rounds = [&](int64_t tokens, int64_t rows, int64_t each) {
         return (double)((((n + tokens - 1) / tokens) * ((M + rows - 1) / rows) + cus * each - 1) / (cus * each));
     };
-    const double few = rounds(32, 16, 1) * (1.7 + (n <= 16 ? 0.12 : 0.2) * nb), small = rounds(32, 64, 1) * (2.0 + 0.4 * nb);
+    auto fits = [&](int64_t tokens, int64_t rows, int64_t threads) {
+        return ((n + tokens - 1) / tokens) * ((M + rows - 1) / rows) * threads < (int64_t)1 << 32;
+    };
+    const double none = 1e30;
+    const double few = n <= 32 * 65535 ? rounds(32, 16, 1) * (1.7 + (n <= 16 ? 0.12 : 0.2) * nb) : none;
+    const double small = fits(32, 64, 1024) ? rounds(32, 64, 1) * (2.0 + 0.4 * nb) : none;
     const bool one = rounds(64, 128, 1) == 1.0;
     const double mid = one ? 2.0 + 0.9 * nb : rounds(64, 128, 2) * (2.0 + 1.4 * nb);
-    const double big = a.vec && !fine ? rounds(128, 384, 1) * (3.5 + 2.65 * nb) : 1e30;
+    const double big = vec && !fine ? rounds(128, 384, 1) * (3.5 + 2.65 * nb) : none;
     const double least = std::min(std::min(few, small), std::min(mid, big));
     return least == few ? kPmFew : least == small ? kPm32x64 : least == mid ? kPm64x128 : kPm128x384;
 }
 
+// Groups that do not consist of whole blocks.
+bool fine_groups(int64_t K, int64_t group) { return group % kPmBlock != 0 && K > group; }
+
 template <typename T, int kBits>
 hipError_t bits_go(const PmArgs& a, hipStream_t s) {
-    const bool fine = a.group % kPmBlock != 0 && a.ng > 1;
+    const bool fine = fine_groups(a.c.K, a.c.group);
     const int64_t cus = device_cu_count();
     if (cus <= 0) return hipErrorInvalidDevice;
-    const PmKernel kernel = choose(a, fine, cus);
+    const PmKernel kernel = choose(a.c.M, a.nb, a.c.n, a.vec, fine, cus);
     if (kernel == kPmFew) return launch_packed_few<T, kBits>(a, fine, s);
     return launch_packed_tile<T, kBits>(a, kernel, fine, s);
 }
@@ -60,6 +69,15 @@ hipError_t typed_go(const PmArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+const char* packed_matmul_kernel_name(int64_t M, int64_t K, int64_t group, int64_t n, bool wide, int64_t cus) {
+    switch (choose(M, (K + kPmBlock - 1) / kPmBlock, n, wide && K % 8 == 0, fine_groups(K, group), cus)) {
+        case kPmFew: return "few tokens";
+        case kPm32x64: return "32 x 64";
+        case kPm64x128: return "64 x 128";
+        default: return "128 x 384";
+    }
+}
 
 hipError_t launch_packed_matmul(const PackedProduct& c, int x_dtype, int y_dtype, hipStream_t s) {
     PmArgs a = {};

@@ -380,7 +380,7 @@ def attention(q, k, v, starts=None, causal: bool = True, scale: Optional[float] 
     ``scale``: 1 / sqrt(d) by default."""
     if out is None:
         out = _like(q, stream)
-    _lib.attention(q, k, v, starts, out, causal, q.shape[-1] ** -0.5 if scale is None else scale, stream)
+    _lib.attention(q, k, v, starts, out, causal, max(q.shape[-1], 1) ** -0.5 if scale is None else scale, stream)
     return out
 
 
@@ -419,6 +419,6 @@ def cached_attention(q, cache: KVCache, table, lengths, scale: Optional[float] =
     _, kv_heads, page_size, _ = cache.keys.shape
     need = _lib.cached_attention_workspace(n, heads, kv_heads, d, table.shape[1], page_size)
     buf = _scratch(need, ws, q.device, stream)
-    _lib.cached_attention(q, cache.keys, cache.values, table, lengths, out, d ** -0.5 if scale is None else scale, buf,
+    _lib.cached_attention(q, cache.keys, cache.values, table, lengths, out, max(d, 1) ** -0.5 if scale is None else scale, buf,
                           stream)
     return out

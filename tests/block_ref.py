@@ -150,3 +150,10 @@ def near(got, want, off, what=""):
     assert far.numel() == 0 or float(far.max()) <= 0, (
         f"{what}: {int((far > 0).sum())} of {far.numel()} off, worst at {worst}: "
         f"{got.flatten()[worst]} for {want.flatten()[worst]} (bound {off.flatten()[worst]})")
+
+
+# name, tokens, rows, columns, group: products with packed weights that reach each kernel of a whole device
+PACKED_KERNELS = [("few tokens", 3, 1000, 512, 128), ("few tokens", 15, 515, 1000, 0), ("few tokens", 32, 2000, 384, 64),
+                  ("32 x 64", 530, 301, 384, 128), ("32 x 64", 300, 700, 1000, 0), ("32 x 64", 250, 1100, 640, 32),
+                  ("64 x 128", 1100, 1035, 512, 128), ("64 x 128", 777, 1363, 1000, 0), ("64 x 128", 2700, 2801, 192, 48),
+                  ("128 x 384", 2700, 2801, 384, 128), ("128 x 384", 2945, 2689, 264, 0), ("128 x 384", 4000, 2305, 512, 256)]

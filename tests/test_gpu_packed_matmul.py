@@ -171,3 +171,26 @@ def test_another_stream(lib):
     got = layer.packed_matmul(w, x, stream=side)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("bits", [2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("name,n,d_out,d,group", ref.PACKED_KERNELS)
+def test_every_kernel(lib, name, n, d_out, d, group, bits, kind):
+    from post_weight_quantization_04_amd import _lib
+    if torch.cuda.get_device_properties(0).multi_processor_count == 256:
+        assert _lib.packed_matmul_kernel(n, d_out, d, group) == name
+    check(n, d, d_out, bits, group, kind, out="f32", seed=bits, whole=True)
+    check(n, d, d_out, bits, group, kind, bias=True, act="silu", residual=True, seed=bits)
+
+
+@pytest.mark.parametrize("n,d_out,d", [(2700, 2800, 136), (1001, 1003, 500), (40, 3001, 1000)])
+def test_unaligned_rows_at_larger_sizes(lib, n, d_out, d):
+    """Rows of X one element off, against the same call on aligned rows of whole numbers."""
+    from post_weight_quantization_04_amd import layer
+    w, x, dense = make(n, d, d_out, 4, 0, torch.float16, whole=True)
+    off = torch.empty(n * (d + 1) + 1, dtype=torch.float16, device="cuda")[1:].view(n, d + 1)[:, :d]
+    off.copy_(x)
+    got = layer.packed_matmul(w, off, dtype=torch.float32)
+    assert torch.equal(got.double().cpu(), x.double() @ dense.T)
+    assert torch.equal(got, layer.packed_matmul(w, x.cuda(), dtype=torch.float32))
