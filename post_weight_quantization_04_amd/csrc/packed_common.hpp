@@ -202,21 +202,38 @@ __device__ __forceinline__ void pm_copy16(__amdgpu_buffer_rsrc_t r, uint8_t* lds
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, base, 0, 0);
 }
 
-// Columns k .. k + 7 of a row of x from p + at on, whose `left` columns need no more
-// than their type's alignment; zeros behind the last.
+// x whose rows start at any element: the words around eight columns, and the columns
+// out of them a step later.  (As eight elements, or as sixteen bytes of any alignment
+// under a condition, each load was waited for on its own: 3000 x 1001 -> 2000 87 us.)
+// The buffer begins at the word that holds the first element and ends with the one that
+// holds the last.
 template <typename T>
-__device__ __forceinline__ frag_t pm_chunk(const T* p, int64_t at, int k, int left) {
-    T v[8] = {};
-    if (left >= kPmBlock) {  // (the same for all lanes: no branch around the load)
-        __builtin_memcpy(v, p + at + k, 16);
-    } else {
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t pm_words_rsrc(const T* x, uint32_t elements, uint32_t& first) {
+    first = (uint32_t)(reinterpret_cast<uintptr_t>(x) / 2 % 2);
+    return pm_rsrc(x - first, (2 * (first + elements) + 3) & ~3u);
+}
+struct PmWords {
+    uint4v w;
+    uint32_t next;
+};
+__device__ __forceinline__ PmWords pm_words(__amdgpu_buffer_rsrc_t r, uint32_t element, uint32_t base) {
+    const uint32_t at = 2 * element & ~3u;
+    PmWords p;
+    p.w = __builtin_amdgcn_raw_buffer_load_b128(r, at, base, 0);
+    p.next = __builtin_amdgcn_raw_buffer_load_b32(r, at + 16, base, 0);
+    return p;
+}
+// left: columns of the row from the first of these on, what follows them as zeros
+__device__ __forceinline__ frag_t pm_columns(const PmWords& p, uint32_t element, int left) {
+    const uint32_t by = element % 2 * 16;
+    uint4v f;
+    f[0] = __builtin_amdgcn_alignbit(p.w[1], p.w[0], by);
+    f[1] = __builtin_amdgcn_alignbit(p.w[2], p.w[1], by);
+    f[2] = __builtin_amdgcn_alignbit(p.w[3], p.w[2], by);
+    f[3] = __builtin_amdgcn_alignbit(p.next, p.w[3], by);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (k + e < left) v[e] = p[at + k + e];
-    }
-    frag_t f;
-    __builtin_memcpy(&f, v, 16);
-    return f;
+    for (int i = 0; i < 4; ++i) f[i] = left >= 2 * i + 2 ? f[i] : left == 2 * i + 1 ? f[i] & 0xffffu : 0u;
+    return __builtin_bit_cast(frag_t, f);
 }
 
 __device__ __forceinline__ float activated(float v, int activation) {

@@ -20,7 +20,7 @@ namespace {
 template <typename T, int kBits, bool kFine, bool kVec, int kWaves, int kQuads>
 __global__ __launch_bounds__(kWaves* kWave) void packed_few_kernel(PmArgs a) {
     constexpr int kTn = (kQuads + 3) / 4;
-    constexpr int kScales = kFine ? 8 : 1;  // of a block
+    constexpr int kScales = kFine ? 2 : 1;  // of a lane: of a run of 32 codes, halves of it
     constexpr int kPart = kTn * 4096;       // a wave's part of a stage
     __shared__ __align__(16) uint8_t lds0[kWaves * kPart];
     __shared__ __align__(16) uint8_t lds1[kWaves * kPart];
@@ -35,17 +35,20 @@ __global__ __launch_bounds__(kWaves* kWave) void packed_few_kernel(PmArgs a) {
     const __amdgpu_buffer_rsrc_t rw = pm_rsrc(c.packed + r0 * a.nw, (uint32_t)rows * (uint32_t)a.nw * 4u);
     const __amdgpu_buffer_rsrc_t rs = pm_rsrc(c.scales + r0 * a.ng, (uint32_t)rows * (uint32_t)a.ng * 4u);
     const __amdgpu_buffer_rsrc_t rz = pm_rsrc(c.zeros + r0 * a.ng, (uint32_t)rows * (uint32_t)a.ng * 4u);
-    const __amdgpu_buffer_rsrc_t rx = pm_rsrc(x, (uint32_t)(((toks - 1) * c.ldx + c.K) * 2));
+    uint32_t first = 0;
+    const uint32_t elements = (uint32_t)((toks - 1) * c.ldx + c.K);
+    const __amdgpu_buffer_rsrc_t rx = kVec ? pm_rsrc(x, 2 * elements) : pm_words_rsrc(x, elements, first);
     const uint32_t wo = 4u * ((uint32_t)(lane / 4) * (uint32_t)a.nw + (uint32_t)(lane % 4 * kBits));
     const uint32_t so = 4u * (uint32_t)(lane / 4) * (uint32_t)a.ng;
     uint32_t xo[kQuads];
     auto chunk_of = [&](int i) { return (lane % 16) ^ pm_swizzle((4 * i + lane / 16) % 16); };
 #pragma unroll
-    for (int i = 0; i < kQuads; ++i) xo[i] = 2 * ((uint32_t)(4 * i + lane / 16) * (uint32_t)c.ldx + 8u * (uint32_t)chunk_of(i));
+    for (int i = 0; i < kQuads; ++i) xo[i] = (kVec ? 2 : 1) * ((uint32_t)(4 * i + lane / 16) * (uint32_t)c.ldx + 8u * (uint32_t)chunk_of(i)) + first;
 
     struct Block {
         uint32_t w[kBits], s[kScales], z[2];
-        frag_t x[kVec ? 1 : kQuads];
+        PmWords x[kVec ? 1 : kQuads];
+        int left;
     };
     auto load = [&](Block& g, uint8_t* st, int b) {
         b = min(b, nb - 1);  // past the last block, that one again, never used
@@ -53,23 +56,24 @@ __global__ __launch_bounds__(kWaves* kWave) void packed_few_kernel(PmArgs a) {
         load_run<kBits>(g.w, rw, wo, (uint32_t)b * (16u * kBits));
         if (kFine) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                g.z[h] = __builtin_amdgcn_raw_buffer_load_b32(rz, so + 4 * group_of(a, k0 + 32 * (lane % 4) + 16 * h), 0, 0);
-#pragma unroll
-            for (int i = 0; i < kScales; ++i) g.s[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, so, 4 * group_of(a, k0 + 16 * i), 0);
+            for (int h = 0; h < kScales; ++h) {
+                const uint32_t at = so + 4 * group_of(a, k0 + 32 * (lane % 4) + 16 * h);
+                g.z[h] = __builtin_amdgcn_raw_buffer_load_b32(rz, at, 0, 0);
+                g.s[h] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
+            }
         } else {
             const uint32_t at = 4 * group_of(a, k0);
             g.z[0] = __builtin_amdgcn_raw_buffer_load_b32(rz, so, at, 0);
             g.s[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, so, at, 0);
         }
-        const int left = (int)(c.K - k0);  // what follows the last column is not the row's
+        const int left = g.left = (int)(c.K - k0);  // what follows the last column is not the row's
         if (kVec) {
 #pragma unroll
             for (int i = 0; i < kQuads; ++i)
                 pm_copy16(rx, st + (w * kPart + 1024 * i), 8 * chunk_of(i) < left ? xo[i] : kPmOut, 2 * k0);
         } else {
 #pragma unroll
-            for (int i = 0; i < kQuads; ++i) g.x[i] = pm_chunk(x, min(4 * i + lane / 16, toks - 1) * c.ldx + k0, 8 * chunk_of(i), left);
+            for (int i = 0; i < kQuads; ++i) g.x[i] = pm_words(rx, xo[i], 2 * k0);
         }
     };
     float4v acc[kTn];
@@ -78,7 +82,8 @@ __global__ __launch_bounds__(kWaves* kWave) void packed_few_kernel(PmArgs a) {
     auto use = [&](const Block& g, uint8_t* st) {
         if (!kVec) {
 #pragma unroll
-            for (int i = 0; i < kQuads; ++i) *reinterpret_cast<frag_t*>(st + (w * kPart + 1024 * i + 16 * lane)) = g.x[i];
+            for (int i = 0; i < kQuads; ++i)
+                *reinterpret_cast<frag_t*>(st + (w * kPart + 1024 * i + 16 * lane)) = pm_columns(g.x[i], xo[i], g.left - 8 * chunk_of(i));
         }
         uint32_t mine[kBits];
         frag_t f[4];
@@ -87,9 +92,9 @@ __global__ __launch_bounds__(kWaves* kWave) void packed_few_kernel(PmArgs a) {
         const int z = (int)from_row(g.z[0], 4 * l16 + (kFine ? kg : 0));
         codes32<T, kBits>(f, mine, z, kFine ? (int)from_row(g.z[1], 4 * l16 + kg) : z);
         turn_blocks(f);
-        float s[kScales];
+        float s[kFine ? 8 : 1];
 #pragma unroll
-        for (int h = 0; h < kScales; ++h) s[h] = __builtin_bit_cast(float, from_row(g.s[h], 4 * l16));
+        for (int h = 0; h < (kFine ? 8 : 1); ++h) s[h] = __builtin_bit_cast(float, from_row(g.s[h % kScales], 4 * l16 + h / 2));
 #pragma unroll
         for (int j = 0; j < kTn; ++j) {
             v8 xf[4];

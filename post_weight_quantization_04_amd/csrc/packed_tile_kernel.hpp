@@ -76,7 +76,9 @@ __global__ __launch_bounds__(kGroups* kWaves* kWave, kGroups* kWaves / 4 * kPerC
     const __amdgpu_buffer_rsrc_t rw = pm_rsrc(c.packed + r0 * a.nw, (uint32_t)rows * (uint32_t)a.nw * 4u);
     const __amdgpu_buffer_rsrc_t rs = pm_rsrc(c.scales + r0 * a.ng, (uint32_t)rows * (uint32_t)a.ng * 4u);
     const __amdgpu_buffer_rsrc_t rz = pm_rsrc(c.zeros + r0 * a.ng, (uint32_t)rows * (uint32_t)a.ng * 4u);
-    const __amdgpu_buffer_rsrc_t rx = pm_rsrc(x, (uint32_t)(((toks - 1) * c.ldx + c.K) * 2));
+    uint32_t first = 0;
+    const uint32_t elements = (uint32_t)((toks - 1) * c.ldx + c.K);
+    const __amdgpu_buffer_rsrc_t rx = kVec ? pm_rsrc(x, 2 * elements) : pm_words_rsrc(x, elements, first);
 
     // Sources of this lane's copies: four rows an instruction; every fourth
     // instruction has the same swizzle.  Rows past the last lie past the end of the
@@ -89,21 +91,23 @@ __global__ __launch_bounds__(kGroups* kWaves* kWave, kGroups* kWaves / 4 * kPerC
     for (int i = 0; i < kCopies; ++i) {
         const int r = copy_row + 4 * i;
         xk[i] = 8 * ((lane % 16) ^ pm_swizzle(r % 16));
-        xo[i] = 2 * ((uint32_t)r * (uint32_t)c.ldx + (uint32_t)xk[i]);
+        xo[i] = (kVec ? 2 : 1) * ((uint32_t)r * (uint32_t)c.ldx + (uint32_t)xk[i]) + first;
     }
     // (steps count the group's blocks: every kGroups-th)
-    frag_t held[kVec ? 1 : kCopies];  // by way of registers: what goes to LDS a step after it was asked for
+    PmWords held[kVec ? 1 : kCopies];  // by way of registers: what goes to LDS a step after it was asked for
     auto copy = [&](uint8_t* st, int step) {
         const int b = step * kGroups + set, left = (int)c.K - b * kPmBlock;
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
             if (kVec) pm_copy16(rx, st + (base + 1024 * (kCopies * w + i)), xk[i] < left ? xo[i] : kPmOut, (uint32_t)(2 * b * kPmBlock));
-            else held[i] = pm_chunk(x, min(copy_row + 4 * i, toks - 1) * c.ldx + b * kPmBlock, xk[i], left);
+            else held[i] = pm_words(rx, xo[i], (uint32_t)(2 * b * kPmBlock));
         }
     };
-    auto put = [&](uint8_t* st) {
+    auto put = [&](uint8_t* st, int step) {
+        const int left = (int)c.K - (step * kGroups + set) * kPmBlock;
 #pragma unroll
-        for (int i = 0; i < kCopies && !kVec; ++i) *reinterpret_cast<frag_t*>(st + (base + 1024 * (kCopies * w + i) + 16 * lane)) = held[i];
+        for (int i = 0; i < kCopies && !kVec; ++i)
+            *reinterpret_cast<frag_t*>(st + (base + 1024 * (kCopies * w + i) + 16 * lane)) = pm_columns(held[i], xo[i], left - xk[i]);
     };
 
     // The wave's rows, 16 j + l16 for this lane; scales and zeros come by way of row 16 j + lane / 4.
@@ -118,21 +122,25 @@ __global__ __launch_bounds__(kGroups* kWaves* kWave, kGroups* kWaves / 4 * kPerC
         for (int j = 0; j < kNt; ++j) load_run<kBits>(words[slot][j], rw, wo, (uint32_t)b * (16u * kBits) + (uint32_t)j * w16);
     };
     // Scales and zeros of four blocks, one a lane of the row's four (groups of
-    // whole blocks; of finer ones, the zeros of this lane's run of codes of one block).
+    // whole blocks; of finer ones, those of a run of 32 codes of one block a lane,
+    // two halves of it).
     constexpr int kZeros = kFine ? 2 : 1;
-    uint32_t ss[kNt], zs[kNt][kZeros];
+    uint32_t ss[kNt][kZeros], zs[kNt][kZeros];
     auto load_grids = [&](int step) {
         const int b = step * kGroups + set;
 #pragma unroll
         for (int j = 0; j < kNt; ++j) {
             if (kFine) {
 #pragma unroll
-                for (int h = 0; h < kZeros; ++h)
-                    zs[j][h] = __builtin_amdgcn_raw_buffer_load_b32(rz, so + 4 * group_of(a, (uint32_t)(b * kPmBlock + 32 * (lane % 4) + 16 * h)), (uint32_t)j * s16, 0);
+                for (int h = 0; h < kZeros; ++h) {
+                    const uint32_t at = so + 4 * group_of(a, (uint32_t)(b * kPmBlock + 32 * (lane % 4) + 16 * h));
+                    zs[j][h] = __builtin_amdgcn_raw_buffer_load_b32(rz, at, (uint32_t)j * s16, 0);
+                    ss[j][h] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, (uint32_t)j * s16, 0);
+                }
             } else {
                 const uint32_t at = so + 4 * group_of(a, (uint32_t)((b + lane % 4 * kGroups) * kPmBlock));
                 zs[j][0] = __builtin_amdgcn_raw_buffer_load_b32(rz, at, (uint32_t)j * s16, 0);
-                ss[j] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, (uint32_t)j * s16, 0);
+                ss[j][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, (uint32_t)j * s16, 0);
             }
         }
     };
@@ -179,7 +187,7 @@ __global__ __launch_bounds__(kGroups* kWaves* kWave, kGroups* kWaves / 4 * kPerC
 #pragma unroll
                     for (int j = 0; j < kNt; ++j) {
                         const int z = (int)from_row(zs[j][0], 4 * l16 + i4);
-                        s[j] = __builtin_bit_cast(float, from_row(ss[j], 4 * l16 + i4));
+                        s[j] = __builtin_bit_cast(float, from_row(ss[j][0], 4 * l16 + i4));
                         codes32<T, kBits>(f[j], words[i4 % kRing][j], z, z);
                         p[j] = (float4v){};
 #pragma unroll
@@ -190,7 +198,7 @@ __global__ __launch_bounds__(kGroups* kWaves* kWave, kGroups* kWaves / 4 * kPerC
                         // (the codes first: they are waited for with the copies before these)
                         load(b + kRing, i4 % kRing);
                         if (i4 == 3) load_grids(b + 1);
-                        put(before);
+                        put(before, b + 2);
                         copy(to, b + 3);
                     }
 #pragma unroll
@@ -217,21 +225,22 @@ __global__ __launch_bounds__(kGroups* kWaves* kWave, kGroups* kWaves / 4 * kPerC
                 codes32<T, kBits>(f[j], words[i4 % kRing][j], (int)from_row(zs[j][0], 4 * l16 + kg), (int)from_row(zs[j][kZeros - 1], 4 * l16 + kg));
                 turn_blocks(f[j]);
             }
+            float sa[4][kNt], sb[4][kNt];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int j = 0; j < kNt; ++j) {
+                    sa[e][j] = __builtin_bit_cast(float, from_row(ss[j][0], 4 * l16 + e));
+                    sb[e][j] = __builtin_bit_cast(float, from_row(ss[j][kZeros - 1], 4 * l16 + e));
+                }
             load(b + kRing, i4 % kRing);
             load_grids(b + 1);
-            put(before);
+            put(before, b + 2);
             copy(to, b + 3);
             // 32 columns at a time, or twice sixteen (the others as zeros)
             const bool halves = a.group % 32 != 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float sa[kNt], sb[kNt];
-                const uint32_t k = (uint32_t)((b * kGroups + set) * kPmBlock + 32 * e), ga = 4 * group_of(a, k), gb = 4 * group_of(a, k + 16);
-#pragma unroll
-                for (int j = 0; j < kNt; ++j) {
-                    sa[j] = __builtin_bit_cast(float, from_row(__builtin_amdgcn_raw_buffer_load_b32(rs, so, ga + (uint32_t)j * s16, 0), 4 * l16));
-                    sb[j] = __builtin_bit_cast(float, from_row(__builtin_amdgcn_raw_buffer_load_b32(rs, so, gb + (uint32_t)j * s16, 0), 4 * l16));
-                }
 #pragma unroll
                 for (int i = 0; i < kMt; ++i) {
                     const v8 xf = tokens(st, i, e);
@@ -241,11 +250,11 @@ __global__ __launch_bounds__(kGroups* kWaves* kWave, kGroups* kWaves / 4 * kPerC
                         const v8 wf = __builtin_bit_cast(v8, f[j][e]);
                         const float4v p = Mat<T>::mfma16(xa, wf, (float4v){});
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(p[v], sa[j], acc[i][j][v]);
+                        for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(p[v], sa[e][j], acc[i][j][v]);
                         if (halves) {
                             const float4v q = Mat<T>::mfma16(xb, wf, (float4v){});
 #pragma unroll
-                            for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(q[v], sb[j], acc[i][j][v]);
+                            for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(q[v], sb[e][j], acc[i][j][v]);
                         }
                     }
                 }
@@ -261,11 +270,11 @@ __global__ __launch_bounds__(kGroups* kWaves* kWave, kGroups* kWaves / 4 * kPerC
         load_grids(0);
         in_order();
         copy(lds0, 0);
-        put(lds0);
+        put(lds0, 0);
         in_order();
         if (kRing > 1) load(kFirst, kFirst);
         copy(lds1, 1);
-        put(lds1);
+        put(lds1, 1);
         in_order();
         if (kRing > 1) load(kFirst + 1, kFirst + 1);
         copy(lds2, 2);
