@@ -1,6 +1,8 @@
 // The kernel of products with packed few-bit weights for many tokens.
 #pragma once
 
+#include <type_traits>
+
 #include "packed_tile.hpp"
 
 namespace gptq {
@@ -237,28 +239,42 @@ __global__ __launch_bounds__(kGroups* kWaves* kWave, kGroups* kWaves / 4 * kPerC
             load_grids(b + 1);
             put(before, b + 2);
             copy(to, b + 3);
-            // 32 columns at a time, or twice sixteen (the others as zeros)
-            const bool halves = a.group % 32 != 0;
+            // 32 columns at a time, or twice sixteen (the others as zeros): one branch
+            // around all of it, since between the products each would be waited for
+            // (500 tokens of 2048 x 2048 in groups of 32 48 us, so 28)
+            auto products = [&](auto halved) {
+                constexpr bool kHalves = decltype(halved)::value;
+                // as above: the next fragments read, these multiplied, the products before scaled
+                v8 xf[2];
+                float4v pa[2][kNt], pb[2][kNt];
+                xf[0] = tokens(st, 0, 0);
+                auto scale = [&](int q) {
+                    const int e = q / kMt, i = q % kMt;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+                    for (int j = 0; j < kNt; ++j)
 #pragma unroll
-                for (int i = 0; i < kMt; ++i) {
-                    const v8 xf = tokens(st, i, e);
-                    const v8 xa = halves && kg >= 2 ? (v8){} : xf, xb = kg >= 2 ? xf : (v8){};
+                        for (int v = 0; v < 4; ++v) {
+                            acc[i][j][v] = fmaf(pa[q % 2][j][v], sa[e][j], acc[i][j][v]);
+                            if (kHalves) acc[i][j][v] = fmaf(pb[q % 2][j][v], sb[e][j], acc[i][j][v]);
+                        }
+                };
+#pragma unroll
+                for (int q = 0; q < 4 * kMt; ++q) {
+                    if (q + 1 < 4 * kMt) xf[(q + 1) % 2] = tokens(st, (q + 1) % kMt, (q + 1) / kMt);
+                    const v8 x = xf[q % 2], xa = kHalves && kg >= 2 ? (v8){} : x, xb = kg >= 2 ? x : (v8){};
 #pragma unroll
                     for (int j = 0; j < kNt; ++j) {
-                        const v8 wf = __builtin_bit_cast(v8, f[j][e]);
-                        const float4v p = Mat<T>::mfma16(xa, wf, (float4v){});
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(p[v], sa[e][j], acc[i][j][v]);
-                        if (halves) {
-                            const float4v q = Mat<T>::mfma16(xb, wf, (float4v){});
-#pragma unroll
-                            for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(q[v], sb[e][j], acc[i][j][v]);
-                        }
+                        const v8 wf = __builtin_bit_cast(v8, f[j][q / kMt]);
+                        pa[q % 2][j] = Mat<T>::mfma16(xa, wf, (float4v){});
+                        if (kHalves) pb[q % 2][j] = Mat<T>::mfma16(xb, wf, (float4v){});
                     }
+                    if (q > 0) scale(q - 1);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-            }
+                scale(4 * kMt - 1);
+            };
+            if (a.group % 32 != 0) products(std::true_type{});
+            else products(std::false_type{});
         }
     };
     if (nb > 0) {
