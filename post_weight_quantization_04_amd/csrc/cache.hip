@@ -10,7 +10,9 @@ namespace gptq {
 
 namespace {
 
-// One thread copies sixteen bytes of a key row and of the value row beside it.
+// One thread copies sixteen bytes of a key row and of the value row beside it: 8192
+// tokens of 8 heads of 128 10 to 11.5 us, 5.8 to 6.6 TB/s of reads and writes, bound by
+// HBM and its caches; 24 tokens 3 us, a launch.
 __global__ __launch_bounds__(256) void cache_store_kernel(CacheStoreCall c, int chunks) {
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t row = id / chunks, e = id % chunks * 8;
@@ -42,6 +44,11 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheStoreCall c, int 
 // (maximum, sum, O) in the workspace: slot 2 w for a part that begins inside the
 // unit, 2 w + 1 for one that begins with it.  cached_join_kernel adds the parts
 // in order.
+//
+// Bound by HBM for long tables: 131072 tokens of 8 key heads of 128 102 us and 8 for the
+// join (5.3 TB/s over the first), 48 sequences of up to 8192 164 to 174 us and 10 (4.9);
+// 64 x 500 tokens 24.6 (5.3).  Short ones by the chain of lengths, pages, keys, launch:
+// 333 tokens 8.4 us.
 // ---------------------------------------------------------------------------
 struct CachedArgs {
     CachedAttentionCall c;
