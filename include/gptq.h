@@ -622,10 +622,10 @@ const char* gptq_packed_matmul_kernel(int64_t d_out, int64_t d_in, int64_t group
  *             sequence s holds the tokens [starts[s], starts[s + 1]), and may
  *             be empty.  Tokens of no sequence are neither read nor written.
  *             NULL with n_seqs = 1: one sequence of all tokens.
- *   scale     finite and above 0; scores times scale have to be finite.
+ *   scale     from 2^-100 to 2^100; scores times scale have to be finite.
  * Errors: GPTQ_EINVAL (negative size, heads not a multiple of kv_heads, a
  * stride below head_dim, starts NULL with n_seqs not 1, causal not 0 or 1,
- * scale not finite or not above 0, unknown dtype, null pointer),
+ * scale outside its range, unknown dtype, null pointer),
  * GPTQ_EUNSUPPORTED (GPTQ_F32, head_dim above 128 or not a multiple of 8,
  * pointers or strides not 16-byte aligned, a token stride above 2^22, n_tokens
  * or n_seqs above 2^24, heads above 2^16, 2^23 or more pieces of 32 rows, a row
@@ -677,6 +677,7 @@ int gptq_cache_store(const void* k, int64_t k_token, int64_t k_head, const void*
  *   table     device [n_seqs, ldt] int32, max_pages columns of it in use.
  *   lengths   device [n_seqs] int32; below 0 counts as 0, above max_pages *
  *             page_size as that.
+ *   scale     as for gptq_attention.
  *   workspace device memory of at least gptq_cached_attention_workspace() bytes,
  *             256-byte aligned; clobbered, needs no clearing.
  * Errors: as gptq_attention and gptq_cache_store (max_pages negative or above

@@ -508,7 +508,8 @@ constexpr int64_t kMaxHeadDim = 128, kMaxHeads = (int64_t)1 << 16, kMaxTokenStri
 inline bool rows16(const void* p, int64_t a, int64_t b, int64_t c = 0) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && a % 8 == 0 && b % 8 == 0 && c % 8 == 0;
 }
-inline bool bad_scale(double scale) { return !(scale > 0.0) || !isfinite((float)scale) || !((float)scale > 0.0f); }
+// (scores are compared with the lowest float32 times the scale, which has to stay far from any real score)
+inline bool bad_scale(double scale) { return !(scale >= 0x1p-100 && scale <= 0x1p100); }
 inline bool bad_heads(int64_t heads, int64_t kv_heads, int64_t d) {
     return heads < 0 || kv_heads < 0 || d < 0 || (kv_heads == 0 ? heads != 0 : heads % kv_heads != 0);
 }

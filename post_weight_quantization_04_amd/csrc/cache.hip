@@ -101,10 +101,11 @@ __device__ __forceinline__ int64_t count_steps(const CachedArgs& a, uint32_t per
 }
 
 // The sequence b that holds step `at` < all, and the steps `before` it (a unit's).
-__device__ __forceinline__ void find_step(const CachedArgs& a, uint32_t per, int64_t units, int64_t at, int64_t& b, int64_t& before) {
+// (False, and every loop over sequences ends, also where lengths change meanwhile.)
+__device__ __forceinline__ bool find_step(const CachedArgs& a, uint32_t per, int64_t units, int64_t at, int64_t& b, int64_t& before) {
     const int lane = threadIdx.x % kWave;
     before = 0;
-    for (b = 0;; b += kWave) {
+    for (b = 0; b < a.c.n_seqs; b += kWave) {
         const int64_t mine = b + lane < a.c.n_seqs ? (cached_length(a, b + lane) + (uint64_t)per - 1) / per : 0;
         const int64_t sum = wave_scan(mine);
         const uint64_t past = __ballot((before + sum) * units > at);
@@ -112,10 +113,11 @@ __device__ __forceinline__ void find_step(const CachedArgs& a, uint32_t per, int
             const int in = __builtin_ctzll(past);
             before += uniform64(__shfl(sum - mine, in, kWave));
             b += in;
-            return;
+            return true;
         }
         before += uniform64(__shfl(sum, kWave - 1, kWave));
     }
+    return false;
 }
 
 // Memory to LDS without registers in between, a wave's lanes one behind the
@@ -162,9 +164,9 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void cached_kernel(CachedArgs a) 
         const int64_t from = (int64_t)blockIdx.x * all / workers, to = ((int64_t)blockIdx.x + 1) * all / workers;
         left = to - from;
         int64_t before;
-        find_step(a, kStep, units, from, b, before);
-        const int64_t steps = (cached_length(a, b) + (uint64_t)kStep - 1) / kStep;
-        unit = (from - before * units) / steps;
+        if (!find_step(a, kStep, units, from, b, before)) return;
+        const int64_t steps = max((int64_t)((cached_length(a, b) + (uint64_t)kStep - 1) / kStep), (int64_t)1);
+        unit = min((from - before * units) / steps, units - 1);
         step = (from - before * units) % steps;
     } else {
         b = blockIdx.x / units;
@@ -179,7 +181,8 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void cached_kernel(CachedArgs a) 
         if (kSplit && unit == units) {
             unit = 0;
             do ++b;
-            while (cached_length(a, b) == 0);
+            while (b < c.n_seqs && cached_length(a, b) == 0);
+            if (b >= c.n_seqs) return;
         }
         const uint32_t length = __builtin_amdgcn_readfirstlane(cached_length(a, b));
         const int64_t steps = ((uint64_t)length + kStep - 1) / kStep;
@@ -408,12 +411,12 @@ __global__ __launch_bounds__(kJoinThreads) void cached_join_kernel(CachedArgs a,
     if (here == 0 || here >= workers) return;
     const int64_t at = here * all / workers;
     int64_t b, before;
-    find_step(a, per_step, units, at, b, before);
-    const int64_t steps = (cached_length(a, b) + (uint64_t)per_step - 1) / per_step;
-    const int64_t unit = (at - before * units) / steps, from = before * units + unit * steps;
+    if (!find_step(a, per_step, units, at, b, before)) return;
+    const int64_t steps = max((int64_t)((cached_length(a, b) + (uint64_t)per_step - 1) / per_step), (int64_t)1);
+    const int64_t unit = min((at - before * units) / steps, units - 1), from = before * units + unit * steps;
     auto worker = [&](int64_t step) { return ((step + 1) * workers - 1) / all; };
     // the first worker's part begins with the unit, the others' inside it
-    const int64_t first = worker(from), last = worker(from + steps - 1);
+    const int64_t first = worker(from), last = min(worker(from + steps - 1), workers - 1);
     if (first + 1 != here) return;
     const int64_t hk = unit / a.head_groups;
     const int h0 = (int)(hk * group + unit % a.head_groups * 16);

@@ -68,7 +68,7 @@ def test_attention_refusals(clib):
     for bad in (dict(n=-1), dict(h=-8), dict(kv=-2), dict(kv=3), dict(kv=0), dict(d=-8), dict(seqs=-1), dict(causal=2), dict(dt=5),
                 dict(qt=63), dict(qh=63), dict(kt=63), dict(kh=63), dict(vt=63), dict(vh=63), dict(ot=63), dict(oh=63),
                 dict(starts=None), dict(scale=0.0), dict(scale=-1.0), dict(scale=nan), dict(scale=inf), dict(scale=1e-60),
-                dict(scale=1e60), dict(q=None), dict(k=None), dict(v=None), dict(o=None)):
+                dict(scale=1e60), dict(scale=1e-38), dict(scale=2e38), dict(q=None), dict(k=None), dict(v=None), dict(o=None)):
         assert attend(clib, **bad) == EINVAL, bad
     wide = dict(qt=2048, qh=256, kt=512, kh=256, vt=512, vh=256, ot=2048, oh=256)
     for bad in (dict(dt=F32), dict(d=136, **wide), dict(d=60), dict(q=ODD), dict(k=ODD), dict(v=ODD), dict(o=ODD), dict(qt=516),
@@ -110,7 +110,7 @@ def cached(lib, q=P, qs=512, qh=64, ck=P, c0=2048, c1=1024, c2=64, cv=P, w0=2048
 def test_cached_refusals(clib):
     nan = float("nan")
     for bad in (dict(n=-1), dict(h=-1), dict(kv=-1), dict(kv=3), dict(d=-1), dict(pages=-1), dict(page=0), dict(most=-1), dict(most=5),
-                dict(dt=9), dict(scale=0.0), dict(scale=nan), dict(qs=63), dict(qh=63), dict(os_=63), dict(oh=63), dict(c0=63),
+                dict(dt=9), dict(scale=0.0), dict(scale=nan), dict(scale=1e-38), dict(scale=2e38), dict(qs=63), dict(qh=63), dict(os_=63), dict(oh=63), dict(c0=63),
                 dict(c1=63), dict(c2=63), dict(w0=63), dict(w1=63), dict(w2=63), dict(q=None), dict(o=None), dict(lengths=None),
                 dict(table=None), dict(ck=None), dict(cv=None)):
         assert cached(clib, **bad) == EINVAL, bad

@@ -204,3 +204,22 @@ def test_another_stream(lib):
     got = layer.attention(q, k, v, stream=side)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+def test_offsets_past_32_bits(lib):
+    """Tokens as far apart as they may be, against the same tokens side by side."""
+    from post_weight_quantization_04_amd import layer
+    n, heads, kv, d, stride = 600, 4, 2, 64, 1 << 22
+    assert n * stride > 1 << 31
+    far = torch.empty(n * stride, dtype=torch.float16, device="cuda").view(n, stride)
+    gen = torch.Generator().manual_seed(2)
+    near, views, at = [], [], 0
+    for h in (heads, kv, kv, heads):
+        t = torch.randn(n, h, d, generator=gen).half().cuda()
+        views.append(far[:, at:at + h * d].view(n, h, d))
+        views[-1].copy_(t)
+        near.append(t)
+        at += h * d
+    starts = torch.tensor([0, 250, n], dtype=torch.int32).cuda()
+    layer.attention(*views[:3], starts, out=views[3])
+    assert torch.equal(views[3], layer.attention(*near[:3], starts))

@@ -194,3 +194,17 @@ def test_unaligned_rows_at_larger_sizes(lib, n, d_out, d):
     got = layer.packed_matmul(w, off, dtype=torch.float32)
     assert torch.equal(got.double().cpu(), x.double() @ dense.T)
     assert torch.equal(got, layer.packed_matmul(w, x.cuda(), dtype=torch.float32))
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_offsets_past_32_bits(lib, shift):
+    """Rows of X and Y as far apart as they may be, against the same rows side by side."""
+    from post_weight_quantization_04_amd import layer
+    n, d, d_out, stride = 1100, 136, 70, 1 << 21
+    assert n * stride > 1 << 31
+    far = torch.empty(n * stride, dtype=torch.float16, device="cuda").view(n, stride)
+    w, x, _ = make(n, d, d_out, 4, 0, torch.float16, whole=True)
+    xv, yv = far[:, shift:shift + d], far[:, 1001:1001 + d_out]
+    xv.copy_(x)
+    layer.packed_matmul(w, xv, out=yv)
+    assert torch.equal(yv, layer.packed_matmul(w, x.cuda()))
