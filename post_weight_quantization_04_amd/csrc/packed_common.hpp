@@ -238,7 +238,9 @@ __device__ __forceinline__ frag_t pm_columns(const PmWords& p, uint32_t element,
 
 __device__ __forceinline__ float activated(float v, int activation) {
     if (activation == 1) return v < 0.0f ? 0.0f : v;  // keeps NaN
-    if (activation == 2) return v / (1.0f + __expf(-v));
+    // (a reciprocal within one unit in the last place: with the division 8192 x 4096 ->
+    // 11008 takes 806 us, with this 730)
+    if (activation == 2) return v * __builtin_amdgcn_rcpf(1.0f + __expf(-v));
     if (activation == 3) return 0.5f * v * (1.0f + erff(v * 0.70710678f));
     return v;
 }
