@@ -58,8 +58,8 @@ __device__ __forceinline__ void pm_finish(const PmArgs& a, const float* sums, in
 // products, 8192 x 4096 -> 11008 took 881 us, 616 of them without the copies.
 //
 // 8192 x 4096 -> 11008, 4 bits: 721 us, 1024 TFLOP/s (730 with SiLU); a dense float16
-// product by the library takes 730.  4.7 VALU instructions an MFMA (conversions 2 to 3,
-// scaling 1) take as many cycles as the MFMA itself (busy in 40%): a tile of more
+// product by the library takes 730.  4.4 VALU instructions an MFMA (conversions 2 to 3,
+// scaling 1) take as many cycles as the MFMA itself (busy in 44%): a tile of more
 // tokens would convert less often but its sums do not fit the registers.
 //
 // A tile that has a CU to itself takes 0.9 us a block whatever its size: each step
