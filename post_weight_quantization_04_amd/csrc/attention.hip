@@ -91,6 +91,7 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
     // separate arrays: the compiler then knows that a read of one does not wait for copies into another
     __shared__ __align__(16) uint8_t lds0[2 * kTile];
     __shared__ __align__(16) uint8_t lds1[2 * kTile];
+    __shared__ int again[kWaves];
     typedef typename Mat<T>::v8 v8;
     typedef typename Mat<T>::v4 v4;
 
@@ -159,9 +160,11 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
 #pragma unroll
     for (int i = 0; i < kDp / 32; ++i) acc[i] = (float16v){};
     float m = kLowest, l = 0.0f, off = 0.0f;
+    bool far = false;  // the row's exponents have passed kFarExponent
 
-    auto compute = [&](const uint8_t* st, int k0, auto masked) {
-        constexpr bool kMasked = decltype(masked)::value;
+    // exact: rows that went far have their maximum taken from the scores themselves
+    auto compute = [&](const uint8_t* st, int k0, auto masked, auto exact) {
+        constexpr bool kMasked = decltype(masked)::value, kExact = decltype(exact)::value;
         float16v s[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -202,10 +205,13 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
             const float keep = exp2_fast((m - top) * a.c2);
             m = top;
             off = exponent_offset(m, a.c2);
+            if (!kExact) far |= fabsf(off) > kFarExponent;
             l *= keep;
 #pragma unroll
             for (int i = 0; i < kDp / 32; ++i) acc[i] *= keep;
         }
+        const float base = kExact && far ? m : 0.0f, rest = kExact && far ? 0.0f : off;
+        auto weight_of = [&](float score) { return exp2_fast(fmaf(kExact ? score - base : score, a.c2, rest)); };
         if (kMasked) {
             // The infinities and NaN of values, times their weights, where the row sees
             // the key.  Below they count as zeros: a weight of zero would make NaN of them.
@@ -214,7 +220,7 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
                 float mine = 0.0f;
 #pragma unroll
                 for (int v = 0; v < 32; ++v) mine = v == at ? s[v / 16][v % 16] : mine;
-                const float weight = exp2_fast(fmaf(__shfl(mine, l32 + key / 4 % 2 * 32, kWave), a.c2, off));
+                const float weight = weight_of(__shfl(mine, l32 + key / 4 % 2 * 32, kWave));
                 const bool seen = k0 + key < limit;
                 const uint8_t* row = st + (kTile + key * 2 * kDp + 8 * kg);
 #pragma unroll
@@ -235,7 +241,7 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
             v8 p;
 #pragma unroll
             for (int v = 0; v < 8; ++v) {
-                const float e = exp2_fast(fmaf(s[j / 2][j % 2 * 8 + v], a.c2, off));
+                const float e = weight_of(s[j / 2][j % 2 * 8 + v]);
                 l += e;
                 p[v] = (T)e;
             }
@@ -258,61 +264,85 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
             }
         }
     };
-    auto step = [&](uint8_t* st, uint8_t* nx, int i, auto masked) {
+    auto step = [&](uint8_t* st, uint8_t* nx, int i, auto masked, auto exact) {
         // this tile has landed for all waves, and all are done with the one before
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if (i + 1 < tiles) copy(nx, i + 1);
-        if (!decltype(masked)::value || i * kTileKeys < wave_last) compute(st, i * kTileKeys, masked);
+        if (!decltype(masked)::value || i * kTileKeys < wave_last) compute(st, i * kTileKeys, masked, exact);
+    };
+    auto finish = [&] {
+        l = add_halves(l);
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        T* out = static_cast<T*>(c.out) + (first + token) * c.ldo[0] + (h0 + head) * c.ldo[1];
+        // A lane holds every other run of four values of its row; the halves of the
+        // wave exchange runs, so that each stores sixteen bytes.
+#pragma unroll
+        for (int i = 0; i < kDp / 32; ++i)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                union {
+                    v4 h;
+                    uint32_t u[2];
+                } x, y;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    x.h[v] = (T)(acc[i][8 * g + v] * inv);
+                    y.h[v] = (T)(acc[i][8 * g + 4 + v] * inv);
+                }
+                union {
+                    uint32_t u[4];
+                    uint4v v;
+                } o;
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const auto sw = __builtin_amdgcn_permlane32_swap(x.u[v], y.u[v], false, false);
+                    o.u[v] = (uint32_t)sw[0];
+                    o.u[2 + v] = (uint32_t)sw[1];
+                }
+                const int d = 32 * i + 16 * g + 8 * kg;
+                if (live && d < c.d) *reinterpret_cast<uint4v*>(out + d) = o.v;
+            }
     };
     // (a loop for each kind of tile: in one loop they would hold their addresses at the same time, and spill)
     int i = 0;
     for (; i + 2 <= full; i += 2) {
-        step(lds0, lds1, i, Plain{});
-        step(lds1, lds0, i + 1, Plain{});
+        step(lds0, lds1, i, Plain{}, Plain{});
+        step(lds1, lds0, i + 1, Plain{}, Plain{});
     }
     if (i < full) {
-        step(lds0, lds1, i, Plain{});
-        if (++i < tiles) step(lds1, lds0, i++, Masked{});
+        step(lds0, lds1, i, Plain{}, Plain{});
+        if (++i < tiles) step(lds1, lds0, i++, Masked{}, Plain{});
     }
     for (; i < tiles; i += 2) {
-        step(lds0, lds1, i, Masked{});
+        step(lds0, lds1, i, Masked{}, Plain{});
         if (i + 1 == tiles) break;
-        step(lds1, lds0, i + 1, Masked{});
+        step(lds1, lds0, i + 1, Masked{}, Plain{});
     }
+    finish();
 
-    l = add_halves(l);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    T* out = static_cast<T*>(c.out) + (first + token) * c.ldo[0] + (h0 + head) * c.ldo[1];
-    // A lane holds every other run of four values of its row; the halves of the
-    // wave exchange runs, so that each stores sixteen bytes.
+    // Rows whose exponents went far (see kFarExponent) are computed once more, with a
+    // subtraction a score that the loops above do without (a subtraction there takes 2 to
+    // 9% of all calls, a branch around it spills).  The workgroup's other rows get the
+    // same bits again.
+    const int mine = __any(far & live);
+    if (lane == 0) again[w] = mine;
+    __syncthreads();
+    int any = 0;
 #pragma unroll
-    for (int i = 0; i < kDp / 32; ++i)
+    for (int i = 0; i < kWaves; ++i) any |= again[i];
+    if (!any) return;
+    m = kLowest, l = 0.0f, off = 0.0f;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            union {
-                v4 h;
-                uint32_t u[2];
-            } x, y;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                x.h[v] = (T)(acc[i][8 * g + v] * inv);
-                y.h[v] = (T)(acc[i][8 * g + 4 + v] * inv);
-            }
-            union {
-                uint32_t u[4];
-                uint4v v;
-            } o;
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const auto sw = __builtin_amdgcn_permlane32_swap(x.u[v], y.u[v], false, false);
-                o.u[v] = (uint32_t)sw[0];
-                o.u[2 + v] = (uint32_t)sw[1];
-            }
-            const int d = 32 * i + 16 * g + 8 * kg;
-            if (live && d < c.d) *reinterpret_cast<uint4v*>(out + d) = o.v;
-        }
+    for (int i = 0; i < kDp / 32; ++i) acc[i] = (float16v){};
+    copy(lds0, 0);
+    for (i = 0; i < tiles; i += 2) {
+        step(lds0, lds1, i, Masked{}, Masked{});
+        if (i + 1 == tiles) break;
+        step(lds1, lds0, i + 1, Masked{}, Masked{});
+    }
+    finish();
 }
 
 template <typename T, int kDp>

@@ -89,4 +89,10 @@ __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_ex
 // -infinity stays one.
 __device__ __forceinline__ float exponent_offset(float m, float c) { return fminf(-m * c, __FLT_MAX__); }
 
+// exponent_offset is rounded: the largest exponent of a row comes out as what that left
+// over in place of zero.  It multiplies all of the row's weights alike and goes out with
+// the division, as long as they stay within their type: up to exponents of 2^12 it is
+// below 2^-12, at 2^33 it is hundreds.
+constexpr float kFarExponent = 0x1p12f;
+
 }  // namespace gptq

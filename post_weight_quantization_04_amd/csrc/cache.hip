@@ -273,7 +273,6 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void cached_kernel(CachedArgs a) 
                 for (int v = 0; v < 4; ++v) top = fmaxf(top, s[t][v]);
             top = fmaxf(top, __shfl_xor(top, 16, kWave));
             top = fmaxf(top, __shfl_xor(top, 32, kWave));
-            const float off = exponent_offset(top, a.c2);
             const float keep = exp2_fast((m - top) * a.c2);
             m = top;
             l *= keep;
@@ -284,7 +283,7 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void cached_kernel(CachedArgs a) 
                 v4 p;
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    const float e = exp2_fast(fmaf(s[t][v], a.c2, off));
+                    const float e = exp2_fast((s[t][v] - top) * a.c2);
                     l += e;
                     p[v] = (T)e;
                 }
