@@ -159,6 +159,7 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
     float16v acc[kDp / 32];
 #pragma unroll
     for (int i = 0; i < kDp / 32; ++i) acc[i] = (float16v){};
+    constexpr float kRaised = raised<T>(kLag);
     float m = kLowest, l = 0.0f, off = 0.0f;
     bool far = false;  // the row's exponents have passed kFarExponent
 
@@ -196,21 +197,21 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void attention_kernel(AttArgs a) 
 #pragma unroll
             for (int v = 0; v < 16; ++v) top = fmaxf(top, s[t][v]);
         top = max_halves(top);
-        // The maximum moves only when the row's weights would pass 2^8, which both
-        // types hold with all of their bits: most tiles leave the sums as they are.
+        // The maximum moves only when the row's weights would pass 2^kLag (raised), which
+        // both types hold with all of their bits: most tiles leave the sums as they are.
         // (Each row by itself: its bits do not depend on its neighbours.)
-        const bool moves = (top - m) * a.c2 > 8.0f;
+        const bool moves = (top - m) * a.c2 > kLag;
         if (__any(moves)) {
             top = moves ? top : m;
             const float keep = exp2_fast((m - top) * a.c2);
             m = top;
-            off = exponent_offset(m, a.c2);
+            off = exponent_offset(m, a.c2) + kRaised;
             if (!kExact) far |= fabsf(off) > kFarExponent;
             l *= keep;
 #pragma unroll
             for (int i = 0; i < kDp / 32; ++i) acc[i] *= keep;
         }
-        const float base = kExact && far ? m : 0.0f, rest = kExact && far ? 0.0f : off;
+        const float base = kExact && far ? m : 0.0f, rest = kExact && far ? kRaised : off;
         auto weight_of = [&](float score) { return exp2_fast(fmaf(kExact ? score - base : score, a.c2, rest)); };
         if (kMasked) {
             // The infinities and NaN of values, times their weights, where the row sees

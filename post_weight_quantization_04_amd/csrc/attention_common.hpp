@@ -95,4 +95,15 @@ __device__ __forceinline__ float exponent_offset(float m, float c) { return fmin
 // below 2^-12, at 2^33 it is hundreds.
 constexpr float kFarExponent = 0x1p12f;
 
+// Weights go into the second product as 16-bit numbers.  float16 has full steps from
+// 2^-14 and nothing below 2^-25, but goes up to 2^15.99: its weights are raised by 2^15,
+// or, beside a maximum that may lag behind by kLag, by as much less; sums and parts
+// with them, so that the division takes it out again.  (Without it a long flat tail 17
+// nats below one key lost up to all of its weight in the product and none in the sum.)
+constexpr float kLag = 4.0f;
+template <typename T>
+__device__ constexpr float raised(float lag) {
+    return __is_same(T, half_t) ? 15.0f - lag : 0.0f;
+}
+
 }  // namespace gptq

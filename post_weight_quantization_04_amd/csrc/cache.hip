@@ -283,7 +283,7 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void cached_kernel(CachedArgs a) 
                 v4 p;
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    const float e = exp2_fast((s[t][v] - top) * a.c2);
+                    const float e = exp2_fast(fmaf(s[t][v] - top, a.c2, raised<T>(0.0f)));
                     l += e;
                     p[v] = (T)e;
                 }

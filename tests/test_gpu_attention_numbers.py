@@ -59,3 +59,55 @@ def test_scores_of_any_size(lib, n, kind, a, b):
         assert bool(((got - want).abs() <= room).all()), (causal, float((got - want).abs().max()))
     got = over_cache(q[-1:], k, v, scale)
     assert bool(((got - mean[-1:]).abs() <= off[-1:]).all()), float((got - mean[-1:]).abs().max())
+
+
+def tail(n, nats, at, kind):
+    """q, k and v of n tokens whose key `at` scores `nats` above all the others (scale 1) and has values of zero beside
+    ones; and that key's weight against another's in 64 bits."""
+    q, k, v = (torch.zeros(n, 1, 64, dtype=kind) for _ in range(3))
+    q[:, 0, 0] = 1.0
+    k[at, 0, 0] = nats
+    v[:] = 1.0
+    v[at] = 0.0
+    return q, k, v, math.exp(-float(k[at, 0, 0]))
+
+
+def tail_mass(seen, with_key, w, kind, least):
+    """(y, bound) of rows that see `seen` keys besides `at`, whether they see that one too (`with_key`).  A weight is
+    rounded to its type (half a step, and never by more than `least` of the largest), like the output; a score's exponent
+    of at most 29 is off by a few 2^-20, and the two sums have `seen` float32 terms each."""
+    y = torch.where(with_key, seen * w / (1.0 + seen * w), torch.ones_like(seen))
+    off = y * (2 * torch.finfo(kind).eps / 2 + 2 * seen * 2.0 ** -24 + 2.0 ** -16)
+    return y, off + torch.where(with_key, seen * least, torch.zeros_like(seen)) + 2.0 ** -25
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("nats", [10.0, 17.0, 17.375, 20.0])
+@pytest.mark.parametrize("at", [0, 9000, 19999])
+def test_a_flat_tail_of_a_prompt(lib, at, nats, kind):
+    """Many keys far below one: each weight is tiny, their sum is not.  (In float16 the largest weight is raised to at
+    least 2^11, where half the smallest step, 2^-25, is 2^-36 of it.)"""
+    kind, n = KINDS[kind], 20000
+    q, k, v, w = tail(n, nats, at, kind)
+    row = torch.arange(n, dtype=torch.float64)
+    least = 2.0 ** -36 if kind == torch.float16 else 0.0
+    with_key = row >= at
+    for causal in (True, False):
+        seen = row + 1 - with_key.double() if causal else torch.full_like(row, n - 1)
+        want, off = tail_mass(seen, with_key if causal else torch.ones_like(with_key), w, kind, least)
+        got = over_prompt(q, k, v, 1.0, causal)[:, 0]
+        far = ((got - want[:, None]).abs() - off[:, None]).amax(1)
+        assert float(far.max()) <= 0, (causal, int(far.argmax()), float(got[far.argmax(), 0]), float(want[far.argmax()]))
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("nats", [10.0, 17.0, 17.375, 20.0])
+@pytest.mark.parametrize("n,at", [(131072, 0), (131072, 131071), (900, 450), (40000, 7)])
+def test_a_flat_tail_of_a_cache(lib, n, at, nats, kind):
+    """The same over the cache, where the largest weight of a part of the tokens is 2^15 (2^-25 is 2^-40 of it)."""
+    kind = KINDS[kind]
+    q, k, v, w = tail(n, nats, at, kind)
+    least = 2.0 ** -40 if kind == torch.float16 else 0.0
+    want, off = tail_mass(torch.tensor([n - 1.0]).double(), torch.tensor([True]), w, kind, least)
+    got = over_cache(q[-1:], k, v, 1.0)[0, 0]
+    assert bool(((got - want).abs() <= off).all()), (float(got[0]), float(want), float(off))
