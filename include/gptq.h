@@ -611,9 +611,11 @@ const char* gptq_packed_matmul_kernel(int64_t d_out, int64_t d_in, int64_t group
  * where j runs over the tokens of i's own sequence, up to i with causal.  What
  * lies outside (later tokens, other sequences) has no influence, infinities and
  * NaN included.  Scores, maxima, sums and outputs are float32; the weights
- * exp(.) go into the second product rounded to the inputs' type, as its
- * matrix instruction takes them, and are summed before that rounding; y is
- * rounded once.
+ * exp(.) go into the second product rounded to the inputs' type (in float16 by
+ * no more than 2^-36 of the largest, however small they are), as its matrix
+ * instruction takes them, and are summed before that rounding; y is rounded
+ * once.  An infinite value that a row sees makes its output infinite, or NaN
+ * where its weight is that small.
  *   q, out    [n_tokens, heads, head_dim], k, v [n_tokens, kv_heads, head_dim]
  *             of dtype (GPTQ_F16 or GPTQ_BF16); each with a stride per token
  *             and one per head, in elements, the last dimension contiguous.
@@ -669,9 +671,10 @@ int gptq_cache_store(const void* k, int64_t k_token, int64_t k_head, const void*
  * behind the length have no influence, infinities and NaN included, and
  * neither have tokens on a page number outside [0, pages): -1 marks a page
  * that was freed.  A sequence without tokens gives zeros.  Numbers as for
- * gptq_attention.  A long sequence is divided among many workgroups, which
- * leave partial results in the workspace; a second kernel joins them in a
- * fixed order.
+ * gptq_attention, but the weights go into the second product in two parts,
+ * within 2^-20 (float16) or 2^-14 (bfloat16) of themselves.  A long sequence is
+ * divided among many workgroups, which leave partial results in the workspace;
+ * a second kernel joins them in a fixed order.
  *   q, out    [n_seqs, heads, head_dim] of dtype, a stride per sequence and one
  *             per head.
  *   table     device [n_seqs, ldt] int32, max_pages columns of it in use.

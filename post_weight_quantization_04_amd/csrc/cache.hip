@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheStoreCall c, int 
 // Bound by HBM for long tables: 131072 tokens of 8 key heads of 128 102 us and 8 for the
 // join (5.3 TB/s over the first), 48 sequences of up to 8192 164 to 174 us and 10 (4.9);
 // 64 x 500 tokens 24.6 (5.3).  Short ones by the chain of lengths, pages, keys, launch:
-// 333 tokens 8.4 us.
+// 333 tokens 8.7 us.
 // ---------------------------------------------------------------------------
 struct CachedArgs {
     CachedAttentionCall c;
@@ -135,6 +135,18 @@ __device__ __forceinline__ void copy_word(const void* p, const void* lds) {
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)lds);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(p) : "memory");
 }
+
+// Weights go into the second product in two parts, so that what their rounding to sixteen
+// bits leaves out counts too: 1.5 2^-21 of each in float16 and 1.5 2^-15 in bfloat16 are lost,
+// and the outputs are as exact as their own rounding (1 x 333 tokens in float16: 2.12e-4 of the
+// norm off 64 bits, 2.57e-4 with one part; 131072 in bfloat16 1.66e-3 and 2.16e-3).
+// HBM hides most of it: 131072 tokens 106.2 -> 107.3 us, 48 sequences 183 as before, but
+// 333 tokens 8.4 -> 8.7 and 900 tokens 13.4 -> 14.3.  (Weights of 32 bits on the float32
+// MFMA: 333 tokens 11.7, 900 tokens 22.4, 48 sequences 204.)
+// The first part is that of a little less than the weight: the second one is then never
+// zero or below, and an infinite value times both remains that infinity.
+template <typename T>
+constexpr float kMost = 1.0f - (__is_same(T, half_t) ? 0x1p-10f : 0x1p-7f);
 
 template <typename T, int kDp, int kWaves, bool kSplit>
 __global__ __launch_bounds__(kWaves* kWave, 2) void cached_kernel(CachedArgs a) {
@@ -280,12 +292,13 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void cached_kernel(CachedArgs a) 
             for (int i = 0; i < kDp / 16; ++i) acc[i] *= keep;
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
-                v4 p;
+                v4 p, rest;
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     const float e = exp2_fast(fmaf(s[t][v] - top, a.c2, raised<T>(0.0f)));
                     l += e;
-                    p[v] = (T)e;
+                    p[v] = (T)(e * kMost<T>);
+                    rest[v] = (T)(e - to_f32(p[v]));
                 }
                 const int r = 16 * t + 4 * kg + l16 / 4;
 #pragma unroll
@@ -293,6 +306,7 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void cached_kernel(CachedArgs a) 
                     const v4 vf = read_turned<T>(st + (w * 2 * kTile + kTile + r * 2 * kDp +
                                                        16 * value_place<kDp>(r, 2 * i + l16 % 4 / 2) + 8 * (l16 % 2)));
                     acc[i] = Mat<T>::mfma16h(vf, p, acc[i]);
+                    acc[i] = Mat<T>::mfma16h(vf, rest, acc[i]);
                 }
             }
         };

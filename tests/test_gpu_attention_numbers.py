@@ -5,6 +5,8 @@ import math
 import pytest
 import torch
 
+import block_ref as ref
+
 pytestmark = pytest.mark.gpu
 KINDS = {"f16": torch.float16, "bf16": torch.bfloat16}
 
@@ -111,3 +113,36 @@ def test_a_flat_tail_of_a_cache(lib, n, at, nats, kind):
     want, off = tail_mass(torch.tensor([n - 1.0]).double(), torch.tensor([True]), w, kind, least)
     got = over_cache(q[-1:], k, v, 1.0)[0, 0]
     assert bool(((got - want).abs() <= off).all()), (float(got[0]), float(want), float(off))
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [2, 20, 333, 1700])
+def test_weights_over_the_cache(lib, n, d, kind):
+    """Over the cache the weights lose no more than 1.5 2^-21 (float16) or 1.5 2^-15 (bfloat16) of themselves on their
+    way into the second product: the output's own rounding is nearly all that is left.  (Low scores, so that their own
+    rounding hides nothing.)"""
+    kind, scale = KINDS[kind], 2.0 ** -7
+    lost = 1.5 * 2.0 ** (-21 if kind == torch.float16 else -15)
+    gen = torch.Generator().manual_seed(n + d)
+    q, k, v = (torch.randn(m, h, d, generator=gen).to(kind) for m, h in ((1, 4), (n, 2), (n, 2)))
+    keep = torch.ones(1, n, dtype=torch.bool)
+    got = over_cache(q, k, v, scale)
+    for h in range(4):
+        part = k[:, h // 2].double(), v[:, h // 2].double()
+        want, off = ref.attend(q[:, h].double(), *part, keep, scale, torch.float32)
+        spread = torch.softmax(q[0, h].double() @ part[0].t() * scale, 0) @ part[1].abs()
+        off = off + lost * spread
+        ref.near(got[:, h], want, off + ref.half_step(kind) * (want.abs() + off) + ref.least(kind), f"head {h}")
+
+
+def test_infinities_over_the_cache(lib):
+    """An infinite value that a row sees is infinite in the output, whatever its weight rounds to."""
+    for kind in KINDS.values():
+        for n in (1, 2, 40, 1100):
+            gen = torch.Generator().manual_seed(n)
+            q, k, v = (torch.randn(m, 2, 64, generator=gen).to(kind) for m in (1, n, n))
+            v[n // 2, 0, 5], v[0, 1, 7] = math.inf, -math.inf
+            got = over_cache(q, k, v, 0.125)
+            assert got[0, 0, 5] == math.inf and got[0, 1, 7] == -math.inf
+            assert int(torch.isfinite(got).sum()) == got.numel() - 2
