@@ -23,7 +23,8 @@ namespace {
 //                 few tokens (16 rows, a round)      32 x 64        64 x 128, one a CU   two   128 x 384
 //   4-bit f16     1.7 + 0.1 (to 4), 0.12 (to 16), 0.2   2.0 + 0.4      2.0 + 0.9   2.0 + 1.4   3.5 + 2.65
 // (of 4-bit codes, the other widths being near).  A kernel whose grid would be too large
-// is left out.
+// is left out, and so are those that a form lacks: 128 x 384 takes aligned rows of x and
+// whole groups, 32 x 64 one of the two.
 PmKernel choose(int64_t M, int64_t nb, int64_t n, bool vec, bool fine, int64_t cus) {
     if (n <= 4) return kPmFew;
     auto rounds = [&](int64_t tokens, int64_t rows, int64_t each) {
@@ -34,7 +35,7 @@ PmKernel choose(int64_t M, int64_t nb, int64_t n, bool vec, bool fine, int64_t c
     };
     const double none = 1e30;
     const double few = n <= 32 * 65535 ? rounds(32, 16, 1) * (1.7 + (n <= 16 ? 0.12 : 0.2) * nb) : none;
-    const double small = fits(32, 64, 1024) ? rounds(32, 64, 1) * (2.0 + 0.4 * nb) : none;
+    const double small = (vec || !fine) && fits(32, 64, 1024) ? rounds(32, 64, 1) * (2.0 + 0.4 * nb) : none;
     const bool one = rounds(64, 128, 1) == 1.0;
     const double mid = one ? 2.0 + 0.9 * nb : rounds(64, 128, 2) * (2.0 + 1.4 * nb);
     const double big = vec && !fine ? rounds(128, 384, 1) * (3.5 + 2.65 * nb) : none;

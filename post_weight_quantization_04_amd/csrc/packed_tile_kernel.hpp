@@ -383,10 +383,13 @@ hipError_t tile_go(PmArgs a, hipStream_t s) {
 
 template <typename T, int kBits>
 hipError_t launch_packed_tile(const PmArgs& a, int kernel, bool fine, hipStream_t s) {
-    if (kernel == kPm32x64)
-        return a.vec ? (fine ? tile_go<T, kBits, true, true, 32, 64, 4, 1, 1, 4>(a, s) : tile_go<T, kBits, false, true, 32, 64, 4, 1, 4, 4>(a, s))
-                     : (fine ? tile_go<T, kBits, true, false, 64, 128, 4, 2, 1, 1>(a, s) : tile_go<T, kBits, false, false, 32, 64, 4, 1, 1, 4>(a, s));
-    if (!a.vec) return fine ? tile_go<T, kBits, true, false, 64, 128, 4, 2, 1, 1>(a, s) : tile_go<T, kBits, false, false, 64, 128, 4, 2, 1, 1>(a, s);
+    // (fine groups of unaligned rows have one tile, and never come with another)
+    if (!a.vec && fine) return tile_go<T, kBits, true, false, 64, 128, 4, 2, 1, 1>(a, s);
+    if (kernel == kPm32x64) {
+        if (!a.vec) return tile_go<T, kBits, false, false, 32, 64, 4, 1, 1, 4>(a, s);
+        return fine ? tile_go<T, kBits, true, true, 32, 64, 4, 1, 1, 4>(a, s) : tile_go<T, kBits, false, true, 32, 64, 4, 1, 4, 4>(a, s);
+    }
+    if (!a.vec) return tile_go<T, kBits, false, false, 64, 128, 4, 2, 1, 1>(a, s);
     if (fine) return tile_go<T, kBits, true, true, 64, 128, 4, 2, 4, 1>(a, s);
     if (kernel == kPm64x128) return tile_go<T, kBits, false, true, 64, 128, 4, 2, 4, 1>(a, s);
     return tile_go<T, kBits, false, true, 128, 384, 8, 1, 1, 1>(a, s);
