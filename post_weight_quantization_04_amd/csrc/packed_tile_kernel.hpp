@@ -28,7 +28,7 @@ __device__ __forceinline__ void pm_finish(const PmArgs& a, const float* sums, in
     // 1363 with bias and GELU 17.2 -> 15.7 us)
     if (c.activation == 3) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = activated(y[k], 3);
+        for (int k = 0; k < 8; ++k) y[k] = gelu(y[k]);
     } else if (c.activation == 2) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) y[k] = activated(y[k], 2);
