@@ -156,12 +156,12 @@ __global__ __launch_bounds__(kWaves* kWave) void packed_few_kernel(PmArgs a) {
         if (t >= c.n || o >= c.M) continue;
         if (a.y32) {
             if (c.bias) y += static_cast<const float*>(c.bias)[o];
-            y = activated(y, c.activation);
+            y = activated(y, c.activation, true);
             if (c.residual) y += static_cast<const float*>(c.residual)[t * c.ldr + o];
             static_cast<float*>(c.y)[t * c.ldy + o] = y;
         } else {
             if (c.bias) y += to_f32(static_cast<const T*>(c.bias)[o]);
-            y = activated(y, c.activation);
+            y = activated(y, c.activation, false);
             if (c.residual) y += to_f32(static_cast<const T*>(c.residual)[t * c.ldr + o]);
             static_cast<T*>(c.y)[t * c.ldy + o] = (T)y;
         }

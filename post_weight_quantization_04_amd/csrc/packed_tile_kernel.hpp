@@ -29,12 +29,15 @@ __device__ __forceinline__ void pm_finish(const PmArgs& a, const float* sums, in
     if (c.activation == 3) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) y[k] = gelu(y[k]);
+    } else if (c.activation == 2 && a.y32) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = silu(y[k], true);
     } else if (c.activation == 2) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = activated(y[k], 2);
+        for (int k = 0; k < 8; ++k) y[k] = silu(y[k], false);
     } else if (c.activation) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = activated(y[k], 1);
+        for (int k = 0; k < 8; ++k) y[k] = activated(y[k], 1, false);
     }
     if (c.residual) {
         if (a.y32) load8<float, false>(e, static_cast<const float*>(c.residual) + t * c.ldr + o, left);

@@ -42,6 +42,17 @@ def test_gelu(lib, x_kind, out_kind, n):
 
 
 @pytest.mark.parametrize("n", [3, 300])
+@pytest.mark.parametrize("x_kind,out_kind", [("f16", "f32"), ("bf16", "f32"), ("f16", "f16"), ("bf16", "bf16")])
+def test_silu(lib, x_kind, out_kind, n):
+    """float32 results: the exponential, an addition and a division, of a unit in the last place each.  Sixteen bits: the
+    exponent of up to 126 rounded to 2^-18, and reciprocal and exponential of a few units: 2^-16."""
+    relative = 2.0 ** -21 if out_kind == "f32" else 2.0 ** -16
+    check(torch.linspace(-87.0, 87.0, 4096), "silu", x_kind, out_kind, n, relative)
+    check(torch.linspace(-9.0, 9.0, 4096), "silu", x_kind, out_kind, n, relative)
+    check(torch.linspace(-1e-3, 1e-3, 4096), "silu", x_kind, out_kind, n, relative)
+
+
+@pytest.mark.parametrize("n", [3, 300])
 @pytest.mark.parametrize("out_kind", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
 def test_ends(lib, act, out_kind, n):
