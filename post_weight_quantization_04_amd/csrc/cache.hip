@@ -60,6 +60,10 @@ struct CachedArgs {
     int64_t workers;   // at most
 };
 
+// Floats of a part: O [rows][dp], then each row's maximum, then its sum, up to a multiple
+// of four, since O is read and written as sixteen bytes.
+__host__ __device__ constexpr int64_t part_floats(int64_t rows, int64_t dp) { return (rows * (dp + 2) + 3) / 4 * 4; }
+
 __device__ const uint32_t kZeroRow[64] = {};  // 256 bytes: what keys that are none are read from
 
 __device__ __forceinline__ uint32_t page_of(const CachedArgs& a, uint32_t pos) {
@@ -381,7 +385,7 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void cached_kernel(CachedArgs a) 
                     *reinterpret_cast<v8*>(static_cast<T*>(c.out) + b * c.ldo[0] + (h0 + r) * c.ldo[1] + e) = out;
                 }
             } else {
-                float* part = a.parts + slot * (a.rows * (kDp + 2));
+                float* part = a.parts + slot * part_floats(a.rows, kDp);
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     *reinterpret_cast<float4v*>(part + (r * kDp + e + 4 * j)) = (float4v){y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]};
@@ -440,7 +444,7 @@ __global__ __launch_bounds__(kJoinThreads) void cached_join_kernel(CachedArgs a,
     if (g < groups) {
 #pragma unroll 2
         for (int64_t w = first + g; w <= last; w += groups) {
-            const float* p = a.parts + (2 * w + (w == first)) * (a.rows * (kDp + 2));
+            const float* p = a.parts + (2 * w + (w == first)) * part_floats(a.rows, kDp);
             const float4v lo = *reinterpret_cast<const float4v*>(p + r * kDp + e), hi = *reinterpret_cast<const float4v*>(p + r * kDp + e + 4);
             const float pt = p[a.rows * kDp + r], ps = p[a.rows * (kDp + 1) + r];
             const float now = fmaxf(top, pt), fa = exp2_fast((top - now) * a.c2), fb = exp2_fast((pt - now) * a.c2);
@@ -530,7 +534,7 @@ hipError_t launch_cache_store(const CacheStoreCall& c, hipStream_t s) {
 size_t cached_attention_workspace_bytes(int64_t n_seqs, int64_t heads, int64_t kv_heads, int64_t d, int64_t max_pages,
                                         int64_t page_size) {
     if (max_pages <= kCachedWhole && max_pages * std::min(page_size, kCachedWhole + 1) <= kCachedWhole) return 0;
-    return (size_t)(2 * kCachedWorkers * unit_rows(heads, kv_heads) * (padded_head(d) + 2)) * sizeof(float);
+    return (size_t)(2 * kCachedWorkers * part_floats(unit_rows(heads, kv_heads), padded_head(d))) * sizeof(float);
 }
 
 hipError_t launch_cached_attention(const CachedAttentionCall& c, int dtype, hipStream_t s) {

@@ -34,3 +34,15 @@ def test_unaligned_rows_in_small_groups(kernel):
     assert kernel(250, 1100, 640, 32, False) == "64 x 128"
     assert kernel(64, 4096, 4096, 32, False) == "few tokens"
     assert kernel(2700, 2801, 192, 48, False) == "64 x 128"
+
+
+def test_parts_of_the_cached_attention_are_aligned():
+    """A part is read and written as sixteen bytes: 1024 of them, each a multiple of that, for any number of query heads
+    that share a key head."""
+    from post_weight_quantization_04_amd import _lib
+    for rows in range(1, 20):
+        for d in (64, 128):
+            need = _lib.cached_attention_workspace(2, 2 * rows, 2, d, 400, 16)
+            held = min(rows, 16)
+            assert need % 1024 == 0 and need // 1024 % 16 == 0, (rows, d)
+            assert 4 * held * (d + 2) <= need // 1024 < 4 * held * (d + 2) + 16, (rows, d)
