@@ -577,7 +577,7 @@ const char* gptq_fp8_gated_kernel(int64_t d_ff, int64_t d_in, int64_t n_tokens, 
  *   residual  [n_tokens, d_out] of y_dtype, row stride ldr, or NULL; it may be
  *             Y itself (same pointer and stride).
  *   Y         [n_tokens, d_out] of y_dtype (x_dtype or GPTQ_F32), row stride
- *             ldy elements.
+ *             ldy elements; it overlaps no other operand, that residual aside.
  *   activation 0: none; 1: max(0, .), a NaN kept; 2: v / (1 + exp(-v)), within
  *             2^-21 of itself for float32 results, 2^-16 before the rounding
  *             to others, zero below -87; 3: v (1 + erf(v / sqrt 2)) / 2, within
@@ -589,7 +589,7 @@ const char* gptq_fp8_gated_kernel(int64_t d_ff, int64_t d_in, int64_t n_tokens, 
  * that run on different kernels, and are the same on one.
  * Errors: GPTQ_EINVAL (negative size, bits outside [2, 8], negative
  * group_size or one not dividing d_in, a stride below its row, unknown dtype
- * or activation, null pointer), GPTQ_EUNSUPPORTED (x_dtype GPTQ_F32, y_dtype
+ * or activation, null pointer, Y the same as X), GPTQ_EUNSUPPORTED (x_dtype GPTQ_F32, y_dtype
  * neither x_dtype nor GPTQ_F32, group_size not a multiple of 16, d_in or ldx
  * above 2^21, d_out or n_tokens above 2^24, more than 2^20 tiles of 256 rows
  * by 256 tokens).

@@ -487,6 +487,7 @@ int gptq_packed_matmul(const uint32_t* packed, int bits, int64_t d_out, int64_t 
     if (d_in > kPackedMaxCols || ldx > kPackedMaxCols || d_out > kPackedMaxRows || n > kPackedMaxRows)
         return GPTQ_EUNSUPPORTED;
     if (((d_out + 255) / 256) * ((n + 255) / 256) > kPackedMaxTiles) return GPTQ_EUNSUPPORTED;
+    if (Y == X && d_in > 0) return GPTQ_EINVAL;  // read by all workgroups while some write
     const PackedProduct c = {packed, scales, zeros, X, bias, residual, Y, d_out, d_in, group_size, n, ldx, ldr, ldy,
                              bits, activation};
     return hip_status(launch_packed_matmul(c, x_dtype, y_dtype, as_stream(stream)));

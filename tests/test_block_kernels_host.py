@@ -46,3 +46,12 @@ def test_parts_of_the_cached_attention_are_aligned():
             held = min(rows, 16)
             assert need % 1024 == 0 and need // 1024 % 16 == 0, (rows, d)
             assert 4 * held * (d + 2) <= need // 1024 < 4 * held * (d + 2) + 16, (rows, d)
+
+
+def test_a_product_onto_its_own_input_is_refused():
+    """Workgroups read all of X while others write Y (made before any HIP call: the pointer is never used)."""
+    import ctypes
+    from post_weight_quantization_04_amd import _lib
+    p, other = ctypes.c_void_p(4096), ctypes.c_void_p(1 << 20)
+    rc = _lib.load().gptq_packed_matmul(other, 4, 256, 256, other, other, 128, p, 0, 4, 256, None, None, 0, p, 0, 256, 0, None)
+    assert rc == 1
