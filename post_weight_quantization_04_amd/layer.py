@@ -126,6 +126,7 @@ def quantize(W, factor: Factor, bits: int, group_size: int, block_size: int, ws:
 def pack(codes, bits: int, stream=None):
     """Few-bit storage of ``codes [d_out, d_in]`` (uint32 words, see
     ``gptq_pack_codes``)."""
+    import torch
     d_out, d_in = codes.shape
     packed = _empty(d_out, max(_lib.packed_words(d_in, bits), 1), torch.int32, codes.device, stream)
     _lib.pack_codes(codes, bits, packed, stream=stream)
