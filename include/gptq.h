@@ -617,7 +617,7 @@ const char* gptq_packed_matmul_kernel(int64_t d_out, int64_t d_in, int64_t group
  * no more than 2^-36 of the largest, however small they are), as its matrix
  * instruction takes them, and are summed before that rounding; y is rounded
  * once.  An infinite value that a row sees makes its output infinite, or NaN
- * where its weight is that small.
+ * where its weight is less than 2^-29 of the largest.
  *   q, out    [n_tokens, heads, head_dim], k, v [n_tokens, kv_heads, head_dim]
  *             of dtype (GPTQ_F16 or GPTQ_BF16); each with a stride per token
  *             and one per head, in elements, the last dimension contiguous.

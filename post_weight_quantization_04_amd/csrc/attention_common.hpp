@@ -91,9 +91,10 @@ __device__ __forceinline__ float exponent_offset(float m, float c) { return fmin
 
 // exponent_offset is rounded: the largest exponent of a row comes out as what that left
 // over in place of zero.  It multiplies all of the row's weights alike and goes out with
-// the division, as long as they stay within their type: up to exponents of 2^12 it is
-// below 2^-12, at 2^33 it is hundreds.
-constexpr float kFarExponent = 0x1p12f;
+// the division, as long as they stay within their type and the row's maximum where it is.
+// Up to exponents of 2^14 it is at most 2^-11, less than a score of that size is rounded
+// by; at 2^33 it is hundreds.
+constexpr float kFarExponent = 0x1p14f;
 
 // Weights go into the second product as 16-bit numbers.  float16 has full steps from
 // 2^-14 and nothing below 2^-25, but goes up to 2^15.99: its weights are raised by 2^15,
