@@ -13,11 +13,13 @@
 // straight to LDS one tile ahead, one barrier a tile; values are read turned.
 //
 // Bound by MFMA and the softmax's arithmetic in turn: 8192 causal tokens, 32 heads of
-// 128 over 8, float16 545 to 570 us (963 to 1008 TFLOP/s), bfloat16 512; MFMA is busy in
-// 50% of the cycles, VALU in 44%, and two waves a SIMD do not lay one over the other.
+// 128 over 8, float16 553 to 590 us by the clocks the card holds (994 to 930 TFLOP/s),
+// bfloat16 521 to 566; MFMA is busy in 49% of the cycles, VALU in 43%, and two waves a SIMD
+// do not lay one over the other.  Heads of 96 take 516 us and of 80 499, as 128 with zeros;
+// of 64 310.
 // Four waves a workgroup: two (keys copied twice as often) and eight (more waiting at
 // the barrier) are slower, and so is one loop for whole and masked tiles, which spills
-// (731 us).  77 tokens 9.0 us: a chain of two tiles of keys, a launch and the stores.
+// (731 us).  77 tokens 9.3 us: a chain of two tiles of keys, a launch and the stores.
 #include "attention_common.hpp"
 #include "kernels.hpp"
 

@@ -45,8 +45,8 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheStoreCall c, int 
 // unit, 2 w + 1 for one that begins with it.  cached_join_kernel adds the parts
 // in order.
 //
-// Bound by HBM for long tables: 131072 tokens of 8 key heads of 128 102 us and 8 for the
-// join (5.3 TB/s over the first), 48 sequences of up to 8192 164 to 174 us and 10 (4.9);
+// Bound by HBM for long tables: 131072 tokens of 8 key heads of 128 103 us and 8 for the
+// join (5.2 TB/s over the first), 48 sequences of up to 8192 172 to 178 us and 10 (4.9);
 // 64 x 500 tokens 24.6 (5.3).  Short ones by the chain of lengths, pages, keys, launch:
 // 333 tokens 8.7 us.
 // ---------------------------------------------------------------------------
@@ -483,7 +483,11 @@ __global__ __launch_bounds__(kJoinThreads) void cached_join_kernel(CachedArgs a,
 }
 
 constexpr int64_t kCachedWorkers = 512;   // at most
-constexpr int64_t kCachedWhole = 1024;    // tokens up to which a unit is one workgroup's
+// Tokens up to which a unit is one workgroup's, without the join's launch: 333 tokens of 8
+// key heads 8.7 us, divided 20.3; 900 tokens 14.3 and 16.7; 1500 tokens 18.7 and 16.6; 4000
+// tokens 40.9 and 18.5.  (By the table, which the host knows, not by the lengths.  Many
+// sequences would gain a little from more: 64 of 2000 tokens 94 us, divided 104.)
+constexpr int64_t kCachedWhole = 1024;
 
 inline int padded_head(int64_t d) { return d <= 64 ? 64 : 128; }
 inline int64_t unit_rows(int64_t heads, int64_t kv_heads) { return std::min(heads / kv_heads, kHeadRows); }
@@ -507,11 +511,11 @@ hipError_t cached_waves(CachedArgs a, int64_t units, int64_t most, int cus, hipS
 }
 
 // Eight waves a workgroup, one a CU, while there is a CU for each unit (333 tokens of 8
-// key heads 8.4 us, 9.3 with four waves; 900 tokens 13.4 and 16.4; 131072 tokens 107 us,
-// 5.0 TB/s, and 108; 16 x 3000 tokens of 16 heads of 64 41 and 50).  Four waves, two
+// key heads 8.7 us, 9.5 with four waves; 900 tokens 14.2 and 17.4; 131072 tokens 108 us,
+// 5.0 TB/s, and 112; 16 x 3000 tokens of 16 heads of 64 42 and 57).  Four waves, two
 // workgroups a CU, for more units, since what a unit's begin and end take then lies beside
-// another's copies (64 x 500 tokens 24.6 us, 28.8 with eight; in longer tables 999 x 50 and
-// one of 7000 137 us and 216, 200 x 500 and one of 7000 104 and 111).
+// another's copies (64 x 500 tokens 24.6 us, 28.9 with eight; in longer tables 999 x 50 and
+// one of 7000 133 us and 216, 200 x 500 and one of 7000 103 and 111).
 template <typename T, int kDp>
 hipError_t cached_go(const CachedArgs& a, hipStream_t s) {
     const CachedAttentionCall& c = a.c;

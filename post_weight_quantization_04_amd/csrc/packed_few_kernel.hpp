@@ -17,9 +17,9 @@ namespace {
 // instruction: 24 tokens of 11008 x 4096 in 23.8 us.)  The waves' sums meet in
 // LDS, added in wave order.
 //
-// One token of 4096 x 4096, 4 bits: 4.7 us, 1.8 TB/s, of which 3 are the launch and
-// the first loads; 1 x 4096 -> 11008 9.4; 24 x 11008 -> 4096 bfloat16 15.3, 1.5 TB/s,
-// bound by the conversions, which every 32 tokens repeat, and their waits.
+// One token of 4096 x 4096, 4 bits: 4.8 us, 1.8 TB/s, of which 3 are the launch and
+// the first loads (bfloat16 5.5); 1 x 4096 -> 11008 9.4; 24 x 11008 -> 4096 13.6, bfloat16
+// 14.9, 1.6 TB/s, bound by the conversions, which every 32 tokens repeat, and their waits.
 // ---------------------------------------------------------------------------
 template <typename T, int kBits, bool kFine, bool kVec, int kWaves, int kQuads>
 __global__ __launch_bounds__(kWaves* kWave) void packed_few_kernel(PmArgs a) {

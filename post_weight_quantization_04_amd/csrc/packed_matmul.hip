@@ -22,9 +22,15 @@ namespace {
 // part of its own and one for a block of 128 columns, in us:
 //                 few tokens (16 rows, a round)      32 x 64        64 x 128, one a CU   two   128 x 384
 //   4-bit f16     1.7 + 0.1 (to 4), 0.12 (to 16), 0.2   2.0 + 0.4      2.0 + 0.9   2.0 + 1.4   3.5 + 2.65
-// (of 4-bit codes, the other widths being near).  A kernel whose grid would be too large
-// is left out, and so are those that a form lacks: 128 x 384 takes aligned rows of x and
-// whole groups, 32 x 64 one of the two.
+// The same figures choose for the other forms, whose kernels change places at much the
+// same sizes: over 4096 -> 4096 and 11008 -> 4096 with 8 to 2048 tokens, fourteen numbers of them,
+// the chosen kernel takes 0.7% more than the fastest in geometric mean for 4-bit float16 in
+// groups of 128, 2% for bfloat16, 1% for 2 and 3 bits, 4% for 8, 1% in groups of 64, 4% of
+// 16, 0 to 1% for unaligned rows.  Furthest off are 33 to 64 tokens of 11008 columns, sent to
+// 32 x 64 (of 8 bits 41 us, 32 with few tokens; in groups of 16 65 and 46), and 65 to 128
+// unaligned ones in small groups, sent to 64 x 128 (62 us, 52 with few tokens).
+// A kernel whose grid would be too large is left out, and so are those that a form lacks:
+// 128 x 384 takes aligned rows of x and whole groups, 32 x 64 one of the two.
 PmKernel choose(int64_t M, int64_t nb, int64_t n, bool vec, bool fine, int64_t cus) {
     if (n <= 4) return kPmFew;
     auto rounds = [&](int64_t tokens, int64_t rows, int64_t each) {

@@ -24,8 +24,9 @@ __device__ __forceinline__ void pm_finish(const PmArgs& a, const float* sums, in
 #pragma unroll
         for (int k = 0; k < 8; ++k) y[k] += e[k];
     }
-    // (one branch for all eight, whose steps then lie beside one another: 777 x 1000 ->
-    // 1363 with bias and GELU 17.2 -> 15.7 us)
+    // (one branch for all eight, whose steps then lie beside one another: a branch each
+    // takes 777 x 1000 -> 1363 with bias and GELU from 12.9 to 15.0 us, 8192 x 4096 ->
+    // 11008 with SiLU from 745 to 803)
     if (c.activation == 3) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) y[k] = gelu(y[k]);
@@ -60,9 +61,10 @@ __device__ __forceinline__ void pm_finish(const PmArgs& a, const float* sums, in
 // with waves two by four over 256 x 192, which copies twice the x for the same
 // products, 8192 x 4096 -> 11008 took 881 us, 616 of them without the copies.
 //
-// 8192 x 4096 -> 11008, 4 bits: 721 us, 1024 TFLOP/s (730 with SiLU); a dense float16
-// product by the library takes 730.  4.4 VALU instructions an MFMA (conversions 2 to 3,
-// scaling 1) take as many cycles as the MFMA itself (busy in 44%): a tile of more
+// 8192 x 4096 -> 11008, 4 bits: 733 us, 1008 TFLOP/s (745 with SiLU; bfloat16, whose
+// conversion goes by way of float32, 812); up to 780 by the clocks the card holds; a dense
+// float16 product by the library takes 714.  4.4 VALU instructions an MFMA (conversions 2
+// to 3, scaling 1) take as many cycles as the MFMA itself (busy in 43%): a tile of more
 // tokens would convert less often but its sums do not fit the registers.
 //
 // A tile that has a CU to itself takes 0.9 us a block whatever its size: each step
