@@ -161,3 +161,35 @@ def test_wide_tables_of_empty_sequences(lib, d):
         layer.cached_attention(q, cache, table, torch.tensor(lengths, dtype=torch.int32, device="cuda"), ws=ws, out=out)
         for b, length in enumerate(lengths):
             assert bool(((out[b] - (1.0 if length > 0 else 0.0)).abs() <= (2.0 ** -10 if length > 0 else 0.0)).all()), (lengths, b)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [40, 64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_far_rows_beside_others(lib, causal, d, kind):
+    """Some rows of packed prompts whose scores are far apart: each takes the value of its best key, and all other rows
+    keep their bits."""
+    from post_weight_quantization_04_amd import layer
+    kind, heads, kv, lengths = KINDS[kind], 6, 2, [100, 37, 0, 300, 1]
+    starts = [sum(lengths[:i]) for i in range(len(lengths) + 1)]
+    n, gen = starts[-1] + 9, torch.Generator().manual_seed(d)
+    q, k, v = (torch.randn(n, h, d, generator=gen).to(kind) for h in (heads, kv, kv))
+    at = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    run = lambda: layer.attention(q.cuda(), k.cuda(), v.cuda(), at, causal=causal, scale=2.0 ** 14).cpu()  # noqa: E731
+    q *= 2.0 ** -14  # scores as usual, whatever the types make of the small numbers
+    clean = run()
+    far = [(5, 1), (99, 0), (120, 3), (137, 5), (300, 2), (436, 4), (437, 0)]
+    for t, h in far:
+        q[t, h] = torch.randn(d, generator=gen).to(kind)
+    got = run()
+    rest = torch.ones(n, heads, dtype=torch.bool)
+    rest[starts[-1]:] = False
+    for t, h in far:
+        rest[t, h] = False
+        a = max(s for s in starts[:-1] if s <= t and t < starts[starts.index(s) + 1 if starts.count(s) == 1 else starts.index(s) + 2])
+        b = t + 1 if causal else min(s for s in starts if s > t)
+        s = k[a:b, h // 3].double() @ q[t, h].double() * 2.0 ** 14
+        best, order = s.argmax(), s.sort(descending=True).values
+        assert b - a == 1 or float(order[0] - order[1]) > 40.0 + d * 2.0 ** -23 * float(s.abs().max())
+        assert torch.equal(got[t, h], v[a + best, h // 3]), (t, h)
+    assert torch.equal(got[rest], clean[rest])
